@@ -73,6 +73,7 @@ typedef enum {
 #define NVFP4_DEV_TIMEOUT 1    /* a pipeline wait exceeded its time budget; y unspecified */
 #define NVFP4_DEV_BAD_EXPERT 2 /* an expert id outside [0, E); those slots are zero */
 #define NVFP4_DEV_INTERNAL 4   /* a launch-plan invariant failed on the device; y unspecified */
+#define NVFP4_DEV_BAD_PAGE 8   /* a cache position, sequence, length or page outside its range */
 
 /*
  * Dense GEMV: y[M, N] = g * W[N, K] . x[M, K]^T (per element as above).
@@ -251,6 +252,138 @@ int64_t nvfp4_sdict_plane_bytes(int N, int K);
  * (NULL dict_out, NULL scales or plane_out for a non-empty tensor, negative size, K % 256 != 0).
  */
 int nvfp4_sdict_encode(const uint8_t* scales, int N, int K, uint8_t* plane_out, uint8_t* dict_out);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * The decode step's operators between the products: norm with the residual's addition, rotary
+ * positions with the append to a paged cache, and attention over that cache. They follow the
+ * conventions above (caller-owned device memory, asynchronous on `stream`, nothing allocated,
+ * argument errors before anything is enqueued, device problems as status bits). Their arguments
+ * come in a struct, which the call reads before it returns. Their launches take part in
+ * programmatic dependent launch (nvfp4_set_pdl) and touch every operand only after the preceding
+ * kernel has completed.
+ *
+ * The cache: k_cache and v_cache are [pages, kv_heads, page_size, head_dim], contiguous inside a
+ * page; page p starts page_stride elements times p after the base (so both may be halves of one
+ * allocation). page_table [seqs, table_stride] int32 names the pages of each sequence in order;
+ * entries past a sequence's length are not read. Values are bf16, or E4M3 codes that stand for
+ * code * scale[kv_head] (k_scale, v_scale [kv_heads] f32; NULL = 1).
+ */
+typedef enum {
+    NVFP4_F32 = 0,
+    NVFP4_BF16 = 1,
+    NVFP4_E4M3 = 2
+} nvfp4_type;
+
+/*
+ * Root-mean-square norm of rows:
+ *     h = x + residual (fp32),  residual_out = h in the residual's type,
+ *     y = h / sqrt(mean(h^2) + eps) * weight                     (fp32, the unrounded h)
+ * y is f32, bf16 or E4M3. E4M3: code = E4M3(y / s) to nearest even with s = max(max|y| / 448, 2^-64)
+ * over the row (group = 0; scales [rows]) or over each `group` columns, a power of two from 16 to
+ * 256 that divides cols (scales [rows, cols / group]); a NaN makes its scale NaN.
+ * residual may be NULL (no addition, residual_out unused). residual_out may be the residual
+ * itself and y may be x where type and row pitch agree. Row pitches ld* are in elements.
+ * 0 <= cols <= 32768. Rows on 16-byte boundaries and cols % 8 == 0 take the vector kernel.
+ */
+typedef struct {
+    const void* x;            /* [rows, cols], x_type */
+    const void* residual;     /* [rows, cols], residual_type, or NULL */
+    const void* weight;       /* [cols], w_type */
+    void* residual_out;       /* [rows, cols], residual_type */
+    void* y;                  /* [rows, cols], y_type */
+    float* scales;            /* E4M3 only */
+    int64_t ldx, ldr, ldro, ldy;
+    int32_t x_type, residual_type, w_type, y_type;
+    int32_t rows, cols, group;
+    float eps;
+} nvfp4_rms_norm_args;
+
+nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
+
+/*
+ * Rotary positions of q and k, then the append of k and v to the cache. Token t stands at position
+ * n = positions[t] of sequence seq_ids[t] (NULL: t / (tokens / seqs)). Per head of q and k:
+ *     u = x, or x / sqrt(mean(x^2) + eps) * norm weight [head_dim] where q_norm / k_norm is given;
+ *     pairs i < rotary_half at (i, i + rotary_half), or (2i, 2i + 1) if interleaved, turn by the angle
+ *     n * inv_freq[i]: (a, b) -> (a c - b s, b c + a s) with c, s = mscale * cos, sin;
+ *     the head's values from 2 * rotary_half on pass through.
+ * q_out [tokens, q_heads, head_dim] bf16 receives q (q = NULL: no queries). k and v go to row
+ * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale), to
+ * nearest even, clamped to +-448. Long-context scalings of the frequencies are the caller's, in
+ * inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
+ * row is zero. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
+ * nothing. Two tokens of one call at the same sequence and position leave either's values.
+ * q, k, v: [tokens, heads, head_dim] with unit stride inside a head and the given strides between
+ * tokens and heads. head_dim <= 1024, 2 * rotary_half <= head_dim, max_pages * page_size <= 2^24.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* positions;
+    const int32_t* seq_ids;
+    const float* inv_freq;
+    const void* q_norm;
+    const void* k_norm;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t k_page_stride, v_page_stride, table_stride;
+    int32_t x_type, norm_type, cache_type;
+    int32_t tokens, seqs, q_heads, kv_heads, head_dim, rotary_half, interleaved;
+    int32_t pages, max_pages, page_size;
+    float mscale, eps;
+} nvfp4_rope_append_args;
+
+nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream);
+
+/*
+ * Attention of each sequence's newest `rows` tokens over its cached keys and values. With n =
+ * lengths[b] (these tokens included), query row r of sequence b stands at position n - rows + r
+ * and sees the keys j <= that position, with window > 0 only the last `window` of them:
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j)
+ * Query head h reads kv head h / (q_heads / kv_heads). q and out are [seqs * rows, q_heads,
+ * head_dim] bf16 (rows of a sequence together; strides as given, out contiguous), lse
+ * [seqs * rows, q_heads] f32 or NULL. A row that sees no key (a position below zero, an empty
+ * sequence), or whose scores are all -inf, gives zeros and lse = -inf. Keys that a row does not
+ * see never reach it, whatever they hold. A length outside [0, max_pages * page_size] or a page
+ * outside [0, pages) sets NVFP4_DEV_BAD_PAGE; the length is clamped, the page's keys are not read.
+ * Scores and sums are fp32; probabilities enter the tensor cores rounded to bf16 (bf16 cache) or
+ * f16 (E4M3 cache).
+ *   workspace: nvfp4_attention_workspace_bytes(...) bytes of device memory, 256-byte aligned. Its
+ *   counters must be zero before its first use and every call leaves them at zero. Calls that
+ *   share a workspace must be ordered.
+ * rows 1..8, head_dim <= 512, max_pages * page_size <= 2^24.
+ */
+typedef struct {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    const int32_t* lengths;
+    void* out;
+    float* lse;
+    void* workspace;
+    int64_t q_token_stride, q_head_stride, k_page_stride, v_page_stride, table_stride;
+    int64_t workspace_bytes;
+    int32_t cache_type;
+    int32_t seqs, rows, q_heads, kv_heads, head_dim;
+    int32_t pages, max_pages, page_size, window;
+    float scale;
+} nvfp4_paged_attention_args;
+
+nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* args, void* stream);
+
+/* Bytes of workspace nvfp4_paged_attention needs on the current device for these sizes (any
+ * lengths); -1 for sizes that the call refuses. */
+int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_heads, int kv_heads, int head_dim);
 
 /* Human-readable name of a status code. The returned string is static. */
 const char* nvfp4_status_string(int status);

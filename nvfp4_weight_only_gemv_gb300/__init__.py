@@ -26,13 +26,16 @@ __all__ = ["gemv", "gemv_gate_up", "gemv_gate_up_swiglu", "ffn_swiglu", "ffn_swi
            "moe_gemv", "gemv_sdict", "moe_gemv_sdict",
            "sdict_plane_bytes", "sdict_encode", "device_status", "set_wait_budget_ns",
            "set_variant", "set_pdl", "fp32_fallbacks", "phase_trace", "describe_plan", "describe_plan_host", "library", "library_path", "NVFP4Error",
-           "OUT_F32", "OUT_BF16", "DEV_TIMEOUT", "DEV_BAD_EXPERT", "DEV_INTERNAL"]
+           "rms_norm", "RMSNormOut", "rope_append", "rope_frequencies", "paged_attention", "attention_workspace",
+           "attention_workspace_bytes", "kv_cache",
+           "OUT_F32", "OUT_BF16", "DEV_TIMEOUT", "DEV_BAD_EXPERT", "DEV_INTERNAL", "DEV_BAD_PAGE"]
 
 OUT_F32 = 0
 OUT_BF16 = 1
 DEV_TIMEOUT = 1
 DEV_BAD_EXPERT = 2
 DEV_INTERNAL = 4
+DEV_BAD_PAGE = 8
 
 _lock = threading.Lock()
 _lib = None
@@ -100,6 +103,12 @@ def _declare(lib):
     lib.nvfp4_sdict_encode.restype = i32
     lib.nvfp4_phase_trace.argtypes = [vp, i32, vp]
     lib.nvfp4_phase_trace.restype = i32
+    for name in ("nvfp4_rms_norm", "nvfp4_rope_append", "nvfp4_paged_attention"):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.c_char_p, vp]  # the argument struct's bytes
+        fn.restype = i32
+    lib.nvfp4_attention_workspace_bytes.argtypes = [i32] * 5
+    lib.nvfp4_attention_workspace_bytes.restype = ctypes.c_int64
     lib.nvfp4_version.argtypes = []
     lib.nvfp4_version.restype = i32
     return lib
@@ -509,3 +518,7 @@ def describe_plan_host(kind: str, M: int, N: int, K: int, T: int = 0, top_k: int
     if n < 0:
         raise ValueError("describe_plan_host: bad arguments")
     return buf.value.decode()
+
+
+from .decode_ops import (RMSNormOut, attention_workspace, attention_workspace_bytes, kv_cache,  # noqa: E402
+                         paged_attention, rms_norm, rope_append, rope_frequencies)

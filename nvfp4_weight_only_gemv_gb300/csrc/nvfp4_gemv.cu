@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "nvfp4_gemv.h"
+#include "ops_common.cuh"
 
 namespace nvfp4 {
 
@@ -4831,6 +4832,25 @@ void* ffn_static_scratch(int dev, cudaStream_t st) {
     return addr[dev];
 }
 
+// ------------------------------------------------------------------ host state shared with the other operators
+
+StatusReader g_status_reader[8];
+int g_status_readers = 0;
+
+bool register_status(StatusReader reader) {
+    if (g_status_readers == 8) std::abort();  // at load time: more translation units than slots
+    g_status_reader[g_status_readers++] = reader;
+    return true;
+}
+
+bool host_pdl_enabled() { return g_pdl; }
+int host_variant() { return g_variant; }
+nvfp4_status host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+int host_sm_count() {
+    const DeviceInfo* d = device_info(nullptr);
+    return d ? d->sm_count : 0;
+}
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
@@ -5065,6 +5085,12 @@ nvfp4_status nvfp4_device_status(int32_t* flags_out, void* stream) {
     const int zero = 0;
     e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e);
+    for (int i = 0; i < g_status_readers; ++i) {
+        int bits = 0;
+        e = g_status_reader[i](&bits);
+        if (e != cudaSuccess) return cuda_fail(e);
+        v |= bits;
+    }
     *flags_out = v;
     return (v & NVFP4_DEV_TIMEOUT) ? NVFP4_ERR_TIMEOUT : NVFP4_OK;
 }
