@@ -33,6 +33,14 @@ struct AttnParams {
     int64_t q_ts, q_hs;
     int seqs, rows, hq, hk, group, D, pages, max_pages, page, window, fp8;
     float scale;
+    // tile kernel
+    int* counters;              // workspace: arrivals per (sequence, kv head), zero between calls
+    float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
+    float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
+    int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
+    int page_tiles, page_shift; // 16-key blocks per page, and its log2 or -1
+    int min_units;              // units of work a CTA takes at least
+    int q_vec;                  // q may be read 8 bytes at a time
 };
 
 __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
@@ -125,12 +133,699 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
     if (p.lse && threadIdx.x == 0) p.lse[t * p.hq + h] = total == 0.0f ? -INFINITY : top + logf(total);
 }
 
+
+// ------------------------------------------------------------------ tile kernel
+//
+// One warp takes 16 keys (or a few times 16: TileShape::kKeys) and up to 8 * NT query rows of one
+// kv head (rows * group of them) at a time, entirely in registers:
+//
+//   S^T [16 keys x 8 rows]   = K [16 x D] . Q^T        mma m16n8k16, A = keys, B = rows
+//   O^T [16 dims x 8 rows]  += V^T [16 x 16 keys] . P^T
+//
+// Keys stand on the tensor core's 16-row side and the few query rows on its 8-column side, so a
+// group of 4 heads wastes half of a column block instead of three quarters of a row block. The
+// order of the head's dimensions inside a product is free, so a lane loads 16 consecutive bytes of
+// a key (K) or of four keys (V) straight from the cache into the operand's registers: neither
+// passes through shared memory. V's pairs of keys are formed by byte permutes (E4M3 codes are
+// widened to f16 behind the permute), P^T by two transposing moves of 8 x 8 halves.
+//
+// The kernel is bound by the cache's bytes. What keeps them coming is loads in flight: K of the
+// next tile is requested as soon as this tile's scores are formed, V as soon as its products are,
+// 8 KB a warp at D = 128.
+//
+// Work is split over the length without the host knowing the lengths: all (sequence, kv head)
+// items lie end to end in units of S tiles (S warps side by side), and every CTA takes an equal
+// run of units. An item inside one CTA is stored at once; the parts of an item that is cut leave
+// (m, l, sum) in the workspace, and the CTA that arrives last joins them in the CTAs' order, so
+// the result does not depend on who was last.
+
+template <int DP, int NT, bool F8>
+struct TileShape {
+    static constexpr int kHalves = F8 ? (DP >= 256 ? 1 : 256 / DP) : (DP >= 128 ? 1 : 128 / DP);  // 16-key blocks
+    static constexpr int kKeys = 16 * kHalves;
+    static constexpr int kES = F8 ? 1 : 2;                 // bytes per value
+    static constexpr int kKC = DP * kES / 64;              // 16-byte chunks of a key row per lane
+    static constexpr int kVW = DP * kES / 32;              // 32-bit words of a key's values per lane
+    static constexpr int kMT = DP / 16;                    // 16-dim blocks of O
+    static constexpr int kKS = DP / 16;                    // 16-dim steps of the scores
+    static constexpr int kWarps = DP >= 256 ? 8 : 4;
+    static constexpr int kCtas = DP >= 256 ? 1 : NT == 1 ? 3 : 2;  // per SM
+    static constexpr bool kQRegs = NT * DP <= 256;
+    static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
+};
+
+__device__ __forceinline__ uint4 ld16(const char* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld8(const char* p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+template <bool F8>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F8)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The joined weight of a part: 1 where only a NaN sum is left (NaN scores leave m at -inf).
+__device__ __forceinline__ float part_weight(float m, float l, float top) {
+    return l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : exp2_fast(m - top);
+}
+
+// What a CTA needs of an item: the sequence's length and the keys that its rows see.
+struct Span {
+    int n, lo, hi_all, lo_all;  // keys [lo, n) for some row, [lo_all, hi_all) for every row
+    int units;
+};
+__device__ __forceinline__ Span span_of(const AttnParams& p, int n, int unit_keys) {
+    Span s;
+    s.n = n;
+    s.hi_all = n - p.rows + 1;
+    const int first = p.window > 0 ? s.hi_all - p.window : 0;
+    s.lo = first > 0 ? first : 0;
+    s.lo_all = p.window > 0 && n > p.window ? n - p.window : 0;
+    const int keys = n - (s.lo & ~15);
+    s.units = keys > 0 ? (keys + unit_keys - 1) / unit_keys : 1;  // an empty item still stores its zeros
+    return s;
+}
+
+template <int DP, int NT, bool F8>
+__global__ void __launch_bounds__(TileShape<DP, NT, F8>::kWarps * 32, TileShape<DP, NT, F8>::kCtas)
+paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
+    using T = TileShape<DP, NT, F8>;
+    constexpr int H = T::kHalves, W = T::kWarps, kThreads = W * 32;
+    constexpr int kRowsW = 8 * NT;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ int64_t s_scan[W];
+    __shared__ int64_t s_before;
+    __shared__ int s_seq, s_last;
+    float* s_o = smem;                                        // [W][kRowsW][kOStride]
+    float2* s_ml = reinterpret_cast<float2*>(s_o + W * kRowsW * T::kOStride);  // [W][kRowsW]
+    uint2* s_q = reinterpret_cast<uint2*>(s_ml + W * kRowsW);  // [row_blocks][NT][kKS][32] (not kQRegs)
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = W / p.row_blocks;
+    const int rows_all = p.rows * p.group, row0 = rb * kRowsW;
+    const int unit_keys = streams * T::kKeys;
+
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // --- the CTA's run of units: prefix sums of the sequences' unit counts
+    const int per = (p.seqs + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.seqs) mine += span_of(p, length_of(p, b), unit_keys).units;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+    for (int i = 0; i < W; ++i) {
+        if (i < warp) before += s_scan[i];
+        total += s_scan[i];
+    }
+    total *= p.hk;
+    const int64_t want = total / p.min_units;
+    const int64_t ctas = want < 1 ? 1 : want < gridDim.x ? want : gridDim.x;
+    if (blockIdx.x >= ctas) return;
+    const int64_t u_begin = total * blockIdx.x / ctas, u_end = total * (blockIdx.x + 1) / ctas;
+    if (u_begin >= before * p.hk && u_begin < (before + mine) * p.hk) {
+        int b = tid * per;
+        for (;; ++b) {
+            const int64_t u = span_of(p, length_of(p, b), unit_keys).units;
+            if (u_begin < (before + u) * p.hk) break;
+            before += u;
+        }
+        s_seq = b;
+        s_before = before;
+    }
+    __syncthreads();
+    int b = s_seq;
+    int64_t item0 = s_before * p.hk;  // first unit of sequence b's first head
+    Span sp = span_of(p, length_of(p, b), unit_keys);
+    int h = static_cast<int>((u_begin - item0) / sp.units);
+    item0 += static_cast<int64_t>(h) * sp.units;
+
+    const char* const cache_k = static_cast<const char*>(p.cache[0]);
+    const char* const cache_v = static_cast<const char*>(p.cache[1]);
+    const int row_bytes = p.D * T::kES;
+
+    for (int64_t u = u_begin; u < u_end;) {
+        const int64_t item_end = item0 + sp.units;
+        const int64_t stop = item_end < u_end ? item_end : u_end;
+        const int u_first = static_cast<int>(u - item0), u_last = static_cast<int>(stop - item0);
+        const int base = sp.lo & ~15;
+        const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
+
+        // --- query rows as the scores' B operand; E4M3 caches: f16, each row times a power of two
+        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kKS : 1];
+        float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + 8 * nt + g;
+            uint2 raw[T::kKS];
+            const int m = row / p.group;
+            const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.rows + m) * p.q_ts +
+                                     static_cast<int64_t>(h * p.group + row - m * p.group) * p.q_hs;
+            const bool live = row < rows_all;
+#pragma unroll
+            for (int ks = 0; ks < T::kKS; ++ks) {
+                const int d = F8 ? 16 * (t + 4 * (ks >> 2)) + 4 * (ks & 3) : 8 * (t + 4 * (ks >> 1)) + 4 * (ks & 1);
+                raw[ks] = make_uint2(0, 0);
+                if (live && d < p.D) {
+                    if (p.q_vec) {
+                        raw[ks] = *reinterpret_cast<const uint2*>(q + d);
+                    } else {
+                        const uint16_t* w = reinterpret_cast<const uint16_t*>(q + d);
+                        raw[ks] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+                    }
+                }
+            }
+            float f = p.scale * 1.4426950408889634f * kscale;
+            if constexpr (F8) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int ks = 0; ks < T::kKS; ++ks)
+                    top = max(max(max(top, raw[ks].x & 0x7fffu), max(raw[ks].x >> 16 & 0x7fffu, raw[ks].y & 0x7fffu)),
+                              raw[ks].y >> 16 & 0x7fffu);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the largest magnitude goes to [2^14, 2^15): every value down to 2^-28 of it is exact
+                // in f16, smaller ones are off by 2^-39 of it at most
+                const int e = static_cast<int>(top >> 7) - 127;
+                const bool plain = top == 0 || top >= 0x7f80u;
+                const int up = plain ? 0 : min(14 - e, 126);
+                const float mul = __int_as_float((127 + up) << 23);
+                f *= __int_as_float((127 - up) << 23);
+#pragma unroll
+                for (int ks = 0; ks < T::kKS; ++ks) {
+                    float v[4] = {bf16_lo(raw[ks].x), bf16_hi(raw[ks].x), bf16_lo(raw[ks].y), bf16_hi(raw[ks].y)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] *= mul;
+                        if (fabsf(v[i]) < INFINITY) v[i] = fminf(fmaxf(v[i], -65504.0f), 65504.0f);
+                    }
+                    raw[ks] = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+                }
+                zf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+                zf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+            } else {
+                zf[nt][0] = zf[nt][1] = f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < T::kKS; ++ks) {
+                if constexpr (T::kQRegs) qf[nt][ks] = raw[ks];
+                else if (stream == 0) s_q[((rb * NT + nt) * T::kKS + ks) * 32 + lane] = raw[ks];
+            }
+        }
+        if constexpr (!T::kQRegs) __syncthreads();
+
+        float o[NT][T::kMT][4], mx[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = mx[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
+        }
+
+        // --- tiles of this warp: stream, stream + streams, ... of the run
+        const int tile_end = u_last * streams;
+        int tile = u_first * streams + stream;
+        uint4 kr[H][2][T::kKC];
+        uint32_t vr[H][4][T::kVW];
+        const char *kp[H], *vp[H];  // the requested tile's blocks
+        int pid[H];                 // page ids of the tile to be requested next
+        int bad = 0, bad_now = 0;   // blocks whose page id is out of range
+
+        auto lookup = [&](int tl) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int key = base + tl * T::kKeys + 16 * i, jb = key >> 4;
+                pid[i] = 0;
+                if (tl < tile_end && key < sp.n)
+                    pid[i] = p.table[b * p.table_stride + (p.page_shift >= 0 ? jb >> p.page_shift : jb / p.page_tiles)];
+            }
+        };
+        auto locate = [&](int tl) {
+            bad = 0;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int key = base + tl * T::kKeys + 16 * i, jb = key >> 4;
+                const int pg = p.page_shift >= 0 ? jb >> p.page_shift : jb / p.page_tiles;
+                const int slot = (jb - pg * p.page_tiles) * 16;
+                int id = pid[i];
+                if (id < 0 || id >= p.pages) {
+                    if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                    id = 0;
+                    bad |= 1 << i;
+                }
+                const int64_t in_page = (static_cast<int64_t>(h) * p.page + slot) * p.D;
+                kp[i] = cache_k + (id * p.page_stride[0] + in_page) * T::kES;
+                vp[i] = cache_v + (id * p.page_stride[1] + in_page) * T::kES;
+            }
+        };
+        // every key of the tile is seen by every row
+        auto whole = [&](int tl) {
+            const int key = base + tl * T::kKeys;
+            return key >= sp.lo_all && key + T::kKeys <= sp.hi_all;
+        };
+        auto seen = [&](int tl, int i, int k) {  // key k of block i is in the sequence's range
+            const int key = base + tl * T::kKeys + 16 * i + k;
+            return key >= sp.lo && key < sp.n && !(bad >> i & 1);
+        };
+        auto request_k = [&](int tl) {
+            const bool all = whole(tl) && bad == 0 && p.D == DP;
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < T::kKC; ++c) {
+                        const int off = 16 * t + 64 * c;
+                        if (all) {
+                            kr[i][r][c] = ld16(kp[i] + (g + 8 * r) * row_bytes + off);
+                        } else {
+                            kr[i][r][c] = make_uint4(0, 0, 0, 0);
+                            if (off < row_bytes && seen(tl, i, g + 8 * r)) kr[i][r][c] = ld16(kp[i] + (g + 8 * r) * row_bytes + off);
+                        }
+                    }
+        };
+        auto request_v = [&](int tl) {
+            const bool all = whole(tl) && bad == 0 && p.D == DP;
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+                    if constexpr (T::kVW == 2) {
+                        const int off = 8 * g;
+                        uint2 v = make_uint2(0, 0);
+                        if (all || (off < row_bytes && seen(tl, i, key))) v = ld8(vp[i] + key * row_bytes + off);
+                        vr[i][k][0] = v.x; vr[i][k][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < T::kVW / 4; ++c) {
+                            const int off = 16 * g + 128 * c;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (all) v = ld16(vp[i] + key * row_bytes + off);
+                            else if (off < row_bytes && seen(tl, i, key)) v = ld16(vp[i] + key * row_bytes + off);
+                            vr[i][k][4 * c] = v.x; vr[i][k][4 * c + 1] = v.y;
+                            vr[i][k][4 * c + 2] = v.z; vr[i][k][4 * c + 3] = v.w;
+                        }
+                    }
+                }
+        };
+
+        if (tile < tile_end) {
+            lookup(tile);
+            locate(tile);
+            request_k(tile);
+            request_v(tile);
+            lookup(tile + streams);
+        }
+        for (; tile < tile_end; tile += streams) {
+            // --- scores
+            float s[H][NT][4];
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < T::kKS; ++ks) {
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (F8) {
+                        const uint4 x = kr[i][0][ks >> 2], y = kr[i][1][ks >> 2];
+                        const uint32_t xw = (ks & 3) == 0 ? x.x : (ks & 3) == 1 ? x.y : (ks & 3) == 2 ? x.z : x.w;
+                        const uint32_t yw = (ks & 3) == 0 ? y.x : (ks & 3) == 1 ? y.y : (ks & 3) == 2 ? y.z : y.w;
+                        a0 = e4m3x2_f16x2(xw); a2 = e4m3x2_f16x2(xw >> 16);
+                        a1 = e4m3x2_f16x2(yw); a3 = e4m3x2_f16x2(yw >> 16);
+                    } else {
+                        const uint4 x = kr[i][0][ks >> 1], y = kr[i][1][ks >> 1];
+                        a0 = ks & 1 ? x.z : x.x; a2 = ks & 1 ? x.w : x.y;
+                        a1 = ks & 1 ? y.z : y.x; a3 = ks & 1 ? y.w : y.y;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 q;
+                        if constexpr (T::kQRegs) q = qf[nt][ks];
+                        else q = s_q[((rb * NT + nt) * T::kKS + ks) * 32 + lane];
+                        mma<F8>(s[i][nt], a0, a1, a2, a3, q.x, q.y);
+                    }
+                }
+            }
+            const bool edge = !whole(tile) || bad != 0;
+            bad_now = bad;
+            const int next = tile + streams;
+            if (next < tile_end) {
+                locate(next);
+                request_k(next);
+            }
+            // --- mask, running maximum, probabilities
+            float top[NT][2];
+            bool moved = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float z = -INFINITY;
+                    int lo = 0, hi = 0;
+                    if (edge) {
+                        const int row = row0 + 8 * nt + 2 * t + c;
+                        hi = row < rows_all ? sp.hi_all + row / p.group : 0;
+                        lo = p.window > 0 ? hi - p.window : 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < H; ++i)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float v = s[i][nt][2 * r + c] * zf[nt][c];
+                            if (edge) {
+                                const int key = base + tile * T::kKeys + 16 * i + 8 * r + g;
+                                if (key < lo || key >= hi || (bad_now >> i & 1)) v = -INFINITY;
+                            }
+                            s[i][nt][2 * r + c] = v;
+                            z = fmaxf(z, v);
+                        }
+                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
+                    top[nt][c] = fmaxf(mx[nt][c], z);
+                    moved |= top[nt][c] != mx[nt][c];
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float keep[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        keep[c] = top[nt][c] == mx[nt][c] ? 1.0f : exp2_fast(mx[nt][c] - top[nt][c]);
+                        mx[nt][c] = top[nt][c];
+                        l[nt][c] *= keep[c];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < T::kMT; ++mt) {
+                        o[nt][mt][0] *= keep[0]; o[nt][mt][2] *= keep[0];
+                        o[nt][mt][1] *= keep[1]; o[nt][mt][3] *= keep[1];
+                    }
+                }
+            }
+            uint32_t pb[H][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0], m1 = mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1];
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    float e[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        e[2 * r] = exp2_fast(s[i][nt][2 * r] - m0);
+                        e[2 * r + 1] = exp2_fast(s[i][nt][2 * r + 1] - m1);
+                        l[nt][0] += e[2 * r];
+                        l[nt][1] += e[2 * r + 1];
+                        pb[i][nt][r] = transpose8x8(F8 ? pack_f16(e[2 * r], e[2 * r + 1]) : pack_bf16(e[2 * r], e[2 * r + 1]));
+                    }
+                }
+            }
+            // --- O^T += V^T P^T. A weight of zero must also silence what is not finite: in tiles that
+            // some row sees only in part, such values are taken row by row of the sequence below.
+            bool special = false;
+            if (edge && (p.rows > 1 || p.window > 0)) {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int w = 0; w < T::kVW; ++w) {
+                            const uint32_t x = vr[i][k][w];
+                            if constexpr (F8) special |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                            else special |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+                        }
+                special = __any_sync(0xffffffffu, special);
+            }
+            auto operands = [&](int i, int mt, const uint32_t (&keep)[4], uint32_t (&a)[4]) {
+                if constexpr (F8) {
+                    const int w = mt >> 1;
+                    const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(vr[i][0][w] & keep[0], vr[i][1][w] & keep[1], sel);
+                    const uint32_t y = __byte_perm(vr[i][2][w] & keep[2], vr[i][3][w] & keep[3], sel);
+                    a[0] = e4m3x2_f16x2(x); a[1] = e4m3x2_f16x2(x >> 16);
+                    a[2] = e4m3x2_f16x2(y); a[3] = e4m3x2_f16x2(y >> 16);
+                } else {
+                    const uint32_t k0 = vr[i][0][mt] & keep[0], k1 = vr[i][1][mt] & keep[1];
+                    const uint32_t k2 = vr[i][2][mt] & keep[2], k3 = vr[i][3][mt] & keep[3];
+                    a[0] = __byte_perm(k0, k1, 0x5410); a[1] = __byte_perm(k0, k1, 0x7632);
+                    a[2] = __byte_perm(k2, k3, 0x5410); a[3] = __byte_perm(k2, k3, 0x7632);
+                }
+            };
+            if (!special) {
+                const uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int mt = 0; mt < T::kMT; ++mt) {
+                        uint32_t a[4];
+                        operands(i, mt, keep, a);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma<F8>(o[nt][mt], a[0], a[1], a[2], a[3], pb[i][nt][0], pb[i][nt][1]);
+                    }
+            } else {
+                for (int m = 0; m < p.rows; ++m) {
+                    const int hi = sp.hi_all + m, lo = p.window > 0 ? hi - p.window : 0;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        uint32_t keep[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = base + tile * T::kKeys + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1);
+                            keep[k] = key >= lo && key < hi ? ~0u : 0u;
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < T::kMT; ++mt) {
+                            uint32_t a[4];
+                            operands(i, mt, keep, a);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma<F8>(d, a[0], a[1], a[2], a[3], pb[i][nt][0], pb[i][nt][1]);
+                                const int row = row0 + 8 * nt + 2 * t;
+                                if (row / p.group == m) { o[nt][mt][0] += d[0]; o[nt][mt][2] += d[2]; }
+                                if ((row + 1) / p.group == m) { o[nt][mt][1] += d[1]; o[nt][mt][3] += d[3]; }
+                            }
+                        }
+                    }
+                }
+            }
+            if (next < tile_end) {
+                request_v(next);
+                lookup(next + streams);
+            }
+        }
+
+        // --- the warps' parts meet in shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v = l[nt][c];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                const int r = 8 * nt + 2 * t + c;
+                if (g == 0) s_ml[warp * kRowsW + r] = make_float2(mx[nt][c], v);
+#pragma unroll
+                for (int x = 0; x < T::kMT / 2; ++x) {
+                    const int d = !F8 ? 64 * (x >> 1) + 8 * g + 4 * (x & 1) : DP == 64 ? 8 * g + 4 * x : 128 * (x >> 2) + 16 * g + 4 * (x & 3);
+                    *reinterpret_cast<float4*>(s_o + (warp * kRowsW + r) * T::kOStride + d) =
+                        make_float4(o[nt][2 * x][c], o[nt][2 * x][2 + c], o[nt][2 * x + 1][c], o[nt][2 * x + 1][2 + c]);
+                }
+            }
+        __syncthreads();
+        const bool direct = u == item0 && stop == item_end;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u == u_begin ? 0 : 1);
+        const int quads = p.D / 4;
+        const float vscale = p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f;
+        auto store = [&](int row, int d, float4 sum, float top, float lsum) {
+            const int m = row / p.group, head = h * p.group + row - m * p.group;
+            const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
+            const float inv = lsum == 0.0f ? 0.0f : vscale / lsum;
+            *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
+                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+            if (d == 0 && p.lse) p.lse[at] = lsum == 0.0f ? -INFINITY : (top + log2f(lsum)) * 0.6931471805599453f;
+        };
+        for (int i = tid; i < rows_all * quads; i += kThreads) {
+            const int row = i / quads, d = 4 * (i - row * quads);
+            const int blk = row / kRowsW, r = row - blk * kRowsW;
+            float m = -INFINITY, lsum = 0.0f;
+            for (int st = 0; st < streams; ++st) m = fmaxf(m, s_ml[(st * p.row_blocks + blk) * kRowsW + r].x);
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int st = 0; st < streams; ++st) {
+                const int w = (st * p.row_blocks + blk) * kRowsW + r;
+                const float2 ml = s_ml[w];
+                const float f = part_weight(ml.x, ml.y, m);
+                if (f == 0.0f) continue;
+                const float4 v = *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d);
+                lsum = fmaf(ml.y, f, lsum);
+                sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+                sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+            }
+            if (direct) {
+                store(row, d, sum, m, lsum);
+            } else {
+                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * rows_all + row) * p.D + d), sum);
+                if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(m, lsum));
+            }
+        }
+        if (!direct) {
+            // --- the last of the item's CTAs joins their parts
+            const int64_t c0 = ((item0 + 1) * ctas - 1) / total, c1 = (item_end * ctas - 1) / total;
+            const int parts = static_cast<int>(c1 - c0 + 1);
+            __threadfence();
+            __syncthreads();
+            int* counter = p.counters + static_cast<int64_t>(b) * p.hk + h;
+            if (tid == 0) {
+                s_last = atomicAdd(counter, 1) == parts - 1;
+                if (s_last) *counter = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // the first CTA's part is its second segment unless its run begins with the item
+                const int64_t first = 2 * c0 + (total * c0 / ctas == item0 ? 0 : 1);
+                for (int i = tid; i < rows_all * quads; i += kThreads) {
+                    const int row = i / quads, d = 4 * (i - row * quads);
+                    float m = -INFINITY, lsum = 0.0f;
+                    for (int c = 0; c < parts; ++c)
+                        m = fmaxf(m, __ldcg(p.part_ml + (c == 0 ? first : 2 * (c0 + c)) * rows_all + row).x);
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int c = 0; c < parts; ++c) {
+                        const int64_t from = (c == 0 ? first : 2 * (c0 + c)) * rows_all + row;
+                        const float2 ml = __ldcg(p.part_ml + from);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * p.D + d));
+                        const float f = part_weight(ml.x, ml.y, m);
+                        if (f != 0.0f) {
+                            lsum = fmaf(ml.y, f, lsum);
+                            sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+                            sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+                        }
+                    }
+                    store(row, d, sum, m, lsum);
+                }
+            }
+        }
+        u = stop;
+        item0 = item_end;
+        if (++h == p.hk) {
+            h = 0;
+            ++b;
+            if (u < u_end) sp = span_of(p, length_of(p, b), unit_keys);
+        }
+        __syncthreads();  // the merge buffer and s_q are free again
+    }
+}
+
 cudaError_t read_status(int* bits) {
     const int zero = 0;
     const cudaError_t e = cudaMemcpyFromSymbol(bits, g_attention_status, sizeof(int));
     return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(int));
 }
 const bool g_registered = register_status(read_status);
+
+
+// The tile kernel's instance for a head size and number of query rows per kv head: the head is
+// padded to 64, 128 or 256 in registers, rows to blocks of 8 NT times the warps that share a tile.
+struct TilePlan {
+    int dp = 0, nt = 1, row_blocks = 1, ctas_per_sm = 1, warps = 4;
+};
+bool plan_tile(int dim, int rows, TilePlan* out) {
+    TilePlan t;
+    if (dim > 256 || rows < 1) return false;
+    t.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+    t.warps = t.dp == 256 ? 8 : 4;
+    t.nt = t.dp == 256 || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    while (t.row_blocks < t.warps && 8 * t.nt * t.row_blocks < rows) t.row_blocks *= 2;
+    if (8 * t.nt * t.row_blocks < rows) return false;
+    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt == 1 ? 3 : 2;
+    *out = t;
+    return true;
+}
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+struct Workspace {
+    int64_t part_o, part_ml, bytes;
+};
+Workspace workspace_of(int grid, int seqs, int rows_all, int kv_heads, int dim) {
+    Workspace w;
+    w.part_o = align256(static_cast<int64_t>(seqs) * kv_heads * 4);
+    w.part_ml = w.part_o + align256(2ll * grid * rows_all * dim * 4);
+    w.bytes = w.part_ml + align256(2ll * grid * rows_all * 8);
+    return w;
+}
+
+int sm_count() {
+    const int n = host_sm_count();
+    return n > 0 ? n : 152;  // sizes asked for without a device: GB300's
+}
+
+template <int DP, int NT, bool F8>
+nvfp4_status launch_tile(const AttnParams& p, int grid, cudaStream_t stream) {
+    using T = TileShape<DP, NT, F8>;
+    const size_t smem = static_cast<size_t>(T::kWarps) * 8 * NT * (T::kOStride * 4 + 8) +
+                        (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kKS * 256);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_attention_tile_kernel<DP, NT, F8>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return host_cuda_fail(e);
+    }
+    return launch(paged_attention_tile_kernel<DP, NT, F8>, dim3(grid), dim3(T::kWarps * 32), smem, stream, p);
+}
+
+template <bool F8>
+nvfp4_status dispatch_tile(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream) {
+    if (t.dp == 256) return launch_tile<256, 1, F8>(p, grid, stream);
+    if (t.dp == 128)
+        return t.nt == 1 ? launch_tile<128, 1, F8>(p, grid, stream) : t.nt == 2 ? launch_tile<128, 2, F8>(p, grid, stream)
+                                                                                : launch_tile<128, 4, F8>(p, grid, stream);
+    return t.nt == 1 ? launch_tile<64, 1, F8>(p, grid, stream) : t.nt == 2 ? launch_tile<64, 2, F8>(p, grid, stream)
+                                                                           : launch_tile<64, 4, F8>(p, grid, stream);
+}
 
 bool sizes_ok(int seqs, int rows, int hq, int hk, int dim) {
     return seqs >= 0 && rows >= 0 && rows <= kMaxRows && hq >= 0 && hk >= 0 && dim >= 0 && (hk == 0 ? hq == 0 : hq % hk == 0);
@@ -142,7 +837,10 @@ bool sizes_ok(int seqs, int rows, int hq, int hk, int dim) {
 extern "C" int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_heads, int kv_heads, int head_dim) {
     using namespace nvfp4;
     if (!sizes_ok(seqs, rows, q_heads, kv_heads, head_dim) || head_dim > kMaxDim) return -1;
-    return 256;
+    TilePlan t;
+    const int rows_all = kv_heads ? rows * (q_heads / kv_heads) : 0;
+    if (!plan_tile(head_dim, rows_all, &t)) return 256;  // one CTA per row and head: nothing to join
+    return workspace_of(t.ctas_per_sm * sm_count(), seqs, rows_all, kv_heads, head_dim).bytes;
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* a, void* stream) {
@@ -173,6 +871,27 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     p.seqs = a->seqs; p.rows = a->rows; p.hq = a->q_heads; p.hk = a->kv_heads; p.group = a->q_heads / a->kv_heads;
     p.D = a->head_dim; p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
     p.window = a->window; p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
+    const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
+    TilePlan t;
+    // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
+    if (host_variant() != 1 && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
+        aligned(p.cache[0], 16) && aligned(p.cache[1], 16) && p.page_stride[0] * es % 16 == 0 && p.page_stride[1] * es % 16 == 0 &&
+        aligned(p.out, 8)) {
+        const int grid = t.ctas_per_sm * sm_count();
+        const Workspace w = workspace_of(grid, p.seqs, rows_all, p.hk, p.D);
+        char* base = static_cast<char*>(a->workspace);
+        p.counters = reinterpret_cast<int*>(base);
+        p.part_o = reinterpret_cast<float*>(base + w.part_o);
+        p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
+        p.row_blocks = t.row_blocks;
+        p.page_tiles = p.page / 16;
+        p.page_shift = -1;
+        for (int s = 0; s < 20; ++s) if (p.page_tiles == 1 << s) p.page_shift = s;
+        p.min_units = 1;
+        p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        return p.fp8 ? dispatch_tile<true>(t, p, grid, st) : dispatch_tile<false>(t, p, grid, st);
+    }
     return launch(paged_attention_scalar_kernel, dim3(a->seqs * a->rows, a->q_heads), dim3(kScalarWarps * 32), 0,
                   static_cast<cudaStream_t>(stream), p);
 }
