@@ -34,7 +34,7 @@ struct AttnParams {
     int seqs, rows, hq, hk, group, D, pages, max_pages, page, window, fp8;
     float scale;
     // tile kernel
-    int* counters;              // workspace: arrivals per (sequence, kv head), zero between calls
+    int* counters;              // workspace: arrivals per (sequence, kv head), then per part; zero between calls
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
@@ -68,6 +68,7 @@ __device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t
 }
 
 constexpr int kScalarWarps = 4;
+constexpr int kJoinOnce = 16;  // parts that one CTA joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
 // any page size, any alignment.
@@ -237,6 +238,135 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int n, int unit_key
     return s;
 }
 
+// The CTA's run of units, and the part of one item in it. Kept in shared memory: the tile loop
+// needs the registers.
+struct Run {
+    int total, ctas, begin, end;    // units: of all items, of this CTA
+    int seq, head;                  // the item
+    int item0, item_end;            // its units
+    int first, last;                // the run's part of it
+    Span span;
+};
+
+__device__ __forceinline__ int run_begin(const Run& r, int64_t cta) {
+    return static_cast<int>(static_cast<int64_t>(r.total) * cta / r.ctas);
+}
+__device__ __forceinline__ int cta_of(const Run& r, int64_t unit) {
+    return static_cast<int>(((unit + 1) * r.ctas - 1) / r.total);
+}
+
+__device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int row, int d, float4 sum, float top, float l) {
+    const int m = row / p.group, head = h * p.group + row - m * p.group;
+    const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
+    const float inv = l == 0.0f ? 0.0f : (p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f) / l;
+    *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
+        make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+    if (d == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+__device__ __forceinline__ void add_part(float4& sum, float& lsum, float2 ml, float4 v, float m) {
+    const float f = part_weight(ml.x, ml.y, m);
+    if (f == 0.0f) return;  // nothing, not even 0 * NaN
+    lsum = fmaf(ml.y, f, lsum);
+    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+}
+
+constexpr int kMaxTileRows = 128;  // query rows per kv head that any tile plan takes
+struct JoinShared {
+    float top[kMaxTileRows], l[kMaxTileRows];
+    int last;
+};
+
+// The parts of an item, as slots of the workspace in the CTAs' order. The first CTA's part is its
+// second segment unless its run begins with the item.
+struct Parts {
+    int64_t slot0;
+    int64_t cta0;
+    __device__ __forceinline__ int64_t slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
+};
+
+// Joins parts first, first + step, ... (`count` of them): into the output, or (to >= 0) into the
+// workspace slot `to`, which may be the first part's own: a value is read and then replaced by one
+// thread, and (m, l) only after all have read them.
+__device__ void join_parts(const AttnParams& p, JoinShared& sh, const Parts& parts, int first, int step, int count,
+                           int64_t to, int b, int h) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int rows_all = p.rows * p.group, quads = p.D / 4;
+    for (int row = warp; row < rows_all; row += warps) {
+        float m = -INFINITY;
+        for (int c = lane; c < count; c += 32)
+            m = fmaxf(m, __ldcg(p.part_ml + parts.slot(first + c * step) * rows_all + row).x);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+        if (lane == 0) sh.top[row] = m;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows_all * quads; i += blockDim.x) {
+        const int row = i / quads, d = 4 * (i - row * quads);
+        const float m = sh.top[row];
+        float lsum = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = 0; c < count; c += 8) {
+            float4 v[8];
+            float2 ml[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t from = parts.slot(first + min(c + j, count - 1) * step) * rows_all + row;
+                ml[j] = __ldcg(p.part_ml + from);
+                v[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * p.D + d));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < count) add_part(sum, lsum, ml[j], v[j], m);
+        }
+        if (to < 0) {
+            store_out(p, b, h, row, d, sum, m, lsum);
+        } else {
+            __stcg(reinterpret_cast<float4*>(p.part_o + (to * rows_all + row) * p.D + d), sum);
+            if (d == 0) sh.l[row] = lsum;
+        }
+    }
+    if (to < 0) return;
+    __syncthreads();
+    for (int row = threadIdx.x; row < rows_all; row += blockDim.x)
+        __stcg(p.part_ml + to * rows_all + row, make_float2(sh.top[row], sh.l[row]));
+}
+
+__device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sh.last = atomicAdd(counter, 1) == of - 1;
+        if (sh.last) *counter = 0;
+    }
+    __syncthreads();
+    if (sh.last) __threadfence();
+    return sh.last != 0;
+}
+
+// Called by every CTA that has left a part of an item in the workspace: the last of them joins the
+// parts. Many parts meet in two steps, first groups of neighbours (by the last of each), then the
+// groups. Out of line, so that its registers are not the tile loop's.
+__device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r) {
+    const int cta0 = cta_of(r, r.item0), parts = cta_of(r, r.item_end - 1) - cta0 + 1;
+    Parts at;
+    at.cta0 = cta0;
+    at.slot0 = 2ll * cta0 + (run_begin(r, cta0) == r.item0 ? 0 : 1);
+    int* const done = p.counters + static_cast<int64_t>(r.seq) * p.hk + r.head;
+    if (parts <= kJoinOnce) {
+        if (arrive_last(sh, done, parts)) join_parts(p, sh, at, 0, 1, parts, -1, r.seq, r.head);
+        return;
+    }
+    int size = kJoinOnce / 2;
+    while (size * size < parts) ++size;
+    const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
+    if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.hk + at.slot(first), count)) return;
+    join_parts(p, sh, at, first, 1, count, at.slot(first), r.seq, r.head);
+    const int groups = (parts + size - 1) / size;
+    if (arrive_last(sh, done, groups)) join_parts(p, sh, at, 0, size, groups, -1, r.seq, r.head);
+}
+
 template <int DP, int NT, bool F8>
 __global__ void __launch_bounds__(TileShape<DP, NT, F8>::kWarps * 32, TileShape<DP, NT, F8>::kCtas)
 paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
@@ -244,9 +374,9 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
     constexpr int H = T::kHalves, W = T::kWarps, kThreads = W * 32;
     constexpr int kRowsW = 8 * NT;
     extern __shared__ __align__(16) float smem[];
-    __shared__ int64_t s_scan[W];
-    __shared__ int64_t s_before;
-    __shared__ int s_seq, s_last;
+    __shared__ int s_scan[W];
+    __shared__ Run s_run;
+    __shared__ JoinShared s_join;
     float* s_o = smem;                                        // [W][kRowsW][kOStride]
     float2* s_ml = reinterpret_cast<float2*>(s_o + W * kRowsW * T::kOStride);  // [W][kRowsW]
     uint2* s_q = reinterpret_cast<uint2*>(s_ml + W * kRowsW);  // [row_blocks][NT][kKS][32] (not kQRegs)
@@ -260,55 +390,62 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
     pdl_wait();
 
     // --- the CTA's run of units: prefix sums of the sequences' unit counts
-    const int per = (p.seqs + kThreads - 1) / kThreads;
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < p.seqs) mine += span_of(p, length_of(p, b), unit_keys).units;
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t total = 0, before = incl - mine;
-    for (int i = 0; i < W; ++i) {
-        if (i < warp) before += s_scan[i];
-        total += s_scan[i];
-    }
-    total *= p.hk;
-    const int64_t want = total / p.min_units;
-    const int64_t ctas = want < 1 ? 1 : want < gridDim.x ? want : gridDim.x;
-    if (blockIdx.x >= ctas) return;
-    const int64_t u_begin = total * blockIdx.x / ctas, u_end = total * (blockIdx.x + 1) / ctas;
-    if (u_begin >= before * p.hk && u_begin < (before + mine) * p.hk) {
-        int b = tid * per;
-        for (;; ++b) {
-            const int64_t u = span_of(p, length_of(p, b), unit_keys).units;
-            if (u_begin < (before + u) * p.hk) break;
-            before += u;
+    {
+        const int per = (p.seqs + kThreads - 1) / kThreads;
+        int mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < p.seqs) mine += span_of(p, length_of(p, b), unit_keys).units;
         }
-        s_seq = b;
-        s_before = before;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int total = 0, before = incl - mine;
+        for (int i = 0; i < W; ++i) {
+            if (i < warp) before += s_scan[i];
+            total += s_scan[i];
+        }
+        total *= p.hk;
+        const int ctas = min(max(total / p.min_units, 1), static_cast<int>(gridDim.x));
+        if (static_cast<int>(blockIdx.x) >= ctas) return;
+        const int begin = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / ctas);
+        before *= p.hk;
+        if (begin >= before && begin < before + mine * p.hk) {
+            int b = tid * per;
+            Span sp;
+            for (;; ++b) {
+                sp = span_of(p, length_of(p, b), unit_keys);
+                if (begin < before + sp.units * p.hk) break;
+                before += sp.units * p.hk;
+            }
+            Run& r = s_run;
+            r.total = total;
+            r.ctas = ctas;
+            r.begin = begin;
+            r.end = run_begin(r, blockIdx.x + 1ll);
+            r.seq = b;
+            r.head = (begin - before) / sp.units;
+            r.item0 = before + r.head * sp.units;
+            r.item_end = r.item0 + sp.units;
+            r.first = begin;
+            r.last = min(r.item_end, r.end);
+            r.span = sp;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    int b = s_seq;
-    int64_t item0 = s_before * p.hk;  // first unit of sequence b's first head
-    Span sp = span_of(p, length_of(p, b), unit_keys);
-    int h = static_cast<int>((u_begin - item0) / sp.units);
-    item0 += static_cast<int64_t>(h) * sp.units;
 
     const char* const cache_k = static_cast<const char*>(p.cache[0]);
     const char* const cache_v = static_cast<const char*>(p.cache[1]);
     const int row_bytes = p.D * T::kES;
 
-    for (int64_t u = u_begin; u < u_end;) {
-        const int64_t item_end = item0 + sp.units;
-        const int64_t stop = item_end < u_end ? item_end : u_end;
-        const int u_first = static_cast<int>(u - item0), u_last = static_cast<int>(stop - item0);
+    for (;;) {
+        const int b = s_run.seq, h = s_run.head;
+        const Span sp = s_run.span;
         const int base = sp.lo & ~15;
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
 
@@ -385,13 +522,13 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         }
 
         // --- tiles of this warp: stream, stream + streams, ... of the run
-        const int tile_end = u_last * streams;
-        int tile = u_first * streams + stream;
+        const int tile_end = (s_run.last - s_run.item0) * streams;
+        int tile = (s_run.first - s_run.item0) * streams + stream;
         uint4 kr[H][2][T::kKC];
         uint32_t vr[H][4][T::kVW];
-        const char *kp[H], *vp[H];  // the requested tile's blocks
-        int pid[H];                 // page ids of the tile to be requested next
-        int bad = 0, bad_now = 0;   // blocks whose page id is out of range
+        int at[H];                 // page ids of the requested tile
+        int pid[H];                // and of the one to be requested next
+        int bad = 0, bad_now = 0;  // blocks whose page id is out of range
 
         auto lookup = [&](int tl) {
 #pragma unroll
@@ -402,23 +539,22 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                     pid[i] = p.table[b * p.table_stride + (p.page_shift >= 0 ? jb >> p.page_shift : jb / p.page_tiles)];
             }
         };
-        auto locate = [&](int tl) {
+        auto locate = [&]() {
             bad = 0;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const int key = base + tl * T::kKeys + 16 * i, jb = key >> 4;
-                const int pg = p.page_shift >= 0 ? jb >> p.page_shift : jb / p.page_tiles;
-                const int slot = (jb - pg * p.page_tiles) * 16;
-                int id = pid[i];
-                if (id < 0 || id >= p.pages) {
+                at[i] = pid[i];
+                if (static_cast<unsigned>(at[i]) >= static_cast<unsigned>(p.pages)) {
                     if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
-                    id = 0;
+                    at[i] = 0;
                     bad |= 1 << i;
                 }
-                const int64_t in_page = (static_cast<int64_t>(h) * p.page + slot) * p.D;
-                kp[i] = cache_k + (id * p.page_stride[0] + in_page) * T::kES;
-                vp[i] = cache_v + (id * p.page_stride[1] + in_page) * T::kES;
             }
+        };
+        auto block_of = [&](int tl, int i, const char* cache, int64_t page_stride) {
+            const int jb = (base + tl * T::kKeys + 16 * i) >> 4;
+            const int slot = p.page_shift >= 0 ? jb & (p.page_tiles - 1) : jb % p.page_tiles;
+            return cache + (at[i] * page_stride + (static_cast<int64_t>(h) * p.page + slot * 16) * p.D) * T::kES;
         };
         // every key of the tile is seen by every row
         auto whole = [&](int tl) {
@@ -432,49 +568,50 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         auto request_k = [&](int tl) {
             const bool all = whole(tl) && bad == 0 && p.D == DP;
 #pragma unroll
-            for (int i = 0; i < H; ++i)
+            for (int i = 0; i < H; ++i) {
+                const char* from = block_of(tl, i, cache_k, p.page_stride[0]) + g * row_bytes + 16 * t;
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int c = 0; c < T::kKC; ++c) {
-                        const int off = 16 * t + 64 * c;
                         if (all) {
-                            kr[i][r][c] = ld16(kp[i] + (g + 8 * r) * row_bytes + off);
+                            kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
                         } else {
                             kr[i][r][c] = make_uint4(0, 0, 0, 0);
-                            if (off < row_bytes && seen(tl, i, g + 8 * r)) kr[i][r][c] = ld16(kp[i] + (g + 8 * r) * row_bytes + off);
+                            if (16 * t + 64 * c < row_bytes && seen(tl, i, g + 8 * r)) kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
                         }
                     }
+            }
         };
         auto request_v = [&](int tl) {
             const bool all = whole(tl) && bad == 0 && p.D == DP;
 #pragma unroll
-            for (int i = 0; i < H; ++i)
+            for (int i = 0; i < H; ++i) {
+                const char* from = block_of(tl, i, cache_v, p.page_stride[1]) + 2 * t * row_bytes + (T::kVW == 2 ? 8 : 16) * g;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+                    const int ahead = (k & 1) + 8 * (k >> 1);  // key 2t + ahead
                     if constexpr (T::kVW == 2) {
-                        const int off = 8 * g;
                         uint2 v = make_uint2(0, 0);
-                        if (all || (off < row_bytes && seen(tl, i, key))) v = ld8(vp[i] + key * row_bytes + off);
+                        if (all || (8 * g < row_bytes && seen(tl, i, 2 * t + ahead))) v = ld8(from + ahead * row_bytes);
                         vr[i][k][0] = v.x; vr[i][k][1] = v.y;
                     } else {
 #pragma unroll
                         for (int c = 0; c < T::kVW / 4; ++c) {
-                            const int off = 16 * g + 128 * c;
                             uint4 v = make_uint4(0, 0, 0, 0);
-                            if (all) v = ld16(vp[i] + key * row_bytes + off);
-                            else if (off < row_bytes && seen(tl, i, key)) v = ld16(vp[i] + key * row_bytes + off);
+                            if (all) v = ld16(from + ahead * row_bytes + 128 * c);
+                            else if (16 * g + 128 * c < row_bytes && seen(tl, i, 2 * t + ahead)) v = ld16(from + ahead * row_bytes + 128 * c);
                             vr[i][k][4 * c] = v.x; vr[i][k][4 * c + 1] = v.y;
                             vr[i][k][4 * c + 2] = v.z; vr[i][k][4 * c + 3] = v.w;
                         }
                     }
                 }
+            }
         };
 
         if (tile < tile_end) {
             lookup(tile);
-            locate(tile);
+            locate();
             request_k(tile);
             request_v(tile);
             lookup(tile + streams);
@@ -513,7 +650,7 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             bad_now = bad;
             const int next = tile + streams;
             if (next < tile_end) {
-                locate(next);
+                locate();
                 request_k(next);
             }
             // --- mask, running maximum, probabilities
@@ -676,87 +813,42 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
         __syncthreads();
-        const bool direct = u == item0 && stop == item_end;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u == u_begin ? 0 : 1);
+        const Run r = s_run;
+        const bool direct = r.first == r.item0 && r.last == r.item_end;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1);
         const int quads = p.D / 4;
-        const float vscale = p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f;
-        auto store = [&](int row, int d, float4 sum, float top, float lsum) {
-            const int m = row / p.group, head = h * p.group + row - m * p.group;
-            const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
-            const float inv = lsum == 0.0f ? 0.0f : vscale / lsum;
-            *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
-                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-            if (d == 0 && p.lse) p.lse[at] = lsum == 0.0f ? -INFINITY : (top + log2f(lsum)) * 0.6931471805599453f;
-        };
         for (int i = tid; i < rows_all * quads; i += kThreads) {
             const int row = i / quads, d = 4 * (i - row * quads);
-            const int blk = row / kRowsW, r = row - blk * kRowsW;
+            const int blk = row / kRowsW, rr = row - blk * kRowsW;
             float m = -INFINITY, lsum = 0.0f;
-            for (int st = 0; st < streams; ++st) m = fmaxf(m, s_ml[(st * p.row_blocks + blk) * kRowsW + r].x);
+            for (int st = 0; st < streams; ++st) m = fmaxf(m, s_ml[(st * p.row_blocks + blk) * kRowsW + rr].x);
             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int st = 0; st < streams; ++st) {
-                const int w = (st * p.row_blocks + blk) * kRowsW + r;
-                const float2 ml = s_ml[w];
-                const float f = part_weight(ml.x, ml.y, m);
-                if (f == 0.0f) continue;
-                const float4 v = *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d);
-                lsum = fmaf(ml.y, f, lsum);
-                sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-                sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+                const int w = (st * p.row_blocks + blk) * kRowsW + rr;
+                add_part(sum, lsum, s_ml[w], *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d), m);
             }
             if (direct) {
-                store(row, d, sum, m, lsum);
+                store_out(p, r.seq, r.head, row, d, sum, m, lsum);
             } else {
                 __stcg(reinterpret_cast<float4*>(p.part_o + (slot * rows_all + row) * p.D + d), sum);
                 if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(m, lsum));
             }
         }
-        if (!direct) {
-            // --- the last of the item's CTAs joins their parts
-            const int64_t c0 = ((item0 + 1) * ctas - 1) / total, c1 = (item_end * ctas - 1) / total;
-            const int parts = static_cast<int>(c1 - c0 + 1);
-            __threadfence();
-            __syncthreads();
-            int* counter = p.counters + static_cast<int64_t>(b) * p.hk + h;
-            if (tid == 0) {
-                s_last = atomicAdd(counter, 1) == parts - 1;
-                if (s_last) *counter = 0;
+        if (!direct) finish_item(p, s_join, s_run);
+        if (r.last == r.end) return;
+        __syncthreads();  // s_run, the merge buffer and s_q are free again
+        if (tid == 0) {
+            Run& n = s_run;
+            if (++n.head == p.hk) {
+                n.head = 0;
+                ++n.seq;
+                n.span = span_of(p, length_of(p, n.seq), unit_keys);
             }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                // the first CTA's part is its second segment unless its run begins with the item
-                const int64_t first = 2 * c0 + (total * c0 / ctas == item0 ? 0 : 1);
-                for (int i = tid; i < rows_all * quads; i += kThreads) {
-                    const int row = i / quads, d = 4 * (i - row * quads);
-                    float m = -INFINITY, lsum = 0.0f;
-                    for (int c = 0; c < parts; ++c)
-                        m = fmaxf(m, __ldcg(p.part_ml + (c == 0 ? first : 2 * (c0 + c)) * rows_all + row).x);
-                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int c = 0; c < parts; ++c) {
-                        const int64_t from = (c == 0 ? first : 2 * (c0 + c)) * rows_all + row;
-                        const float2 ml = __ldcg(p.part_ml + from);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * p.D + d));
-                        const float f = part_weight(ml.x, ml.y, m);
-                        if (f != 0.0f) {
-                            lsum = fmaf(ml.y, f, lsum);
-                            sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-                            sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
-                        }
-                    }
-                    store(row, d, sum, m, lsum);
-                }
-            }
+            n.first = n.item0 = r.item_end;
+            n.item_end = n.item0 + n.span.units;
+            n.last = min(n.item_end, n.end);
         }
-        u = stop;
-        item0 = item_end;
-        if (++h == p.hk) {
-            h = 0;
-            ++b;
-            if (u < u_end) sp = span_of(p, length_of(p, b), unit_keys);
-        }
-        __syncthreads();  // the merge buffer and s_q are free again
+        __syncthreads();
     }
 }
 
@@ -793,7 +885,7 @@ struct Workspace {
 };
 Workspace workspace_of(int grid, int seqs, int rows_all, int kv_heads, int dim) {
     Workspace w;
-    w.part_o = align256(static_cast<int64_t>(seqs) * kv_heads * 4);
+    w.part_o = align256((static_cast<int64_t>(seqs) * kv_heads + 2ll * grid) * 4);
     w.part_ml = w.part_o + align256(2ll * grid * rows_all * dim * 4);
     w.bytes = w.part_ml + align256(2ll * grid * rows_all * 8);
     return w;
@@ -872,9 +964,11 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     p.D = a->head_dim; p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
     p.window = a->window; p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
     const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
+    // units are counted in 31 bits: at least 16 keys each, one at least per sequence and head
+    const int64_t most_units = (static_cast<int64_t>(a->max_pages) * a->page_size / 16 + 2) * a->seqs * a->kv_heads;
     TilePlan t;
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
-    if (host_variant() != 1 && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
+    if (host_variant() != 1 && most_units < (1ll << 31) && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
         aligned(p.cache[0], 16) && aligned(p.cache[1], 16) && p.page_stride[0] * es % 16 == 0 && p.page_stride[1] * es % 16 == 0 &&
         aligned(p.out, 8)) {
         const int grid = t.ctas_per_sm * sm_count();

@@ -37,6 +37,7 @@ struct AppendParams {
     int T, hq, hk, D, half, seqs, per_seq, pages, max_pages, page;
     int norm_type, interleaved, fp8;
     float mscale, eps;
+    int tokens_per_cta, lanes_log2;  // vector kernel
 };
 
 // cos and sin of n * f for a whole n below 2^24. The product is taken exactly as p + e, and whole
@@ -137,6 +138,131 @@ __global__ void __launch_bounds__(128) rope_append_scalar_kernel(const __grid_co
     }
 }
 
+// Vector kernel: a lane holds 8 values of a head as two vectors of 4, chosen so that both members of
+// each rotated pair are its own: in halves, values 4i.. and half + 4i..; interleaved, or beyond the
+// rotary part, 8 neighbours. D / 8 lanes make a head. A CTA takes a few tokens: their cosines and
+// sines are formed once, in shared memory, and serve all heads of q and k.
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t pack4_e4m3(const float (&v)[4]) {
+    return pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16;
+}
+
+template <typename XT>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ AppendParams p) {
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per_cta][half]
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * p.tokens_per_cta;
+    const int tokens = min(p.tokens_per_cta, p.T - t0);
+    const int heads = p.hq + 2 * p.hk, lanes = 1 << p.lanes_log2;
+    const int i = tid & (lanes - 1);        // lane within the head
+    const bool live = 8 * i < p.D;
+    // offsets of the lane's two vectors, and its first rotated pair (-1: none)
+    int oa = 8 * i, ob = 8 * i + 4, pair = -1;
+    if (8 * i < 2 * p.half) {
+        pair = 4 * i;
+        if (!p.interleaved) { oa = 4 * i; ob = p.half + 4 * i; }
+    }
+    for (int j = tid; j < tokens * p.half; j += kThreads) {
+        const int n = p.positions[t0 + j / p.half];
+        float2 v = cos_sin(n < 0 ? 0 : n, p.inv_freq[j % p.half]);
+        cs[j] = make_float2(v.x * p.mscale, v.y * p.mscale);
+    }
+    __syncthreads();
+    const int step = kThreads >> p.lanes_log2;  // heads at a time
+    const int first = blockIdx.y * step + (tid >> p.lanes_log2), stride = gridDim.y * step;
+    // every lane of a warp passes through every turn: the norm's shuffles need them all
+    const int turns = (tokens * heads - blockIdx.y * step + stride - 1) / stride;
+    for (int k = 0, item = first; k < turns; ++k, item += stride) {
+        const bool in = item < tokens * heads && live;
+        const int tk = in ? item / heads : 0;
+        int h = in ? item - tk * heads : 0;
+        const int t = t0 + tk;
+        const int part = h < p.hq ? 0 : h < p.hq + p.hk ? 1 : 2;
+        h -= part == 0 ? 0 : part == 1 ? p.hq : p.hq + p.hk;
+        float a[4] = {}, b[4] = {};
+        if (in) {
+            const XT* x = static_cast<const XT*>(p.x[part]) + t * p.ts[part] + h * p.hs[part];
+            load_vec(x + oa, a);
+            load_vec(x + ob, b);
+        }
+        const void* w = part == 0 ? p.q_norm : part == 1 ? p.k_norm : nullptr;
+        if (p.q_norm || p.k_norm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = fmaf(a[e], a[e], fmaf(b[e], b[e], sum));
+            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (w && in) {
+                const float rstd = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+                float wa[4], wb[4];
+                if (p.norm_type == NVFP4_F32) {
+                    load_vec(static_cast<const float*>(w) + oa, wa);
+                    load_vec(static_cast<const float*>(w) + ob, wb);
+                } else {
+                    load_vec(static_cast<const __nv_bfloat16*>(w) + oa, wa);
+                    load_vec(static_cast<const __nv_bfloat16*>(w) + ob, wb);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { a[e] *= rstd * wa[e]; b[e] *= rstd * wb[e]; }
+            }
+        }
+        if (!in) continue;
+        if (part < 2 && pair >= 0) {
+            float2 r[4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(cs + tk * p.half + pair + e);
+                r[e] = make_float2(v.x, v.y);
+                r[e + 1] = make_float2(v.z, v.w);
+            }
+            if (p.interleaved) {
+                auto turn = [](float& u, float& v, float2 c) {
+                    const float x = u * c.x - v * c.y;
+                    v = v * c.x + u * c.y;
+                    u = x;
+                };
+                turn(a[0], a[1], r[0]); turn(a[2], a[3], r[1]); turn(b[0], b[1], r[2]); turn(b[2], b[3], r[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = a[e] * r[e].x - b[e] * r[e].y;
+                    b[e] = b[e] * r[e].x + a[e] * r[e].y;
+                    a[e] = x;
+                }
+            }
+        }
+        const int n = p.positions[t];
+        if (part == 0) {
+            if (n < 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = b[e] = 0.0f;
+            }
+            __nv_bfloat16* to = p.q_out + (static_cast<int64_t>(t) * p.hq + h) * p.D;
+            store_vec(to + oa, a);
+            store_vec(to + ob, b);
+            continue;
+        }
+        Place at;
+        if (!place_of(p, t, n, at)) continue;
+        const int64_t to = at.page * p.page_stride[part - 1] + (static_cast<int64_t>(h) * p.page + at.slot) * p.D;
+        if (p.fp8) {
+            const float* sc = p.cache_scale[part - 1];
+            const float s = sc ? sc[h] : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { a[e] /= s; b[e] /= s; }
+            uint8_t* c = static_cast<uint8_t*>(p.cache[part - 1]) + to;
+            *reinterpret_cast<uint32_t*>(c + oa) = pack4_e4m3(a);
+            *reinterpret_cast<uint32_t*>(c + ob) = pack4_e4m3(b);
+        } else {
+            __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.cache[part - 1]) + to;
+            store_vec(c + oa, a);
+            store_vec(c + ob, b);
+        }
+    }
+}
+
 cudaError_t read_status(int* bits) {
     const int zero = 0;
     const cudaError_t e = cudaMemcpyFromSymbol(bits, g_append_status, sizeof(int));
@@ -184,6 +310,25 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
     p.norm_type = a->norm_type; p.interleaved = a->interleaved; p.fp8 = a->cache_type == NVFP4_E4M3;
     p.mscale = a->mscale; p.eps = a->eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Vectors of 4 values: 8-byte pieces of bf16, 16-byte pieces of fp32, 4-byte pieces of codes.
+    const int xb = a->x_type == NVFP4_F32 ? 16 : 8, nb = p.norm_type == NVFP4_F32 ? 16 : 8;
+    const int cb = p.fp8 ? 4 : 8;
+    bool vec = p.D % 8 == 0 && p.D <= 256 && p.half % 4 == 0 && aligned(p.q_out, 8) && aligned(p.q_norm, nb) &&
+               aligned(p.k_norm, nb);
+    for (int i = 0; i < 3; ++i) vec = vec && aligned(p.x[i], xb) && p.ts[i] % 4 == 0 && p.hs[i] % 4 == 0;
+    for (int i = 0; i < 2; ++i) vec = vec && aligned(p.cache[i], cb) && p.page_stride[i] % 4 == 0;
+    if (vec && host_variant() != 1) {
+        while ((8 << p.lanes_log2) < p.D) ++p.lanes_log2;
+        const int step = kThreads >> p.lanes_log2, heads = p.hq + 2 * p.hk, sms = host_sm_count();
+        // Few tokens: one a CTA, its heads over several CTAs. Many: 4 a CTA share one barrier.
+        p.tokens_per_cta = p.T >= 8 * sms ? 4 : 1;
+        const int groups = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+        int parts = p.T >= 2 * sms ? 1 : (heads + step - 1) / step;
+        const dim3 grid(groups, parts);
+        const size_t smem = static_cast<size_t>(p.tokens_per_cta) * p.half * sizeof(float2);
+        return a->x_type == NVFP4_F32 ? launch(rope_append_kernel<float>, grid, dim3(kThreads), smem, st, p)
+                                      : launch(rope_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), smem, st, p);
+    }
     const dim3 grid(p.T, p.hq + 2 * p.hk);
     return a->x_type == NVFP4_F32 ? launch(rope_append_scalar_kernel<float>, grid, dim3(128), p.D * 4, st, p)
                                   : launch(rope_append_scalar_kernel<__nv_bfloat16>, grid, dim3(128), p.D * 4, st, p);
