@@ -38,7 +38,9 @@ struct AttnParams {
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
-    int page_tiles, page_shift; // 16-key blocks per page, and its log2 or -1
+    int page_tiles;             // 16-key blocks per page
+    uint32_t page_step[2];      // page strides in 16-byte pieces
+    int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
     int min_units;              // units of work a CTA takes at least
     int q_vec;                  // q may be read 8 bytes at a time
 };
@@ -68,6 +70,7 @@ __device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t
 }
 
 constexpr int kScalarWarps = 4;
+constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
 constexpr int kJoinOnce = 16;  // parts that one CTA joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
@@ -150,6 +153,16 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 // passes through shared memory. V's pairs of keys are formed by byte permutes (E4M3 codes are
 // widened to f16 behind the permute), P^T by two transposing moves of 8 x 8 halves.
 //
+// E4M3 keys and values are widened to f16 in registers (exact; mma.sync on E4M3 operands is no
+// instruction here but is built from the same conversions and f16 products: it executed 11 % more
+// instructions). A query row next to them is f16 too, times a power of two that brings its largest
+// magnitude to [2^14, 2^15): exact down to 2^-28 of that, off by 2^-39 of it below.
+//
+// Probabilities are exp2(s - m) for a reference m that follows the running maximum only when a score
+// passes it by more than 2^8: the rescaling of O, and the maximum over the lanes, are then rare.
+// They enter the products rounded, to bf16 next to bf16 values and to f16 next to E4M3 ones (at most
+// 2^8, far inside f16's range); the sum of exponentials is taken before the rounding.
+//
 // The kernel is bound by the cache's bytes. What keeps them coming is loads in flight: K of the
 // next tile is requested as soon as this tile's scores are formed, V as soon as its products are,
 // 8 KB a warp at D = 128.
@@ -162,15 +175,17 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 
 template <int DP, int NT, bool F8>
 struct TileShape {
-    static constexpr int kHalves = F8 ? (DP >= 256 ? 1 : 256 / DP) : (DP >= 128 ? 1 : 128 / DP);  // 16-key blocks
+    // 16-key blocks of a tile: 64 registers of keys and values, 32 where many rows need theirs
+    static constexpr int kFull = F8 ? 256 / DP : 128 / DP, kFit = F8 && NT * DP > 64 && NT > 1 && (NT == 4 || DP == 64) ? kFull / 2 : kFull;
+    static constexpr int kHalves = kFit < 1 ? 1 : kFit;
     static constexpr int kKeys = 16 * kHalves;
     static constexpr int kES = F8 ? 1 : 2;                 // bytes per value
     static constexpr int kKC = DP * kES / 64;              // 16-byte chunks of a key row per lane
     static constexpr int kVW = DP * kES / 32;              // 32-bit words of a key's values per lane
     static constexpr int kMT = DP / 16;                    // 16-dim blocks of O
-    static constexpr int kKS = DP / 16;                    // 16-dim steps of the scores
+    static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
-    static constexpr int kCtas = DP >= 256 ? 1 : NT == 1 ? 3 : 2;  // per SM
+    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? 3 : 2;  // per SM
     static constexpr bool kQRegs = NT * DP <= 256;
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
 };
@@ -185,6 +200,12 @@ __device__ __forceinline__ uint2 ld8(const char* p) {
     uint2 v;
     asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
+}
+
+template <int WORDS>
+__device__ __forceinline__ auto ld_piece(const char* p) {
+    if constexpr (WORDS == 2) return ld8(p);
+    else return ld16(p);
 }
 
 template <bool F8>
@@ -208,6 +229,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+__device__ __forceinline__ float2 f16x2_f32(uint32_t v) {
+    return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(v & 0xffffu))),
+                       __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16))));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -241,96 +267,94 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int n, int unit_key
 // The CTA's run of units, and the part of one item in it. Kept in shared memory: the tile loop
 // needs the registers.
 struct Run {
-    int total, ctas, begin, end;    // units: of all items, of this CTA
+    int share, extra;               // units per CTA; the first `extra` CTAs take one more
+    int begin, end;                 // this CTA's units
     int seq, head;                  // the item
     int item0, item_end;            // its units
     int first, last;                // the run's part of it
     Span span;
 };
 
-__device__ __forceinline__ int run_begin(const Run& r, int64_t cta) {
-    return static_cast<int>(static_cast<int64_t>(r.total) * cta / r.ctas);
-}
-__device__ __forceinline__ int cta_of(const Run& r, int64_t unit) {
-    return static_cast<int>(((unit + 1) * r.ctas - 1) / r.total);
+__device__ __forceinline__ int run_begin(int share, int extra, int cta) { return share * cta + min(cta, extra); }
+__device__ __forceinline__ int cta_of(const Run& r, int unit) {
+    const int long_units = r.extra * (r.share + 1);
+    return unit < long_units ? unit / (r.share + 1) : r.extra + (unit - long_units) / r.share;
 }
 
-__device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int row, int d, float4 sum, float top, float l) {
+// Four values of a row gathered from parts, one part after the other.
+struct Gathered {
+    float m = -INFINITY, l = 0.0f;
+    float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ void add(float2 ml, float4 v) {
+        const float top = fmaxf(m, ml.x);
+        const float keep = top == m ? 1.0f : exp2_fast(m - top), f = part_weight(ml.x, ml.y, top);
+        m = top;
+        l *= keep;
+        o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+        if (f == 0.0f) return;  // nothing, not even 0 * NaN
+        l = fmaf(ml.y, f, l);
+        o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+    }
+};
+
+__device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int row, int d, const Gathered& a) {
     const int m = row / p.group, head = h * p.group + row - m * p.group;
     const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
-    const float inv = l == 0.0f ? 0.0f : (p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f) / l;
+    const float inv = a.l == 0.0f ? 0.0f : (p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f) / a.l;
     *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
-        make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-    if (d == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
-}
-
-__device__ __forceinline__ void add_part(float4& sum, float& lsum, float2 ml, float4 v, float m) {
-    const float f = part_weight(ml.x, ml.y, m);
-    if (f == 0.0f) return;  // nothing, not even 0 * NaN
-    lsum = fmaf(ml.y, f, lsum);
-    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+        make_uint2(pack_bf16(a.o.x * inv, a.o.y * inv), pack_bf16(a.o.z * inv, a.o.w * inv));
+    if (d == 0 && p.lse) p.lse[at] = a.l == 0.0f ? -INFINITY : (a.m + log2f(a.l)) * 0.6931471805599453f;
 }
 
 constexpr int kMaxTileRows = 128;  // query rows per kv head that any tile plan takes
 struct JoinShared {
-    float top[kMaxTileRows], l[kMaxTileRows];
+    float2 ml[kMaxTileRows];
     int last;
 };
 
 // The parts of an item, as slots of the workspace in the CTAs' order. The first CTA's part is its
 // second segment unless its run begins with the item.
 struct Parts {
-    int64_t slot0;
-    int64_t cta0;
-    __device__ __forceinline__ int64_t slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
+    int slot0, cta0;
+    __device__ __forceinline__ int slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
 };
 
 // Joins parts first, first + step, ... (`count` of them): into the output, or (to >= 0) into the
 // workspace slot `to`, which may be the first part's own: a value is read and then replaced by one
 // thread, and (m, l) only after all have read them.
-__device__ void join_parts(const AttnParams& p, JoinShared& sh, const Parts& parts, int first, int step, int count,
-                           int64_t to, int b, int h) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int rows_all = p.rows * p.group, quads = p.D / 4;
-    for (int row = warp; row < rows_all; row += warps) {
-        float m = -INFINITY;
-        for (int c = lane; c < count; c += 32)
-            m = fmaxf(m, __ldcg(p.part_ml + parts.slot(first + c * step) * rows_all + row).x);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-        if (lane == 0) sh.top[row] = m;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows_all * quads; i += blockDim.x) {
-        const int row = i / quads, d = 4 * (i - row * quads);
-        const float m = sh.top[row];
-        float lsum = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+__device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, const Parts& parts, int first, int step,
+                                           int count, int to, int b, int h) {
+    const int rows_all = p.rows * p.group, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
+#pragma unroll 1
+    for (int row = threadIdx.x >> p.quad_log2; row < rows_all; row += blockDim.x >> p.quad_log2) {
+        if (d >= p.D) continue;
+        float* const po = p.part_o + row * p.D + d;
+        Gathered a;
+#pragma unroll 1
         for (int c = 0; c < count; c += 8) {
             float4 v[8];
             float2 ml[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int64_t from = parts.slot(first + min(c + j, count - 1) * step) * rows_all + row;
-                ml[j] = __ldcg(p.part_ml + from);
-                v[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * p.D + d));
+                const int from = parts.slot(first + min(c + j, count - 1) * step) * rows_all;
+                ml[j] = __ldcg(p.part_ml + from + row);
+                v[j] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(from) * p.D));
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (c + j < count) add_part(sum, lsum, ml[j], v[j], m);
+                if (c + j < count) a.add(ml[j], v[j]);
         }
         if (to < 0) {
-            store_out(p, b, h, row, d, sum, m, lsum);
+            store_out(p, b, h, row, d, a);
         } else {
-            __stcg(reinterpret_cast<float4*>(p.part_o + (to * rows_all + row) * p.D + d), sum);
-            if (d == 0) sh.l[row] = lsum;
+            __stcg(reinterpret_cast<float4*>(po + static_cast<int64_t>(to) * rows_all * p.D), a.o);
+            if (d == 0) sh.ml[row] = make_float2(a.m, a.l);
         }
     }
     if (to < 0) return;
     __syncthreads();
-    for (int row = threadIdx.x; row < rows_all; row += blockDim.x)
-        __stcg(p.part_ml + to * rows_all + row, make_float2(sh.top[row], sh.l[row]));
+    for (int row = threadIdx.x; row < rows_all; row += blockDim.x) __stcg(p.part_ml + to * rows_all + row, sh.ml[row]);
 }
 
 __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of) {
@@ -352,7 +376,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
     const int cta0 = cta_of(r, r.item0), parts = cta_of(r, r.item_end - 1) - cta0 + 1;
     Parts at;
     at.cta0 = cta0;
-    at.slot0 = 2ll * cta0 + (run_begin(r, cta0) == r.item0 ? 0 : 1);
+    at.slot0 = 2 * cta0 + (run_begin(r.share, r.extra, cta0) == r.item0 ? 0 : 1);
     int* const done = p.counters + static_cast<int64_t>(r.seq) * p.hk + r.head;
     if (parts <= kJoinOnce) {
         if (arrive_last(sh, done, parts)) join_parts(p, sh, at, 0, 1, parts, -1, r.seq, r.head);
@@ -413,7 +437,8 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         total *= p.hk;
         const int ctas = min(max(total / p.min_units, 1), static_cast<int>(gridDim.x));
         if (static_cast<int>(blockIdx.x) >= ctas) return;
-        const int begin = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / ctas);
+        const int share = total / ctas, extra = total - share * ctas;
+        const int begin = run_begin(share, extra, blockIdx.x);
         before *= p.hk;
         if (begin >= before && begin < before + mine * p.hk) {
             int b = tid * per;
@@ -424,10 +449,10 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                 before += sp.units * p.hk;
             }
             Run& r = s_run;
-            r.total = total;
-            r.ctas = ctas;
+            r.share = share;
+            r.extra = extra;
             r.begin = begin;
-            r.end = run_begin(r, blockIdx.x + 1ll);
+            r.end = run_begin(share, extra, blockIdx.x + 1);
             r.seq = b;
             r.head = (begin - before) / sp.units;
             r.item0 = before + r.head * sp.units;
@@ -442,74 +467,194 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
     const char* const cache_k = static_cast<const char*>(p.cache[0]);
     const char* const cache_v = static_cast<const char*>(p.cache[1]);
     const int row_bytes = p.D * T::kES;
+    constexpr int kRow = DP * T::kES;  // the same where the head is not padded
 
     for (;;) {
         const int b = s_run.seq, h = s_run.head;
         const Span sp = s_run.span;
         const int base = sp.lo & ~15;
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
+        const int32_t* const pages = p.table + b * p.table_stride;
+        const uint32_t head_at = static_cast<uint32_t>(h * p.page * row_bytes);
 
-        // --- query rows as the scores' B operand; E4M3 caches: f16, each row times a power of two
-        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kKS : 1];
+        // --- tiles of this warp: stream, stream + streams, ... of the run. A tile's first 16-key block
+        // stands at block `slot` of the sequence's page `page`; both walk along with the tiles.
+        const int tile_end = (s_run.last - s_run.item0) * streams;
+        int tile = (s_run.first - s_run.item0) * streams + stream;
+        const int step_page = streams * H / p.page_tiles, step_slot = streams * H % p.page_tiles;
+        int next_page = ((base >> 4) + tile * H) / p.page_tiles, next_slot = ((base >> 4) + tile * H) % p.page_tiles;
+        uint4 kr[H][2][T::kKC];
+        uint32_t vr[H][4][T::kVW];
+        int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
+        uint32_t at[H], next_at[H];     // where the block starts in its page, bytes
+        int bad = 0;                    // blocks of the requested tile whose page id is out of range
+
+        // looks up the tile after the requested one
+        auto look_up = [&](int tl) {
+            int pg = next_page, sl = next_slot;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                next_id[i] = 0;
+                if (tl < tile_end && base + tl * T::kKeys + 16 * i < sp.n) next_id[i] = pages[pg];
+                next_at[i] = head_at + static_cast<uint32_t>(sl * 16 * row_bytes);
+                if (++sl == p.page_tiles) { sl = 0; ++pg; }
+            }
+            next_slot += step_slot;
+            next_page += step_page;
+            if (next_slot >= p.page_tiles) { next_slot -= p.page_tiles; ++next_page; }
+        };
+        auto take = [&]() {
+            bad = 0;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                id[i] = next_id[i];
+                at[i] = next_at[i];
+                if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
+                    if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                    id[i] = 0;
+                    bad |= 1 << i;
+                }
+            }
+        };
+        auto block_of = [&](int i, const char* cache, uint32_t page_step, uint32_t lane_at) {
+            return cache + static_cast<uint64_t>(static_cast<uint32_t>(id[i])) * page_step * 16 + (at[i] + lane_at);
+        };
+        // every key of the tile is there for every row
+        auto whole = [&](int tl) {
+            const int key = base + tl * T::kKeys;
+            return key >= sp.lo_all && key + T::kKeys <= sp.hi_all && bad == 0;
+        };
+        auto present = [&](int tl, int i, int k) {  // key k of block i is one that some row sees
+            const int key = base + tl * T::kKeys + 16 * i + k;
+            return key >= sp.lo && key < sp.n && !(bad >> i & 1);
+        };
+        const uint32_t k_lane = g * row_bytes + 16 * t, v_lane = 2 * t * row_bytes + (T::kVW == 2 ? 8 : 16) * g;
+        auto request_k = [&](int tl) {
+            if (whole(tl) && row_bytes == kRow) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const char* from = block_of(i, cache_k, p.page_step[0], k_lane);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int c = 0; c < T::kKC; ++c) kr[i][r][c] = ld16(from + 8 * r * kRow + 64 * c);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const char* from = block_of(i, cache_k, p.page_step[0], k_lane);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int c = 0; c < T::kKC; ++c) {
+                            kr[i][r][c] = make_uint4(0, 0, 0, 0);
+                            if (16 * t + 64 * c < row_bytes && present(tl, i, g + 8 * r)) kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
+                        }
+                }
+            }
+        };
+        auto put_v = [&](int i, int k, int c, auto v) {
+            if constexpr (T::kVW == 2) {
+                vr[i][k][0] = v.x; vr[i][k][1] = v.y;
+            } else {
+                vr[i][k][4 * c] = v.x; vr[i][k][4 * c + 1] = v.y; vr[i][k][4 * c + 2] = v.z; vr[i][k][4 * c + 3] = v.w;
+            }
+        };
+        constexpr int kVC = T::kVW == 2 ? 1 : T::kVW / 4;  // pieces of a key's values per lane
+        auto request_v = [&](int tl) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of each block
+            if (whole(tl) && row_bytes == kRow) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const char* from = block_of(i, cache_v, p.page_step[1], v_lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < kVC; ++c) put_v(i, k, c, ld_piece<T::kVW>(from + ((k & 1) + 8 * (k >> 1)) * kRow + 128 * c));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const char* from = block_of(i, cache_v, p.page_step[1], v_lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < kVC; ++c) {
+                            const int ahead = (k & 1) + 8 * (k >> 1);
+                            put_v(i, k, c, make_uint4(0, 0, 0, 0));
+                            if ((T::kVW == 2 ? 8 : 16) * g + 128 * c < row_bytes && present(tl, i, 2 * t + ahead))
+                                put_v(i, k, c, ld_piece<T::kVW>(from + ahead * row_bytes + 128 * c));
+                        }
+                }
+            }
+        };
+        look_up(tile);
+
+        // --- query rows as the scores' B operand
+        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kQ : 1];
         float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = row0 + 8 * nt + g;
-            uint2 raw[T::kKS];
+            uint2 raw[T::kQ];
             const int m = row / p.group;
             const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.rows + m) * p.q_ts +
                                      static_cast<int64_t>(h * p.group + row - m * p.group) * p.q_hs;
             const bool live = row < rows_all;
 #pragma unroll
-            for (int ks = 0; ks < T::kKS; ++ks) {
-                const int d = F8 ? 16 * (t + 4 * (ks >> 2)) + 4 * (ks & 3) : 8 * (t + 4 * (ks >> 1)) + 4 * (ks & 1);
-                raw[ks] = make_uint2(0, 0);
+            for (int i = 0; i < T::kQ; ++i) {  // 4 values each, in the order of the keys' registers
+                const int d = F8 ? 16 * (t + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (t + 4 * (i >> 1)) + 4 * (i & 1);
+                raw[i] = make_uint2(0, 0);
                 if (live && d < p.D) {
                     if (p.q_vec) {
-                        raw[ks] = *reinterpret_cast<const uint2*>(q + d);
+                        raw[i] = *reinterpret_cast<const uint2*>(q + d);
                     } else {
                         const uint16_t* w = reinterpret_cast<const uint16_t*>(q + d);
-                        raw[ks] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+                        raw[i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                     }
                 }
             }
+            // The factor from scores to base-2 units is made positive (its sign goes to q), so that the
+            // maximum can be taken over raw scores; a zero becomes 2^-126, or masked scores would be NaN.
             float f = p.scale * 1.4426950408889634f * kscale;
+            const uint32_t flip = f < 0.0f ? 0x80008000u : 0u;
+            f = fabsf(f);
             if constexpr (F8) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int ks = 0; ks < T::kKS; ++ks)
-                    top = max(max(max(top, raw[ks].x & 0x7fffu), max(raw[ks].x >> 16 & 0x7fffu, raw[ks].y & 0x7fffu)),
-                              raw[ks].y >> 16 & 0x7fffu);
+                for (int i = 0; i < T::kQ; ++i)
+                    top = max(max(max(top, raw[i].x & 0x7fffu), max(raw[i].x >> 16 & 0x7fffu, raw[i].y & 0x7fffu)),
+                              raw[i].y >> 16 & 0x7fffu);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the largest magnitude goes to [2^14, 2^15): every value down to 2^-28 of it is exact
-                // in f16, smaller ones are off by 2^-39 of it at most
-                const int e = static_cast<int>(top >> 7) - 127;
                 const bool plain = top == 0 || top >= 0x7f80u;
-                const int up = plain ? 0 : min(14 - e, 126);
+                const int up = plain ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
                 const float mul = __int_as_float((127 + up) << 23);
                 f *= __int_as_float((127 - up) << 23);
+                auto narrow = [&](uint32_t w) {  // values beyond f16 (next to an infinity) stay finite
+                    float v[2] = {bf16_lo(w) * mul, bf16_hi(w) * mul};
 #pragma unroll
-                for (int ks = 0; ks < T::kKS; ++ks) {
-                    float v[4] = {bf16_lo(raw[ks].x), bf16_hi(raw[ks].x), bf16_lo(raw[ks].y), bf16_hi(raw[ks].y)};
+                    for (int e = 0; e < 2; ++e)
+                        if (fabsf(v[e]) < INFINITY) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
+                    return pack_f16(v[0], v[1]);
+                };
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] *= mul;
-                        if (fabsf(v[i]) < INFINITY) v[i] = fminf(fmaxf(v[i], -65504.0f), 65504.0f);
-                    }
-                    raw[ks] = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
-                }
-                zf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-                zf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-            } else {
-                zf[nt][0] = zf[nt][1] = f;
+                for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(narrow(raw[i].x), narrow(raw[i].y));
             }
+            if (f < 1.1754943508e-38f) f = 1.1754943508e-38f;
 #pragma unroll
-            for (int ks = 0; ks < T::kKS; ++ks) {
-                if constexpr (T::kQRegs) qf[nt][ks] = raw[ks];
-                else if (stream == 0) s_q[((rb * NT + nt) * T::kKS + ks) * 32 + lane] = raw[ks];
+            for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(raw[i].x ^ flip, raw[i].y ^ flip);
+            zf[nt][0] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t) : f;
+            zf[nt][1] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t + 4) : f;
+#pragma unroll
+            for (int i = 0; i < T::kQ; ++i) {
+                if constexpr (T::kQRegs) qf[nt][i] = raw[i];
+                else if (stream == 0) s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane] = raw[i];
             }
         }
+        auto query = [&](int nt, int i) {
+            if constexpr (T::kQRegs) return qf[nt][i];
+            else return s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane];
+        };
         if constexpr (!T::kQRegs) __syncthreads();
 
         float o[NT][T::kMT][4], mx[NT][2], l[NT][2];
@@ -521,100 +666,11 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
-        // --- tiles of this warp: stream, stream + streams, ... of the run
-        const int tile_end = (s_run.last - s_run.item0) * streams;
-        int tile = (s_run.first - s_run.item0) * streams + stream;
-        uint4 kr[H][2][T::kKC];
-        uint32_t vr[H][4][T::kVW];
-        int at[H];                 // page ids of the requested tile
-        int pid[H];                // and of the one to be requested next
-        int bad = 0, bad_now = 0;  // blocks whose page id is out of range
-
-        auto lookup = [&](int tl) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int key = base + tl * T::kKeys + 16 * i, jb = key >> 4;
-                pid[i] = 0;
-                if (tl < tile_end && key < sp.n)
-                    pid[i] = p.table[b * p.table_stride + (p.page_shift >= 0 ? jb >> p.page_shift : jb / p.page_tiles)];
-            }
-        };
-        auto locate = [&]() {
-            bad = 0;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                at[i] = pid[i];
-                if (static_cast<unsigned>(at[i]) >= static_cast<unsigned>(p.pages)) {
-                    if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
-                    at[i] = 0;
-                    bad |= 1 << i;
-                }
-            }
-        };
-        auto block_of = [&](int tl, int i, const char* cache, int64_t page_stride) {
-            const int jb = (base + tl * T::kKeys + 16 * i) >> 4;
-            const int slot = p.page_shift >= 0 ? jb & (p.page_tiles - 1) : jb % p.page_tiles;
-            return cache + (at[i] * page_stride + (static_cast<int64_t>(h) * p.page + slot * 16) * p.D) * T::kES;
-        };
-        // every key of the tile is seen by every row
-        auto whole = [&](int tl) {
-            const int key = base + tl * T::kKeys;
-            return key >= sp.lo_all && key + T::kKeys <= sp.hi_all;
-        };
-        auto seen = [&](int tl, int i, int k) {  // key k of block i is in the sequence's range
-            const int key = base + tl * T::kKeys + 16 * i + k;
-            return key >= sp.lo && key < sp.n && !(bad >> i & 1);
-        };
-        auto request_k = [&](int tl) {
-            const bool all = whole(tl) && bad == 0 && p.D == DP;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const char* from = block_of(tl, i, cache_k, p.page_stride[0]) + g * row_bytes + 16 * t;
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int c = 0; c < T::kKC; ++c) {
-                        if (all) {
-                            kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
-                        } else {
-                            kr[i][r][c] = make_uint4(0, 0, 0, 0);
-                            if (16 * t + 64 * c < row_bytes && seen(tl, i, g + 8 * r)) kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
-                        }
-                    }
-            }
-        };
-        auto request_v = [&](int tl) {
-            const bool all = whole(tl) && bad == 0 && p.D == DP;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const char* from = block_of(tl, i, cache_v, p.page_stride[1]) + 2 * t * row_bytes + (T::kVW == 2 ? 8 : 16) * g;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int ahead = (k & 1) + 8 * (k >> 1);  // key 2t + ahead
-                    if constexpr (T::kVW == 2) {
-                        uint2 v = make_uint2(0, 0);
-                        if (all || (8 * g < row_bytes && seen(tl, i, 2 * t + ahead))) v = ld8(from + ahead * row_bytes);
-                        vr[i][k][0] = v.x; vr[i][k][1] = v.y;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < T::kVW / 4; ++c) {
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (all) v = ld16(from + ahead * row_bytes + 128 * c);
-                            else if (16 * g + 128 * c < row_bytes && seen(tl, i, 2 * t + ahead)) v = ld16(from + ahead * row_bytes + 128 * c);
-                            vr[i][k][4 * c] = v.x; vr[i][k][4 * c + 1] = v.y;
-                            vr[i][k][4 * c + 2] = v.z; vr[i][k][4 * c + 3] = v.w;
-                        }
-                    }
-                }
-            }
-        };
-
         if (tile < tile_end) {
-            lookup(tile);
-            locate();
+            take();
             request_k(tile);
             request_v(tile);
-            lookup(tile + streams);
+            look_up(tile + streams);
         }
         for (; tile < tile_end; tile += streams) {
             // --- scores
@@ -624,75 +680,78 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
 #pragma unroll
-                for (int ks = 0; ks < T::kKS; ++ks) {
-                    uint32_t a0, a1, a2, a3;
+                for (int c = 0; c < T::kKC; ++c) {
+                    const uint4 x = kr[i][0][c], y = kr[i][1][c];
                     if constexpr (F8) {
-                        const uint4 x = kr[i][0][ks >> 2], y = kr[i][1][ks >> 2];
-                        const uint32_t xw = (ks & 3) == 0 ? x.x : (ks & 3) == 1 ? x.y : (ks & 3) == 2 ? x.z : x.w;
-                        const uint32_t yw = (ks & 3) == 0 ? y.x : (ks & 3) == 1 ? y.y : (ks & 3) == 2 ? y.z : y.w;
-                        a0 = e4m3x2_f16x2(xw); a2 = e4m3x2_f16x2(xw >> 16);
-                        a1 = e4m3x2_f16x2(yw); a3 = e4m3x2_f16x2(yw >> 16);
-                    } else {
-                        const uint4 x = kr[i][0][ks >> 1], y = kr[i][1][ks >> 1];
-                        a0 = ks & 1 ? x.z : x.x; a2 = ks & 1 ? x.w : x.y;
-                        a1 = ks & 1 ? y.z : y.x; a3 = ks & 1 ? y.w : y.y;
-                    }
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint2 q;
-                        if constexpr (T::kQRegs) q = qf[nt][ks];
-                        else q = s_q[((rb * NT + nt) * T::kKS + ks) * 32 + lane];
-                        mma<F8>(s[i][nt], a0, a1, a2, a3, q.x, q.y);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a0 = e4m3x2_f16x2(xw[e]), a2 = e4m3x2_f16x2(xw[e] >> 16);
+                            const uint32_t a1 = e4m3x2_f16x2(yw[e]), a3 = e4m3x2_f16x2(yw[e] >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint2 q = query(nt, 4 * c + e);
+                                mma<true>(s[i][nt], a0, a1, a2, a3, q.x, q.y);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint2 q = query(nt, 2 * c);
+                            mma<false>(s[i][nt], x.x, y.x, x.y, y.y, q.x, q.y);
+                            q = query(nt, 2 * c + 1);
+                            mma<false>(s[i][nt], x.z, y.z, x.w, y.w, q.x, q.y);
+                        }
                     }
                 }
             }
-            const bool edge = !whole(tile) || bad != 0;
-            bad_now = bad;
-            const int next = tile + streams;
+            const bool edge = !whole(tile);
+            const int bad_now = bad, next = tile + streams;
             if (next < tile_end) {
-                locate();
+                take();
                 request_k(next);
             }
-            // --- mask, running maximum, probabilities
+            // --- mask, reference maximum, probabilities
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = row0 + 8 * nt + 2 * t + c;
+                        const int hi = row < rows_all ? sp.hi_all + row / p.group : 0, lo = p.window > 0 ? hi - p.window : 0;
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const int key = base + tile * T::kKeys + 16 * i + 8 * r + g;
+                                if (key < lo || key >= hi || (bad_now >> i & 1)) s[i][nt][2 * r + c] = -INFINITY;
+                            }
+                    }
+            }
             float top[NT][2];
-            bool moved = false;
+            bool passed = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float z = -INFINITY;
-                    int lo = 0, hi = 0;
-                    if (edge) {
-                        const int row = row0 + 8 * nt + 2 * t + c;
-                        hi = row < rows_all ? sp.hi_all + row / p.group : 0;
-                        lo = p.window > 0 ? hi - p.window : 0;
-                    }
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float v = s[i][nt][2 * r + c] * zf[nt][c];
-                            if (edge) {
-                                const int key = base + tile * T::kKeys + 16 * i + 8 * r + g;
-                                if (key < lo || key >= hi || (bad_now >> i & 1)) v = -INFINITY;
-                            }
-                            s[i][nt][2 * r + c] = v;
-                            z = fmaxf(z, v);
-                        }
-                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
-                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
-                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
-                    top[nt][c] = fmaxf(mx[nt][c], z);
-                    moved |= top[nt][c] != mx[nt][c];
+                    for (int i = 0; i < H; ++i) z = fmaxf(z, fmaxf(s[i][nt][c], s[i][nt][2 + c]));
+                    top[nt][c] = z * zf[nt][c];
+                    passed |= top[nt][c] > mx[nt][c] + kSlack;
                 }
-            if (__any_sync(0xffffffffu, moved)) {
+            if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float keep[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        keep[c] = top[nt][c] == mx[nt][c] ? 1.0f : exp2_fast(mx[nt][c] - top[nt][c]);
-                        mx[nt][c] = top[nt][c];
+                        float z = top[nt][c];
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+                        z = fmaxf(fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16)), mx[nt][c]);
+                        keep[c] = z == mx[nt][c] ? 1.0f : exp2_fast(mx[nt][c] - z);
+                        mx[nt][c] = z;
                         l[nt][c] *= keep[c];
                     }
 #pragma unroll
@@ -711,8 +770,8 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                     float e[4];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        e[2 * r] = exp2_fast(s[i][nt][2 * r] - m0);
-                        e[2 * r + 1] = exp2_fast(s[i][nt][2 * r + 1] - m1);
+                        e[2 * r] = exp2_fast(fmaf(s[i][nt][2 * r], zf[nt][0], -m0));
+                        e[2 * r + 1] = exp2_fast(fmaf(s[i][nt][2 * r + 1], zf[nt][1], -m1));
                         l[nt][0] += e[2 * r];
                         l[nt][1] += e[2 * r + 1];
                         pb[i][nt][r] = transpose8x8(F8 ? pack_f16(e[2 * r], e[2 * r + 1]) : pack_bf16(e[2 * r], e[2 * r + 1]));
@@ -790,7 +849,7 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             }
             if (next < tile_end) {
                 request_v(next);
-                lookup(next + streams);
+                look_up(next + streams);
             }
         }
 
@@ -816,22 +875,21 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         const Run r = s_run;
         const bool direct = r.first == r.item0 && r.last == r.item_end;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1);
-        const int quads = p.D / 4;
-        for (int i = tid; i < rows_all * quads; i += kThreads) {
-            const int row = i / quads, d = 4 * (i - row * quads);
-            const int blk = row / kRowsW, rr = row - blk * kRowsW;
-            float m = -INFINITY, lsum = 0.0f;
-            for (int st = 0; st < streams; ++st) m = fmaxf(m, s_ml[(st * p.row_blocks + blk) * kRowsW + rr].x);
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int d = 4 * (tid & ((1 << p.quad_log2) - 1));
+#pragma unroll 1
+        for (int row = tid >> p.quad_log2; row < rows_all; row += kThreads >> p.quad_log2) {
+            if (d >= p.D) continue;
+            Gathered a;
+#pragma unroll 1
             for (int st = 0; st < streams; ++st) {
-                const int w = (st * p.row_blocks + blk) * kRowsW + rr;
-                add_part(sum, lsum, s_ml[w], *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d), m);
+                const int w = st * p.row_blocks * kRowsW + row;
+                a.add(s_ml[w], *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d));
             }
             if (direct) {
-                store_out(p, r.seq, r.head, row, d, sum, m, lsum);
+                store_out(p, r.seq, r.head, row, d, a);
             } else {
-                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * rows_all + row) * p.D + d), sum);
-                if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(m, lsum));
+                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * rows_all + row) * p.D + d), a.o);
+                if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(a.m, a.l));
             }
         }
         if (!direct) finish_item(p, s_join, s_run);
@@ -873,7 +931,7 @@ bool plan_tile(int dim, int rows, TilePlan* out) {
     t.nt = t.dp == 256 || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     while (t.row_blocks < t.warps && 8 * t.nt * t.row_blocks < rows) t.row_blocks *= 2;
     if (8 * t.nt * t.row_blocks < rows) return false;
-    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt == 1 ? 3 : 2;
+    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? 3 : 2;
     *out = t;
     return true;
 }
@@ -900,7 +958,7 @@ template <int DP, int NT, bool F8>
 nvfp4_status launch_tile(const AttnParams& p, int grid, cudaStream_t stream) {
     using T = TileShape<DP, NT, F8>;
     const size_t smem = static_cast<size_t>(T::kWarps) * 8 * NT * (T::kOStride * 4 + 8) +
-                        (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kKS * 256);
+                        (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kQ * 256);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(paged_attention_tile_kernel<DP, NT, F8>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -970,7 +1028,8 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
     if (host_variant() != 1 && most_units < (1ll << 31) && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
         aligned(p.cache[0], 16) && aligned(p.cache[1], 16) && p.page_stride[0] * es % 16 == 0 && p.page_stride[1] * es % 16 == 0 &&
-        aligned(p.out, 8)) {
+        aligned(p.out, 8) && p.page_stride[0] >= 0 && p.page_stride[1] >= 0 && p.page_stride[0] * es / 16 < (1ll << 32) &&
+        p.page_stride[1] * es / 16 < (1ll << 32) && static_cast<int64_t>(p.hk) * p.page * p.D * es < (1ll << 31)) {
         const int grid = t.ctas_per_sm * sm_count();
         const Workspace w = workspace_of(grid, p.seqs, rows_all, p.hk, p.D);
         char* base = static_cast<char*>(a->workspace);
@@ -978,9 +1037,9 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         p.part_o = reinterpret_cast<float*>(base + w.part_o);
         p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
         p.row_blocks = t.row_blocks;
+        for (int i = 0; i < 2; ++i) p.page_step[i] = static_cast<uint32_t>(p.page_stride[i] * es / 16);
+        while ((4 << p.quad_log2) < p.D) ++p.quad_log2;
         p.page_tiles = p.page / 16;
-        p.page_shift = -1;
-        for (int s = 0; s < 20; ++s) if (p.page_tiles == 1 << s) p.page_shift = s;
         p.min_units = 1;
         p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
