@@ -4846,6 +4846,15 @@ bool register_status(StatusReader reader) {
 bool host_pdl_enabled() { return g_pdl; }
 int host_variant() { return g_variant; }
 nvfp4_status host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+uint64_t host_wait_ns() { return g_wait_ns; }
+bool host_encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    const auto encode = tensor_map_encoder();
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return encode && encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 int host_sm_count() {
     const DeviceInfo* d = device_info(nullptr);
     return d ? d->sm_count : 0;

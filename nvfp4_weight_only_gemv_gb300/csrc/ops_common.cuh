@@ -2,6 +2,7 @@
 // the host state that lives beside the GEMV entry points (nvfp4_gemv.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -17,6 +18,10 @@ bool host_pdl_enabled();                       // nvfp4_set_pdl
 int host_variant();                            // nvfp4_set_variant
 nvfp4_status host_cuda_fail(cudaError_t e);    // records e for nvfp4_last_cuda_error
 int host_sm_count();                           // SMs of the current device, 0 on an error
+uint64_t host_wait_ns();                       // nvfp4_set_wait_budget_ns
+// Encodes a tiled tensor map (unit element strides, no interleave, zero fill).
+bool host_encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // Device status words of the operators' own translation units (device symbols are not shared
 // between units): each unit registers, when the library is loaded, a function that reads its word

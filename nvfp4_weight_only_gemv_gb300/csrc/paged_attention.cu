@@ -8,6 +8,8 @@
 
 #include "ops_common.cuh"
 
+#include <cuda.h>
+
 #include <cmath>
 
 namespace nvfp4 {
@@ -39,10 +41,14 @@ struct AttnParams {
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
     int page_tiles;             // 16-key blocks per page
-    uint32_t page_step[2];      // page strides in 16-byte pieces
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
+    uint64_t wait_ns;           // budget of a wait for a copy
     int min_units;              // units of work a CTA takes at least
     int q_vec;                  // q may be read 8 bytes at a time
+};
+
+struct TileParams : AttnParams {
+    CUtensorMap map[2];  // k, v: [pages][kv heads][page][D], boxes of 16 keys x 128 bytes
 };
 
 __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
@@ -71,6 +77,7 @@ __device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t
 
 constexpr int kScalarWarps = 4;
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
+constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kJoinOnce = 16;  // parts that one CTA joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
@@ -141,17 +148,22 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 // ------------------------------------------------------------------ tile kernel
 //
 // One warp takes 16 keys (or a few times 16: TileShape::kKeys) and up to 8 * NT query rows of one
-// kv head (rows * group of them) at a time, entirely in registers:
+// kv head (rows * group of them) at a time:
 //
 //   S^T [16 keys x 8 rows]   = K [16 x D] . Q^T        mma m16n8k16, A = keys, B = rows
 //   O^T [16 dims x 8 rows]  += V^T [16 x 16 keys] . P^T
 //
 // Keys stand on the tensor core's 16-row side and the few query rows on its 8-column side, so a
 // group of 4 heads wastes half of a column block instead of three quarters of a row block. The
-// order of the head's dimensions inside a product is free, so a lane loads 16 consecutive bytes of
-// a key (K) or of four keys (V) straight from the cache into the operand's registers: neither
-// passes through shared memory. V's pairs of keys are formed by byte permutes (E4M3 codes are
-// widened to f16 behind the permute), P^T by two transposing moves of 8 x 8 halves.
+// order of the head's dimensions inside a product is free, so what a lane needs of a key (K) or of
+// four keys (V) is whole 16-byte pieces. V's pairs of keys are formed by byte permutes (E4M3 codes
+// are widened to f16 behind the permute), P^T by two transposing moves of 8 x 8 halves.
+//
+// Every warp keeps a ring of its own tiles (kStages of 8 KB at D <= 128) filled by TMA tensor copies
+// of 16 keys x 128 bytes, swizzled so that V's pieces are read without a bank conflict and K's with
+// two lanes to a bank; K and V of a stage have a barrier each and are requested again as soon as
+// they are read, by the warp itself, so no warp waits for another. Straight into registers, with one
+// tile a warp in flight, E4M3 with 16 rows reached 4.2 TB/s; by cp.async into the same ring 3.9.
 //
 // E4M3 keys and values are widened to f16 in registers (exact; mma.sync on E4M3 operands is no
 // instruction here but is built from the same conversions and f16 products: it executed 11 % more
@@ -163,9 +175,7 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 // They enter the products rounded, to bf16 next to bf16 values and to f16 next to E4M3 ones (at most
 // 2^8, far inside f16's range); the sum of exponentials is taken before the rounding.
 //
-// The kernel is bound by the cache's bytes. What keeps them coming is loads in flight: K of the
-// next tile is requested as soon as this tile's scores are formed, V as soon as its products are,
-// 8 KB a warp at D = 128.
+// The kernel is bound by the cache's bytes.
 //
 // Work is split over the length without the host knowing the lengths: all (sequence, kv head)
 // items lie end to end in units of S tiles (S warps side by side), and every CTA takes an equal
@@ -175,9 +185,7 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 
 template <int DP, int NT, bool F8>
 struct TileShape {
-    // 16-key blocks of a tile: 64 registers of keys and values, 32 where many rows need theirs
-    static constexpr int kFull = F8 ? 256 / DP : 128 / DP, kFit = F8 && NT * DP > 64 && NT > 1 && (NT == 4 || DP == 64) ? kFull / 2 : kFull;
-    static constexpr int kHalves = kFit < 1 ? 1 : kFit;
+    static constexpr int kHalves = F8 ? (DP >= 256 ? 1 : 256 / DP) : (DP >= 128 ? 1 : 128 / DP);  // 16-key blocks
     static constexpr int kKeys = 16 * kHalves;
     static constexpr int kES = F8 ? 1 : 2;                 // bytes per value
     static constexpr int kKC = DP * kES / 64;              // 16-byte chunks of a key row per lane
@@ -185,27 +193,80 @@ struct TileShape {
     static constexpr int kMT = DP / 16;                    // 16-dim blocks of O
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
-    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? 3 : 2;  // per SM
+    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 256 ? 3 : 2;  // per SM
     static constexpr bool kQRegs = NT * DP <= 256;
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
+    static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
+    static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
+    static constexpr int kBox = 16 * kBoxBytes;
+    static constexpr int kPart = kHalves * kBoxes * kBox;  // K (or V) bytes of a tile
+    static constexpr int kStages = DP * kES == 512 ? 1 : 2;
+    static constexpr int kRing = kWarps * kStages * 2 * kPart;
+    static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
+    static constexpr int kMain = kRing > kMerge ? kRing : kMerge;  // the merge takes the ring's place
 };
 
-__device__ __forceinline__ uint4 ld16(const char* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+__device__ __forceinline__ void barrier_init(uint32_t bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint2 ld8(const char* p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t ns;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(ns));
+    return ns;
+}
+// Waits for a barrier's phase at most `budget` ns (0: polls once); the same answer in every lane.
+__device__ __noinline__ bool barrier_wait_slow(uint32_t bar, uint32_t parity, uint64_t budget) {
+    const uint64_t begin = global_ns();
+    bool ok = false;
+    while (!ok && global_ns() - begin <= budget) ok = barrier_try(bar, parity);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, uint64_t budget) {
+    const bool ok = budget == 0 ? barrier_test(bar, parity) : barrier_try(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return budget != 0 && barrier_wait_slow(bar, parity, budget);
 }
 
-template <int WORDS>
-__device__ __forceinline__ auto ld_piece(const char* p) {
-    if constexpr (WORDS == 2) return ld8(p);
-    else return ld16(p);
+// A cache is read once per call and is larger than L2 when it matters: its lines leave L2 first.
+__device__ __forceinline__ uint64_t evict_first() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int x, int key, int head, int page, uint32_t bar,
+                                         uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        ::"r"(to), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(key), "r"(head), "r"(page), "r"(bar), "l"(pol) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
 }
 
 template <bool F8>
@@ -393,17 +454,20 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
 
 template <int DP, int NT, bool F8>
 __global__ void __launch_bounds__(TileShape<DP, NT, F8>::kWarps * 32, TileShape<DP, NT, F8>::kCtas)
-paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
+paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     using T = TileShape<DP, NT, F8>;
     constexpr int H = T::kHalves, W = T::kWarps, kThreads = W * 32;
     constexpr int kRowsW = 8 * NT;
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ uint8_t smem_raw[];
+    // rings [W][kStages][K, V], on a boundary of the swizzle's pattern; then s_q
+    float* const smem = reinterpret_cast<float*>(smem_raw + (-static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u));
+    __shared__ __align__(8) uint64_t s_bar[W][T::kStages][2];
     __shared__ int s_scan[W];
     __shared__ Run s_run;
     __shared__ JoinShared s_join;
-    float* s_o = smem;                                        // [W][kRowsW][kOStride]
+    float* s_o = smem;                                        // merge, in the rings' place: [W][kRowsW][kOStride]
     float2* s_ml = reinterpret_cast<float2*>(s_o + W * kRowsW * T::kOStride);  // [W][kRowsW]
-    uint2* s_q = reinterpret_cast<uint2*>(s_ml + W * kRowsW);  // [row_blocks][NT][kKS][32] (not kQRegs)
+    uint2* s_q = reinterpret_cast<uint2*>(smem + T::kMain / 4);  // [row_blocks][NT][kQ][32] (not kQRegs)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = W / p.row_blocks;
@@ -411,6 +475,10 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
     const int unit_keys = streams * T::kKeys;
 
     pdl_launch_dependents();
+    const uint32_t bars = static_cast<uint32_t>(__cvta_generic_to_shared(&s_bar[warp][0][0]));
+    if (lane < 2 * T::kStages) barrier_init(bars + 8 * lane);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map[tid])) : "memory");
     pdl_wait();
 
     // --- the CTA's run of units: prefix sums of the sequences' unit counts
@@ -464,10 +532,19 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         __syncthreads();
     }
 
-    const char* const cache_k = static_cast<const char*>(p.cache[0]);
-    const char* const cache_v = static_cast<const char*>(p.cache[1]);
-    const int row_bytes = p.D * T::kES;
-    constexpr int kRow = DP * T::kES;  // the same where the head is not padded
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (T::kStages * 2 * T::kPart);
+    uint32_t cur = 0;      // the stage of the tile in work
+    uint32_t parity = 0;   // of each barrier's next phase, bit 2 * stage + which
+    uint32_t pending = 0;  // copies in flight, bits alike
+    bool dead = false;     // a copy did not come in time
+    // offsets of this lane's pieces in a box: K's of rows g (and g + 8), V's of rows 2t and 2t + 1
+    // (and 8 further). A 16-byte piece j of row r stands at piece j ^ (r & 7), in rows of 64 bytes at
+    // j ^ (r >> 1 & 3).
+    constexpr int kRow = T::kBoxBytes;
+    const uint32_t k_off = kRow == 128 ? g * 128 + ((t ^ g) << 4) : g * 64 + ((t ^ (g >> 1 & 3)) << 4);
+    const uint32_t v_off[2] = {
+        kRow == 128 ? 2 * t * 128 + ((g ^ 2 * t) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8,
+        kRow == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4) : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8};
 
     for (;;) {
         const int b = s_run.seq, h = s_run.head;
@@ -475,7 +552,6 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         const int base = sp.lo & ~15;
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
         const int32_t* const pages = p.table + b * p.table_stride;
-        const uint32_t head_at = static_cast<uint32_t>(h * p.page * row_bytes);
 
         // --- tiles of this warp: stream, stream + streams, ... of the run. A tile's first 16-key block
         // stands at block `slot` of the sequence's page `page`; both walk along with the tiles.
@@ -483,11 +559,9 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         int tile = (s_run.first - s_run.item0) * streams + stream;
         const int step_page = streams * H / p.page_tiles, step_slot = streams * H % p.page_tiles;
         int next_page = ((base >> 4) + tile * H) / p.page_tiles, next_slot = ((base >> 4) + tile * H) % p.page_tiles;
-        uint4 kr[H][2][T::kKC];
-        uint32_t vr[H][4][T::kVW];
         int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
-        uint32_t at[H], next_at[H];     // where the block starts in its page, bytes
-        int bad = 0;                    // blocks of the requested tile whose page id is out of range
+        int at[H], next_at[H];          // the block's first key in its page
+        uint32_t bad = 0, bads = 0;     // blocks whose page id is out of range: requested tile; tiles in the ring
 
         // looks up the tile after the requested one
         auto look_up = [&](int tl) {
@@ -496,7 +570,7 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             for (int i = 0; i < H; ++i) {
                 next_id[i] = 0;
                 if (tl < tile_end && base + tl * T::kKeys + 16 * i < sp.n) next_id[i] = pages[pg];
-                next_at[i] = head_at + static_cast<uint32_t>(sl * 16 * row_bytes);
+                next_at[i] = 16 * sl;
                 if (++sl == p.page_tiles) { sl = 0; ++pg; }
             }
             next_slot += step_slot;
@@ -512,80 +586,36 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                 if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
                     if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
                     id[i] = 0;
-                    bad |= 1 << i;
+                    bad |= 1u << i;
                 }
             }
         };
-        auto block_of = [&](int i, const char* cache, uint32_t page_step, uint32_t lane_at) {
-            return cache + static_cast<uint64_t>(static_cast<uint32_t>(id[i])) * page_step * 16 + (at[i] + lane_at);
+        // copies K (which = 0) or V of the taken tile to a stage; every lane is through with its last use
+        auto request = [&](uint32_t stage, int which) {
+            __syncwarp();
+            const uint32_t bar = bars + 16 * stage + 8 * which, to = ring + (2 * stage + which) * T::kPart;
+            if (lane == 0) {
+                const uint64_t pol = evict_first();
+                barrier_expect(bar, T::kPart);
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int x = 0; x < T::kBoxes; ++x)
+                        copy_box(to + (i * T::kBoxes + x) * T::kBox, &p.map[which], x * (T::kBoxBytes / T::kES), at[i], h, id[i], bar, pol);
+            }
+            pending |= 1u << (2 * stage + which);
+        };
+        auto arrived = [&](uint32_t stage, int which) {
+            const uint32_t bit = 2 * stage + which;
+            if (!barrier_wait(bars + 8 * bit, parity >> bit & 1u, p.wait_ns)) return false;
+            parity ^= 1u << bit;
+            pending &= ~(1u << bit);
+            return true;
         };
         // every key of the tile is there for every row
         auto whole = [&](int tl) {
             const int key = base + tl * T::kKeys;
-            return key >= sp.lo_all && key + T::kKeys <= sp.hi_all && bad == 0;
-        };
-        auto present = [&](int tl, int i, int k) {  // key k of block i is one that some row sees
-            const int key = base + tl * T::kKeys + 16 * i + k;
-            return key >= sp.lo && key < sp.n && !(bad >> i & 1);
-        };
-        const uint32_t k_lane = g * row_bytes + 16 * t, v_lane = 2 * t * row_bytes + (T::kVW == 2 ? 8 : 16) * g;
-        auto request_k = [&](int tl) {
-            if (whole(tl) && row_bytes == kRow) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const char* from = block_of(i, cache_k, p.page_step[0], k_lane);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int c = 0; c < T::kKC; ++c) kr[i][r][c] = ld16(from + 8 * r * kRow + 64 * c);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const char* from = block_of(i, cache_k, p.page_step[0], k_lane);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int c = 0; c < T::kKC; ++c) {
-                            kr[i][r][c] = make_uint4(0, 0, 0, 0);
-                            if (16 * t + 64 * c < row_bytes && present(tl, i, g + 8 * r)) kr[i][r][c] = ld16(from + 8 * r * row_bytes + 64 * c);
-                        }
-                }
-            }
-        };
-        auto put_v = [&](int i, int k, int c, auto v) {
-            if constexpr (T::kVW == 2) {
-                vr[i][k][0] = v.x; vr[i][k][1] = v.y;
-            } else {
-                vr[i][k][4 * c] = v.x; vr[i][k][4 * c + 1] = v.y; vr[i][k][4 * c + 2] = v.z; vr[i][k][4 * c + 3] = v.w;
-            }
-        };
-        constexpr int kVC = T::kVW == 2 ? 1 : T::kVW / 4;  // pieces of a key's values per lane
-        auto request_v = [&](int tl) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of each block
-            if (whole(tl) && row_bytes == kRow) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const char* from = block_of(i, cache_v, p.page_step[1], v_lane);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int c = 0; c < kVC; ++c) put_v(i, k, c, ld_piece<T::kVW>(from + ((k & 1) + 8 * (k >> 1)) * kRow + 128 * c));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const char* from = block_of(i, cache_v, p.page_step[1], v_lane);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int c = 0; c < kVC; ++c) {
-                            const int ahead = (k & 1) + 8 * (k >> 1);
-                            put_v(i, k, c, make_uint4(0, 0, 0, 0));
-                            if ((T::kVW == 2 ? 8 : 16) * g + 128 * c < row_bytes && present(tl, i, 2 * t + ahead))
-                                put_v(i, k, c, ld_piece<T::kVW>(from + ahead * row_bytes + 128 * c));
-                        }
-                }
-            }
+            return key >= sp.lo_all && key + T::kKeys <= sp.hi_all;
         };
         look_up(tile);
 
@@ -666,14 +696,22 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
-        if (tile < tile_end) {
-            take();
-            request_k(tile);
-            request_v(tile);
-            look_up(tile + streams);
+#pragma unroll
+        for (int st = 0; st < T::kStages; ++st) {
+            const int tl = tile + st * streams;
+            if (tl < tile_end && !dead) {
+                take();
+                const uint32_t stage = cur + st < T::kStages ? cur + st : cur + st - T::kStages;
+                request(stage, 0);
+                request(stage, 1);
+                bads |= bad << 8 * st;
+                look_up(tl + streams);
+            }
         }
-        for (; tile < tile_end; tile += streams) {
+        for (; tile < tile_end && !dead; tile += streams) {
             // --- scores
+            if (!arrived(cur, 0)) { dead = true; break; }
+            const uint32_t kt = ring + 2 * cur * T::kPart + k_off, vt = ring + (2 * cur + 1) * T::kPart;
             float s[H][NT][4];
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -681,7 +719,9 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                 for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < T::kKC; ++c) {
-                    const uint4 x = kr[i][0][c], y = kr[i][1][c];
+                    // piece t + 4c of rows g and g + 8
+                    const uint32_t from = (kt ^ (kRow == 128 ? 64 * (c & 1) : 0)) + (i * T::kBoxes + (kRow == 128 ? c >> 1 : c)) * T::kBox;
+                    const uint4 x = lds16(from), y = lds16(from + 8 * kRow);
                     if constexpr (F8) {
                         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -705,11 +745,14 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                     }
                 }
             }
-            const bool edge = !whole(tile);
-            const int bad_now = bad, next = tile + streams;
+            const uint32_t bad_now = bads & 0xffu;
+            const bool edge = !whole(tile) || bad_now != 0;
+            const int next = tile + T::kStages * streams;
+            bads >>= 8;
             if (next < tile_end) {
                 take();
-                request_k(next);
+                request(cur, 0);
+                bads |= bad << 8 * (T::kStages - 1);
             }
             // --- mask, reference maximum, probabilities
             if (edge) {
@@ -724,7 +767,7 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const int key = base + tile * T::kKeys + 16 * i + 8 * r + g;
-                                if (key < lo || key >= hi || (bad_now >> i & 1)) s[i][nt][2 * r + c] = -INFINITY;
+                                if (key < lo || key >= hi || (bad_now >> i & 1u)) s[i][nt][2 * r + c] = -INFINITY;
                             }
                     }
             }
@@ -780,61 +823,89 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
             }
             // --- O^T += V^T P^T. A weight of zero must also silence what is not finite: in tiles that
             // some row sees only in part, such values are taken row by row of the sequence below.
+            if (!arrived(cur, 1)) { dead = true; break; }
+            uint32_t vr[4][T::kVW];
+            auto load_v = [&](int i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+                    const uint32_t from = vt + i * (T::kBoxes * T::kBox) + v_off[k & 1] + (k >> 1) * (8 * kRow);
+                    if constexpr (T::kVW == 2) {
+                        const uint2 v = lds8(from);
+                        vr[k][0] = v.x; vr[k][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < T::kVW / 4; ++c) {
+                            const uint4 v = lds16(from + c * T::kBox);
+                            vr[k][4 * c] = v.x; vr[k][4 * c + 1] = v.y; vr[k][4 * c + 2] = v.z; vr[k][4 * c + 3] = v.w;
+                        }
+                    }
+                }
+            };
+            // keeps values of keys [lo, hi) of block i (of none if its page is bad), zeros the others
+            auto keep_v = [&](int i, int lo, int hi) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = base + tile * T::kKeys + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1);
+                    if (key < lo || key >= hi || (bad_now >> i & 1u)) {
+#pragma unroll
+                        for (int w = 0; w < T::kVW; ++w) vr[k][w] = 0;
+                    }
+                }
+            };
+            auto operands = [&](int mt, uint32_t (&a)[4]) {
+                if constexpr (F8) {
+                    const int w = mt >> 1;
+                    const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(vr[0][w], vr[1][w], sel), y = __byte_perm(vr[2][w], vr[3][w], sel);
+                    a[0] = e4m3x2_f16x2(x); a[1] = e4m3x2_f16x2(x >> 16);
+                    a[2] = e4m3x2_f16x2(y); a[3] = e4m3x2_f16x2(y >> 16);
+                } else {
+                    a[0] = __byte_perm(vr[0][mt], vr[1][mt], 0x5410); a[1] = __byte_perm(vr[0][mt], vr[1][mt], 0x7632);
+                    a[2] = __byte_perm(vr[2][mt], vr[3][mt], 0x5410); a[3] = __byte_perm(vr[2][mt], vr[3][mt], 0x7632);
+                }
+            };
             bool special = false;
             if (edge && (p.rows > 1 || p.window > 0)) {
-#pragma unroll
-                for (int i = 0; i < H; ++i)
+#pragma unroll 1
+                for (int i = 0; i < H; ++i) {
+                    load_v(i);
+                    keep_v(i, sp.lo, sp.n);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int w = 0; w < T::kVW; ++w) {
-                            const uint32_t x = vr[i][k][w];
+                            const uint32_t x = vr[k][w];
                             if constexpr (F8) special |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
                             else special |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
                         }
+                }
                 special = __any_sync(0xffffffffu, special);
             }
-            auto operands = [&](int i, int mt, const uint32_t (&keep)[4], uint32_t (&a)[4]) {
-                if constexpr (F8) {
-                    const int w = mt >> 1;
-                    const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
-                    const uint32_t x = __byte_perm(vr[i][0][w] & keep[0], vr[i][1][w] & keep[1], sel);
-                    const uint32_t y = __byte_perm(vr[i][2][w] & keep[2], vr[i][3][w] & keep[3], sel);
-                    a[0] = e4m3x2_f16x2(x); a[1] = e4m3x2_f16x2(x >> 16);
-                    a[2] = e4m3x2_f16x2(y); a[3] = e4m3x2_f16x2(y >> 16);
-                } else {
-                    const uint32_t k0 = vr[i][0][mt] & keep[0], k1 = vr[i][1][mt] & keep[1];
-                    const uint32_t k2 = vr[i][2][mt] & keep[2], k3 = vr[i][3][mt] & keep[3];
-                    a[0] = __byte_perm(k0, k1, 0x5410); a[1] = __byte_perm(k0, k1, 0x7632);
-                    a[2] = __byte_perm(k2, k3, 0x5410); a[3] = __byte_perm(k2, k3, 0x7632);
-                }
-            };
             if (!special) {
-                const uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
-                for (int i = 0; i < H; ++i)
+                for (int i = 0; i < H; ++i) {
+                    load_v(i);
+                    if (edge) keep_v(i, sp.lo, sp.n);  // what a page holds beyond the sequence may be anything
 #pragma unroll
                     for (int mt = 0; mt < T::kMT; ++mt) {
                         uint32_t a[4];
-                        operands(i, mt, keep, a);
+                        operands(mt, a);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma<F8>(o[nt][mt], a[0], a[1], a[2], a[3], pb[i][nt][0], pb[i][nt][1]);
                     }
+                }
             } else {
+#pragma unroll 1
                 for (int m = 0; m < p.rows; ++m) {
                     const int hi = sp.hi_all + m, lo = p.window > 0 ? hi - p.window : 0;
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        uint32_t keep[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int key = base + tile * T::kKeys + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1);
-                            keep[k] = key >= lo && key < hi ? ~0u : 0u;
-                        }
+                        load_v(i);
+                        keep_v(i, max(lo, 0), min(hi, sp.n));
 #pragma unroll
                         for (int mt = 0; mt < T::kMT; ++mt) {
                             uint32_t a[4];
-                            operands(i, mt, keep, a);
+                            operands(mt, a);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -848,10 +919,20 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
             if (next < tile_end) {
-                request_v(next);
+                request(cur, 1);
                 look_up(next + streams);
             }
+            cur = cur + 1 == T::kStages ? 0 : cur + 1;
         }
+        if (dead) {
+            // the result is unspecified, but no copy may outlive the CTA
+            if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_TIMEOUT);
+#pragma unroll 1
+            for (int i = 0; i < 2 * T::kStages; ++i)
+                if (pending >> i & 1u) barrier_wait(bars + 8 * i, parity >> i & 1u, kDrainNs);
+            pending = 0;
+        }
+        __syncthreads();  // every warp is through with its ring
 
         // --- the warps' parts meet in shared memory
 #pragma unroll
@@ -894,7 +975,8 @@ paged_attention_tile_kernel(const __grid_constant__ AttnParams p) {
         }
         if (!direct) finish_item(p, s_join, s_run);
         if (r.last == r.end) return;
-        __syncthreads();  // s_run, the merge buffer and s_q are free again
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge buffer is the rings' again
+        __syncthreads();  // and s_run and s_q are free
         if (tid == 0) {
             Run& n = s_run;
             if (++n.head == p.hk) {
@@ -931,7 +1013,7 @@ bool plan_tile(int dim, int rows, TilePlan* out) {
     t.nt = t.dp == 256 || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     while (t.row_blocks < t.warps && 8 * t.nt * t.row_blocks < rows) t.row_blocks *= 2;
     if (8 * t.nt * t.row_blocks < rows) return false;
-    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? 3 : 2;
+    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 256 ? 3 : 2;
     *out = t;
     return true;
 }
@@ -955,10 +1037,21 @@ int sm_count() {
 }
 
 template <int DP, int NT, bool F8>
-nvfp4_status launch_tile(const AttnParams& p, int grid, cudaStream_t stream) {
+nvfp4_status launch_tile(const AttnParams& a, int grid, cudaStream_t stream) {
     using T = TileShape<DP, NT, F8>;
-    const size_t smem = static_cast<size_t>(T::kWarps) * 8 * NT * (T::kOStride * 4 + 8) +
-                        (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kQ * 256);
+    TileParams p;
+    static_cast<AttnParams&>(p) = a;
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t row = static_cast<uint64_t>(p.D) * T::kES, page = row * p.page;
+        const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.page), static_cast<uint64_t>(p.hk),
+                                  static_cast<uint64_t>(p.pages)};
+        const uint64_t strides[3] = {row, page, p.pages > 1 ? static_cast<uint64_t>(p.page_stride[i]) * T::kES : page * p.hk};
+        const uint32_t box[4] = {T::kBoxBytes / T::kES, 16, 1, 1};
+        if (!host_encode_map(&p.map[i], F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.cache[i], dims,
+                             strides, box, T::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return NVFP4_ERR_UNSUPPORTED;
+    }
+    const size_t smem = 1024 + T::kMain + (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kQ * 256);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(paged_attention_tile_kernel<DP, NT, F8>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1028,8 +1121,8 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
     if (host_variant() != 1 && most_units < (1ll << 31) && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
         aligned(p.cache[0], 16) && aligned(p.cache[1], 16) && p.page_stride[0] * es % 16 == 0 && p.page_stride[1] * es % 16 == 0 &&
-        aligned(p.out, 8) && p.page_stride[0] >= 0 && p.page_stride[1] >= 0 && p.page_stride[0] * es / 16 < (1ll << 32) &&
-        p.page_stride[1] * es / 16 < (1ll << 32) && static_cast<int64_t>(p.hk) * p.page * p.D * es < (1ll << 31)) {
+        aligned(p.out, 8) && p.pages > 0 && p.page_stride[0] > 0 && p.page_stride[1] > 0 &&
+        p.page_stride[0] * es < (1ll << 40) && p.page_stride[1] * es < (1ll << 40)) {
         const int grid = t.ctas_per_sm * sm_count();
         const Workspace w = workspace_of(grid, p.seqs, rows_all, p.hk, p.D);
         char* base = static_cast<char*>(a->workspace);
@@ -1037,7 +1130,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         p.part_o = reinterpret_cast<float*>(base + w.part_o);
         p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
         p.row_blocks = t.row_blocks;
-        for (int i = 0; i < 2; ++i) p.page_step[i] = static_cast<uint32_t>(p.page_stride[i] * es / 16);
+        p.wait_ns = host_wait_ns();
         while ((4 << p.quad_log2) < p.D) ++p.quad_log2;
         p.page_tiles = p.page / 16;
         p.min_units = 1;

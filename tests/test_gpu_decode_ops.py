@@ -592,3 +592,18 @@ def test_attention_workspace_is_left_ready():
     nv.paged_attention(q, kc, vc, table, ln // 3, workspace=ws)
     nv.paged_attention(q[:, :4], kc, vc, table, ln, workspace=ws)
     assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, workspace=ws), want)
+
+
+def test_paged_attention_wait_budget():
+    # with no time for its copies the call sets the status, ends, and leaves the workspace ready
+    q, kc, vc, table, ln, _, _ = _attend_inputs([3000, 30], 1, 8, 2, 128, BF16, 16, 7)
+    ws = nv.attention_workspace(2, 1, 8, 2, 128)
+    want = nv.paged_attention(q, kc, vc, table, ln, workspace=ws)
+    try:
+        nv.set_wait_budget_ns(0)
+        nv.paged_attention(q, kc, vc, table, ln, workspace=ws)
+        assert nv.device_status() == nv.DEV_TIMEOUT
+    finally:
+        nv.set_wait_budget_ns(None)
+    assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, workspace=ws), want)
+    assert nv.device_status() == 0
