@@ -39,6 +39,7 @@ struct AttnParams {
     int* counters;              // workspace: arrivals per (sequence, kv head), then per part; zero between calls
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
+    int wide_box, tall_box;     // one copy brings all of a block's boxes; all blocks of a tile
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
     int page_tiles;             // 16-key blocks per page
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
@@ -48,7 +49,9 @@ struct AttnParams {
 };
 
 struct TileParams : AttnParams {
-    CUtensorMap map[2];  // k, v: [pages][kv heads][page][D], boxes of 16 keys x 128 bytes
+    // k, v: [pages][kv heads][D / 64 pieces of 128 bytes][page][piece] (wide boxes) or
+    // [pages][kv heads][1][page][D]; boxes of 16 keys x 128 bytes, or multiples of them
+    CUtensorMap map[2];
 };
 
 __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
@@ -193,14 +196,14 @@ struct TileShape {
     static constexpr int kMT = DP / 16;                    // 16-dim blocks of O
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
-    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 256 ? 3 : 2;  // per SM
+    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? 3 : 2;  // per SM
     static constexpr bool kQRegs = NT * DP <= 256;
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
     static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
     static constexpr int kBox = 16 * kBoxBytes;
     static constexpr int kPart = kHalves * kBoxes * kBox;  // K (or V) bytes of a tile
-    static constexpr int kStages = DP * kES == 512 ? 1 : 2;
+    static constexpr int kStages = DP * kES == 512 ? 1 : NT * DP == 256 ? 3 : NT * DP <= 128 ? 1 : 2;
     static constexpr int kRing = kWarps * kStages * 2 * kPart;
     static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
     static constexpr int kMain = kRing > kMerge ? kRing : kMerge;  // the merge takes the ring's place
@@ -253,8 +256,8 @@ __device__ __forceinline__ uint64_t evict_first() {
 __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int x, int key, int head, int page, uint32_t bar,
                                          uint64_t pol) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, 0, %4, %5}], [%6], %7;"
         ::"r"(to), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(key), "r"(head), "r"(page), "r"(bar), "l"(pol) : "memory");
 }
 
@@ -313,14 +316,14 @@ struct Span {
     int n, lo, hi_all, lo_all;  // keys [lo, n) for some row, [lo_all, hi_all) for every row
     int units;
 };
-__device__ __forceinline__ Span span_of(const AttnParams& p, int n, int unit_keys) {
+__device__ __forceinline__ Span span_of(const AttnParams& p, int n, int unit_keys, int align) {
     Span s;
     s.n = n;
     s.hi_all = n - p.rows + 1;
     const int first = p.window > 0 ? s.hi_all - p.window : 0;
     s.lo = first > 0 ? first : 0;
     s.lo_all = p.window > 0 && n > p.window ? n - p.window : 0;
-    const int keys = n - (s.lo & ~15);
+    const int keys = n - (s.lo & ~(align - 1));
     s.units = keys > 0 ? (keys + unit_keys - 1) / unit_keys : 1;  // an empty item still stores its zeros
     return s;
 }
@@ -381,30 +384,57 @@ struct Parts {
     __device__ __forceinline__ int slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
 };
 
+__device__ __forceinline__ int part_bytes(const AttnParams& p) { return p.rows * p.group * (p.D * 4 + 8); }
+
 // Joins parts first, first + step, ... (`count` of them): into the output, or (to >= 0) into the
 // workspace slot `to`, which may be the first part's own: a value is read and then replaced by one
-// thread, and (m, l) only after all have read them.
-__device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, const Parts& parts, int first, int step,
-                                           int count, int to, int b, int h) {
+// thread, and (m, l) only after all have read them. Parts that fit into `room` (the rings' place) are
+// copied there all at once, so that joining costs one trip to L2; larger ones are read 8 at a time.
+__device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, char* room, int room_bytes, const Parts& parts,
+                                           int first, int step, int count, int to, int b, int h) {
     const int rows_all = p.rows * p.group, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
+    const int o_bytes = rows_all * p.D * 4, ml_bytes = rows_all * 8;
+    const bool fits = count * part_bytes(p) <= room_bytes;
+    if (fits) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(room));
+#pragma unroll 1
+        for (int c = 0; c < count; ++c) {
+            const int64_t from = static_cast<int64_t>(parts.slot(first + c * step)) * rows_all;
+            const char* const o = reinterpret_cast<const char*>(p.part_o + from * p.D);
+            const char* const ml = reinterpret_cast<const char*>(p.part_ml + from);
+            for (int i = 16 * threadIdx.x; i < o_bytes; i += 16 * blockDim.x)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + c * o_bytes + i), "l"(o + i) : "memory");
+            for (int i = 8 * threadIdx.x; i < ml_bytes; i += 8 * blockDim.x)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + count * o_bytes + c * ml_bytes + i), "l"(ml + i) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int row = threadIdx.x >> p.quad_log2; row < rows_all; row += blockDim.x >> p.quad_log2) {
         if (d >= p.D) continue;
         float* const po = p.part_o + row * p.D + d;
         Gathered a;
+        if (fits) {
+            const float2* const ml = reinterpret_cast<const float2*>(room + count * o_bytes) + row;
+            const char* const o = room + (row * p.D + d) * 4;
+#pragma unroll 4
+            for (int c = 0; c < count; ++c) a.add(ml[c * rows_all], *reinterpret_cast<const float4*>(o + c * o_bytes));
+        } else {
 #pragma unroll 1
-        for (int c = 0; c < count; c += 8) {
-            float4 v[8];
-            float2 ml[8];
+            for (int c = 0; c < count; c += 8) {
+                float4 v[8];
+                float2 ml[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int from = parts.slot(first + min(c + j, count - 1) * step) * rows_all;
-                ml[j] = __ldcg(p.part_ml + from + row);
-                v[j] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(from) * p.D));
+                for (int j = 0; j < 8; ++j) {
+                    const int from = parts.slot(first + min(c + j, count - 1) * step) * rows_all;
+                    ml[j] = __ldcg(p.part_ml + from + row);
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(from) * p.D));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < count) a.add(ml[j], v[j]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < count) a.add(ml[j], v[j]);
         }
         if (to < 0) {
             store_out(p, b, h, row, d, a);
@@ -418,38 +448,39 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, 
     for (int row = threadIdx.x; row < rows_all; row += blockDim.x) __stcg(p.part_ml + to * rows_all + row, sh.ml[row]);
 }
 
+// True in the CTA that is the last of `of` to come by `counter`, which it leaves at zero. The CTA's
+// stores come before its arrival, and the other CTAs' before what the last one reads.
 __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of) {
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        sh.last = atomicAdd(counter, 1) == of - 1;
+        int old;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+        sh.last = old == of - 1;
         if (sh.last) *counter = 0;
     }
     __syncthreads();
-    if (sh.last) __threadfence();
     return sh.last != 0;
 }
 
 // Called by every CTA that has left a part of an item in the workspace: the last of them joins the
 // parts. Many parts meet in two steps, first groups of neighbours (by the last of each), then the
 // groups. Out of line, so that its registers are not the tile loop's.
-__device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r) {
+__device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r, char* room, int room_bytes) {
     const int cta0 = cta_of(r, r.item0), parts = cta_of(r, r.item_end - 1) - cta0 + 1;
     Parts at;
     at.cta0 = cta0;
     at.slot0 = 2 * cta0 + (run_begin(r.share, r.extra, cta0) == r.item0 ? 0 : 1);
     int* const done = p.counters + static_cast<int64_t>(r.seq) * p.hk + r.head;
-    if (parts <= kJoinOnce) {
-        if (arrive_last(sh, done, parts)) join_parts(p, sh, at, 0, 1, parts, -1, r.seq, r.head);
-        return;
+    int size = parts;
+    if (parts > kJoinOnce && parts * part_bytes(p) > room_bytes) {
+        size = kJoinOnce / 2;
+        while (size * size < parts) ++size;
+        const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
+        if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.hk + at.slot(first), count)) return;
+        join_parts(p, sh, room, room_bytes, at, first, 1, count, at.slot(first), r.seq, r.head);
     }
-    int size = kJoinOnce / 2;
-    while (size * size < parts) ++size;
-    const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
-    if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.hk + at.slot(first), count)) return;
-    join_parts(p, sh, at, first, 1, count, at.slot(first), r.seq, r.head);
-    const int groups = (parts + size - 1) / size;
-    if (arrive_last(sh, done, groups)) join_parts(p, sh, at, 0, size, groups, -1, r.seq, r.head);
+    const int groups = (parts + size - 1) / size, of = size < parts ? groups : parts;
+    if (arrive_last(sh, done, of)) join_parts(p, sh, room, room_bytes, at, 0, size < parts ? size : 1, of, -1, r.seq, r.head);
 }
 
 template <int DP, int NT, bool F8>
@@ -472,7 +503,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = W / p.row_blocks;
     const int rows_all = p.rows * p.group, row0 = rb * kRowsW;
-    const int unit_keys = streams * T::kKeys;
+    const int unit_keys = streams * T::kKeys, align = p.tall_box ? T::kKeys : 16;
 
     pdl_launch_dependents();
     const uint32_t bars = static_cast<uint32_t>(__cvta_generic_to_shared(&s_bar[warp][0][0]));
@@ -487,7 +518,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         int mine = 0;
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
-            if (b < p.seqs) mine += span_of(p, length_of(p, b), unit_keys).units;
+            if (b < p.seqs) mine += span_of(p, length_of(p, b), unit_keys, align).units;
         }
         int incl = mine;
 #pragma unroll
@@ -512,7 +543,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             int b = tid * per;
             Span sp;
             for (;; ++b) {
-                sp = span_of(p, length_of(p, b), unit_keys);
+                sp = span_of(p, length_of(p, b), unit_keys, align);
                 if (begin < before + sp.units * p.hk) break;
                 before += sp.units * p.hk;
             }
@@ -534,8 +565,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (T::kStages * 2 * T::kPart);
     uint32_t cur = 0;      // the stage of the tile in work
-    uint32_t parity = 0;   // of each barrier's next phase, bit 2 * stage + which
-    uint32_t pending = 0;  // copies in flight, bits alike
+    uint32_t parity = 0;   // of the phase that the stage in work completes; the stages take turns
     bool dead = false;     // a copy did not come in time
     // offsets of this lane's pieces in a box: K's of rows g (and g + 8), V's of rows 2t and 2t + 1
     // (and 8 further). A 16-byte piece j of row r stands at piece j ^ (r & 7), in rows of 64 bytes at
@@ -549,7 +579,8 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     for (;;) {
         const int b = s_run.seq, h = s_run.head;
         const Span sp = s_run.span;
-        const int base = sp.lo & ~15;
+        // whole tiles stand in one page where pages are multiples of a tile
+        const int base = sp.lo & ~(p.tall_box ? T::kKeys - 1 : 15);
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
         const int32_t* const pages = p.table + b * p.table_stride;
 
@@ -561,6 +592,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         int next_page = ((base >> 4) + tile * H) / p.page_tiles, next_slot = ((base >> 4) + tile * H) % p.page_tiles;
         int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
         int at[H], next_at[H];          // the block's first key in its page
+        int k_taken = 0;                // the wait that failed was for V: this tile's K had come
         uint32_t bad = 0, bads = 0;     // blocks whose page id is out of range: requested tile; tiles in the ring
 
         // looks up the tile after the requested one
@@ -568,6 +600,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             int pg = next_page, sl = next_slot;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
+                if (i > 0 && p.tall_box) break;
                 next_id[i] = 0;
                 if (tl < tile_end && base + tl * T::kKeys + 16 * i < sp.n) next_id[i] = pages[pg];
                 next_at[i] = 16 * sl;
@@ -581,12 +614,13 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             bad = 0;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
+                if (i > 0 && p.tall_box) break;
                 id[i] = next_id[i];
                 at[i] = next_at[i];
                 if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
                     if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
                     id[i] = 0;
-                    bad |= 1u << i;
+                    bad |= p.tall_box ? (1u << H) - 1 : 1u << i;
                 }
             }
         };
@@ -601,17 +635,11 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 for (int i = 0; i < H; ++i)
 #pragma unroll
                     for (int x = 0; x < T::kBoxes; ++x)
-                        copy_box(to + (i * T::kBoxes + x) * T::kBox, &p.map[which], x * (T::kBoxBytes / T::kES), at[i], h, id[i], bar, pol);
+                        if ((i == 0 || !p.tall_box) && (x == 0 || !p.wide_box))
+                            copy_box(to + (i * T::kBoxes + x) * T::kBox, &p.map[which], x * (T::kBoxBytes / T::kES), at[i], h, id[i], bar, pol);
             }
-            pending |= 1u << (2 * stage + which);
         };
-        auto arrived = [&](uint32_t stage, int which) {
-            const uint32_t bit = 2 * stage + which;
-            if (!barrier_wait(bars + 8 * bit, parity >> bit & 1u, p.wait_ns)) return false;
-            parity ^= 1u << bit;
-            pending &= ~(1u << bit);
-            return true;
-        };
+        auto arrived = [&](int which) { return barrier_wait(bars + 16 * cur + 8 * which, parity, p.wait_ns); };
         // every key of the tile is there for every row
         auto whole = [&](int tl) {
             const int key = base + tl * T::kKeys;
@@ -619,30 +647,44 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         };
         look_up(tile);
 
-        // --- query rows as the scores' B operand
-        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kQ : 1];
-        float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
+        // --- query rows as the scores' B operand: loaded here, put to use behind the first requests
+        uint2 raw[NT][T::kQ];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + 8 * nt + g;
-            uint2 raw[T::kQ];
-            const int m = row / p.group;
+            const int row = row0 + 8 * nt + g, m = row / p.group;
             const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.rows + m) * p.q_ts +
                                      static_cast<int64_t>(h * p.group + row - m * p.group) * p.q_hs;
             const bool live = row < rows_all;
 #pragma unroll
             for (int i = 0; i < T::kQ; ++i) {  // 4 values each, in the order of the keys' registers
                 const int d = F8 ? 16 * (t + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (t + 4 * (i >> 1)) + 4 * (i & 1);
-                raw[i] = make_uint2(0, 0);
+                raw[nt][i] = make_uint2(0, 0);
                 if (live && d < p.D) {
                     if (p.q_vec) {
-                        raw[i] = *reinterpret_cast<const uint2*>(q + d);
+                        raw[nt][i] = *reinterpret_cast<const uint2*>(q + d);
                     } else {
                         const uint16_t* w = reinterpret_cast<const uint16_t*>(q + d);
-                        raw[i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+                        raw[nt][i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                     }
                 }
             }
+        }
+#pragma unroll
+        for (int st = 0; st < T::kStages; ++st) {
+            const int tl = tile + st * streams;
+            if (tl < tile_end && !dead) {
+                take();
+                const uint32_t stage = cur + st < T::kStages ? cur + st : cur + st - T::kStages;
+                request(stage, 0);
+                request(stage, 1);
+                bads |= bad << 8 * st;
+                look_up(tl + streams);
+            }
+        }
+        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kQ : 1];
+        float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             // The factor from scores to base-2 units is made positive (its sign goes to q), so that the
             // maximum can be taken over raw scores; a zero becomes 2^-126, or masked scores would be NaN.
             float f = p.scale * 1.4426950408889634f * kscale;
@@ -652,8 +694,8 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < T::kQ; ++i)
-                    top = max(max(max(top, raw[i].x & 0x7fffu), max(raw[i].x >> 16 & 0x7fffu, raw[i].y & 0x7fffu)),
-                              raw[i].y >> 16 & 0x7fffu);
+                    top = max(max(max(top, raw[nt][i].x & 0x7fffu), max(raw[nt][i].x >> 16 & 0x7fffu, raw[nt][i].y & 0x7fffu)),
+                              raw[nt][i].y >> 16 & 0x7fffu);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const bool plain = top == 0 || top >= 0x7f80u;
@@ -668,17 +710,17 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                     return pack_f16(v[0], v[1]);
                 };
 #pragma unroll
-                for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(narrow(raw[i].x), narrow(raw[i].y));
+                for (int i = 0; i < T::kQ; ++i) raw[nt][i] = make_uint2(narrow(raw[nt][i].x), narrow(raw[nt][i].y));
             }
             if (f < 1.1754943508e-38f) f = 1.1754943508e-38f;
 #pragma unroll
-            for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(raw[i].x ^ flip, raw[i].y ^ flip);
+            for (int i = 0; i < T::kQ; ++i) raw[nt][i] = make_uint2(raw[nt][i].x ^ flip, raw[nt][i].y ^ flip);
             zf[nt][0] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t) : f;
             zf[nt][1] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t + 4) : f;
 #pragma unroll
             for (int i = 0; i < T::kQ; ++i) {
-                if constexpr (T::kQRegs) qf[nt][i] = raw[i];
-                else if (stream == 0) s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane] = raw[i];
+                if constexpr (T::kQRegs) qf[nt][i] = raw[nt][i];
+                else if (stream == 0) s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane] = raw[nt][i];
             }
         }
         auto query = [&](int nt, int i) {
@@ -696,54 +738,64 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
-#pragma unroll
-        for (int st = 0; st < T::kStages; ++st) {
-            const int tl = tile + st * streams;
-            if (tl < tile_end && !dead) {
-                take();
-                const uint32_t stage = cur + st < T::kStages ? cur + st : cur + st - T::kStages;
-                request(stage, 0);
-                request(stage, 1);
-                bads |= bad << 8 * st;
-                look_up(tl + streams);
-            }
-        }
         for (; tile < tile_end && !dead; tile += streams) {
             // --- scores
-            if (!arrived(cur, 0)) { dead = true; break; }
+            if (!arrived(0)) { dead = true; break; }
             const uint32_t kt = ring + 2 * cur * T::kPart + k_off, vt = ring + (2 * cur + 1) * T::kPart;
             float s[H][NT][4];
+            float s2[H][NT][4];  // a second chain of sums where there would be one
+            constexpr bool kTwo = H * NT == 1;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
+            for (int i = 0; i < H; ++i)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < T::kKC; ++c) {
+                    for (int e = 0; e < 4; ++e) s[i][nt][e] = s2[i][nt][e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < T::kKC; ++c) {
+                uint4 x[H], y[H];
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
                     // piece t + 4c of rows g and g + 8
                     const uint32_t from = (kt ^ (kRow == 128 ? 64 * (c & 1) : 0)) + (i * T::kBoxes + (kRow == 128 ? c >> 1 : c)) * T::kBox;
-                    const uint4 x = lds16(from), y = lds16(from + 8 * kRow);
-                    if constexpr (F8) {
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                    x[i] = lds16(from);
+                    y[i] = lds16(from + 8 * kRow);
+                }
+                if constexpr (F8) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t a0 = e4m3x2_f16x2(xw[e]), a2 = e4m3x2_f16x2(xw[e] >> 16);
-                            const uint32_t a1 = e4m3x2_f16x2(yw[e]), a3 = e4m3x2_f16x2(yw[e] >> 16);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t a[H][4];
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 q = query(nt, 4 * c + e);
-                                mma<true>(s[i][nt], a0, a1, a2, a3, q.x, q.y);
-                            }
+                        for (int i = 0; i < H; ++i) {
+                            const uint32_t xw = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+                            const uint32_t yw = e == 0 ? y[i].x : e == 1 ? y[i].y : e == 2 ? y[i].z : y[i].w;
+                            a[i][0] = e4m3x2_f16x2(xw); a[i][2] = e4m3x2_f16x2(xw >> 16);
+                            a[i][1] = e4m3x2_f16x2(yw); a[i][3] = e4m3x2_f16x2(yw >> 16);
                         }
-                    } else {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            uint2 q = query(nt, 2 * c);
-                            mma<false>(s[i][nt], x.x, y.x, x.y, y.y, q.x, q.y);
-                            q = query(nt, 2 * c + 1);
-                            mma<false>(s[i][nt], x.z, y.z, x.w, y.w, q.x, q.y);
+                            const uint2 q = query(nt, 4 * c + e);
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                mma<true>(kTwo && (e & 1) ? s2[i][nt] : s[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], q.x, q.y);
                         }
                     }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 q = query(nt, 2 * c + e);
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                mma<false>(kTwo && e ? s2[i][nt] : s[i][nt], e ? x[i].z : x[i].x, e ? y[i].z : y[i].x,
+                                           e ? x[i].w : x[i].y, e ? y[i].w : y[i].y, q.x, q.y);
+                        }
                 }
+            }
+            if constexpr (kTwo) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[0][0][e] += s2[0][0][e];
             }
             const uint32_t bad_now = bads & 0xffu;
             const bool edge = !whole(tile) || bad_now != 0;
@@ -823,7 +875,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             }
             // --- O^T += V^T P^T. A weight of zero must also silence what is not finite: in tiles that
             // some row sees only in part, such values are taken row by row of the sequence below.
-            if (!arrived(cur, 1)) { dead = true; break; }
+            if (!arrived(1)) { dead = true; k_taken = 1; break; }
             uint32_t vr[4][T::kVW];
             auto load_v = [&](int i) {
 #pragma unroll
@@ -922,15 +974,20 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 request(cur, 1);
                 look_up(next + streams);
             }
-            cur = cur + 1 == T::kStages ? 0 : cur + 1;
+            if (++cur == T::kStages) { cur = 0; parity ^= 1; }
         }
-        if (dead) {
-            // the result is unspecified, but no copy may outlive the CTA
+        if (dead && tile < tile_end) {
+            // the result is unspecified, but no copy may outlive the CTA: what was requested and has not
+            // been waited for is K of this tile or of the one after the ring's, and all the ring's V
             if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_TIMEOUT);
 #pragma unroll 1
-            for (int i = 0; i < 2 * T::kStages; ++i)
-                if (pending >> i & 1u) barrier_wait(bars + 8 * i, parity >> i & 1u, kDrainNs);
-            pending = 0;
+            for (int st = 0; st < 2 * T::kStages; ++st) {
+                const int ahead = (st >> 1) + (st & 1 ? 0 : k_taken);  // tiles after this one
+                const uint32_t turn = cur + ahead, stage = turn % T::kStages;
+                if (tile + ahead * streams < tile_end)
+                    barrier_wait(bars + 16 * stage + 8 * (st & 1), parity ^ (turn / T::kStages & 1), kDrainNs);
+            }
+            tile = tile_end;
         }
         __syncthreads();  // every warp is through with its ring
 
@@ -973,7 +1030,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(a.m, a.l));
             }
         }
-        if (!direct) finish_item(p, s_join, s_run);
+        if (!direct) finish_item(p, s_join, s_run, reinterpret_cast<char*>(smem), T::kMain);
         if (r.last == r.end) return;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge buffer is the rings' again
         __syncthreads();  // and s_run and s_q are free
@@ -982,7 +1039,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             if (++n.head == p.hk) {
                 n.head = 0;
                 ++n.seq;
-                n.span = span_of(p, length_of(p, n.seq), unit_keys);
+                n.span = span_of(p, length_of(p, n.seq), unit_keys, align);
             }
             n.first = n.item0 = r.item_end;
             n.item_end = n.item0 + n.span.units;
@@ -1013,7 +1070,7 @@ bool plan_tile(int dim, int rows, TilePlan* out) {
     t.nt = t.dp == 256 || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     while (t.row_blocks < t.warps && 8 * t.nt * t.row_blocks < rows) t.row_blocks *= 2;
     if (8 * t.nt * t.row_blocks < rows) return false;
-    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 256 ? 3 : 2;
+    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? 3 : 2;
     *out = t;
     return true;
 }
@@ -1041,13 +1098,18 @@ nvfp4_status launch_tile(const AttnParams& a, int grid, cudaStream_t stream) {
     using T = TileShape<DP, NT, F8>;
     TileParams p;
     static_cast<AttnParams&>(p) = a;
+    p.wide_box = T::kBoxes > 1 && p.D * T::kES % T::kBoxBytes == 0;
+    p.tall_box = T::kHalves > 1 && p.page % T::kKeys == 0;
     for (int i = 0; i < 2; ++i) {
         const uint64_t row = static_cast<uint64_t>(p.D) * T::kES, page = row * p.page;
-        const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.page), static_cast<uint64_t>(p.hk),
-                                  static_cast<uint64_t>(p.pages)};
-        const uint64_t strides[3] = {row, page, p.pages > 1 ? static_cast<uint64_t>(p.page_stride[i]) * T::kES : page * p.hk};
-        const uint32_t box[4] = {T::kBoxBytes / T::kES, 16, 1, 1};
-        if (!host_encode_map(&p.map[i], F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.cache[i], dims,
+        const uint64_t piece = T::kBoxBytes / T::kES, pieces = p.wide_box ? p.D / piece : 1;
+        const uint64_t dims[5] = {p.wide_box ? piece : static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.page), pieces,
+                                  static_cast<uint64_t>(p.hk), static_cast<uint64_t>(p.pages)};
+        const uint64_t strides[4] = {row, p.wide_box ? T::kBoxBytes : row, page,
+                                     p.pages > 1 ? static_cast<uint64_t>(p.page_stride[i]) * T::kES : page * p.hk};
+        const uint32_t box[5] = {static_cast<uint32_t>(piece), static_cast<uint32_t>(p.tall_box ? T::kKeys : 16),
+                                 static_cast<uint32_t>(p.wide_box ? T::kBoxes : 1), 1, 1};
+        if (!host_encode_map(&p.map[i], F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, p.cache[i], dims,
                              strides, box, T::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
             return NVFP4_ERR_UNSUPPORTED;
     }
