@@ -4,15 +4,18 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRC = os.path.join(PKG_DIR, "csrc", "nvfp4_gemv.cu")
 OPERATORS = tuple(os.path.join(PKG_DIR, "csrc", f) for f in ("rms_norm.cu", "rope_append.cu", "paged_attention.cu"))
 HEADER = os.path.join(ROOT, "include", "nvfp4_gemv.h")
+BINDING = os.path.join(PKG_DIR, "csrc", "decode_ops_binding.cpp")
 SOURCES = (SRC, *OPERATORS, os.path.join(PKG_DIR, "csrc", "ops_common.cuh"), HEADER)
 LIB_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(LIB_DIR, "libnvfp4gemv.so")
+BINDING_PATH = os.path.join(LIB_DIR, "_decode_ops.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -35,6 +38,38 @@ def newest_source() -> float:
 
 def is_stale() -> bool:
     return not os.path.exists(LIB_PATH) or newest_source() > os.path.getmtime(LIB_PATH)
+
+
+def binding_command(out: str = BINDING_PATH) -> list:
+    """The Python module that checks the decode operators' tensors, built against the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    cuda_inc = [d for d in (os.path.join(cuda, "include"), os.path.join(cuda, "targets", "sbsa-linux", "include"),
+                            "/usr/local/cuda/include") if os.path.isdir(d)]
+    inc = [os.path.join(ROOT, "include"), os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], *cuda_inc]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{d}" for d in inc), "-o", out, BINDING, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+
+
+def binding_is_stale() -> bool:
+    return not os.path.exists(BINDING_PATH) or max(map(os.path.getmtime, (BINDING, HEADER))) > os.path.getmtime(BINDING_PATH)
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and not binding_is_stale():
+        return BINDING_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = binding_command(tmp)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def _compile(out: str, extra: tuple = (), verbose: bool = False) -> None:
@@ -62,11 +97,12 @@ def _compile(out: str, extra: tuple = (), verbose: bool = False) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if it is missing or older than its sources; return its path."""
-    if not force and not is_stale():
-        return LIB_PATH
-    os.makedirs(LIB_DIR, exist_ok=True)
-    _compile(LIB_PATH, verbose=verbose)
+    """Compile the library and the Python binding of the decode operators, where they are missing or
+    older than their sources; return the library's path."""
+    if force or is_stale():
+        os.makedirs(LIB_DIR, exist_ok=True)
+        _compile(LIB_PATH, verbose=verbose)
+    build_binding(force)
     return LIB_PATH
 
 
