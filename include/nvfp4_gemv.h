@@ -353,8 +353,8 @@ nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream)
  * sequence), or whose scores are all -inf, gives zeros and lse = -inf. Keys that a row does not
  * see never reach it, whatever they hold. A length outside [0, max_pages * page_size] or a page
  * outside [0, pages) sets NVFP4_DEV_BAD_PAGE; the length is clamped, the page's keys are not read.
- * Scores and sums are fp32; probabilities enter the tensor cores rounded to bf16 (bf16 cache) or
- * f16 (E4M3 cache).
+ * Scores and sums are fp32; weights enter the tensor cores with 16 bits (bf16 cache) or 11 (E4M3
+ * cache).
  *   workspace: nvfp4_attention_workspace_bytes(...) bytes of device memory, 256-byte aligned. Its
  *   counters must be zero before its first use and every call leaves them at zero. Calls that
  *   share a workspace must be ordered.

@@ -607,3 +607,16 @@ def test_paged_attention_wait_budget():
         nv.set_wait_budget_ns(None)
     assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, workspace=ws), want)
     assert nv.device_status() == 0
+
+
+def test_infinite_values_stay_infinite():
+    # a value of +-inf under a weight above zero makes that output +-inf, its sign kept; the rest is untouched
+    n, D = 50, 128
+    q, kc, vc, table, ln, _, _ = _attend_inputs([n], 2, 4, 2, D, BF16, 16, 31)
+    clean = nv.paged_attention(q, kc, vc, table, ln)
+    vc[int(table[0, 0]), :, 3, 5] = math.inf
+    vc[int(table[0, 1]), :, 7, 90] = -math.inf
+    got = nv.paged_attention(q, kc, vc, table, ln)
+    assert bool((got[:, :, 5] == math.inf).all()) and bool((got[:, :, 90] == -math.inf).all())
+    rest = [d for d in range(D) if d not in (5, 90)]
+    assert torch.equal(got[:, :, rest], clean[:, :, rest])
