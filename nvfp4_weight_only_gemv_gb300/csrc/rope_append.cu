@@ -36,24 +36,22 @@ struct AppendParams {
     int64_t table_stride;
     int T, hq, hk, D, half, seqs, per_seq, pages, max_pages, page;
     int norm_type, interleaved, fp8;
-    float mscale, eps;
-    int tokens_per_cta, lanes_log2;  // vector kernel
+    float mscale, eps, one_over_d;
+    int shares, lanes_log2;  // vector kernel: warps per token, lanes per head
 };
 
-// cos and sin of n * f for a whole n below 2^24. The product is taken exactly as p + e, and whole
-// turns are removed in three parts of 2 pi (Cody and Waite, "Software Manual for the Elementary
-// Functions", 1980), so the angle keeps its absolute error of about 2^-23 at every position; the
-// product alone, rounded to fp32, would be off by up to half a unit in its last place, 0.03 at
-// n f = 10^6.
+// cos and sin of n * f for a whole n below 2^24. f / pi is taken as a sum of two floats (1 / pi as
+// 0x1.45f306p-2 + 0x1.b9391p-27), n times its first part exactly as another such sum, and whole turns
+// leave that without an error, so the angle is as exact at position 10^7 as at 10: about 2^-23 off. The
+// product alone, rounded to fp32, would be off by half a unit in its last place, 0.03 at n f = 10^6.
 __device__ __forceinline__ float2 cos_sin(int n, float f) {
+    const float c1 = 0x1.45f306p-2f, c2 = 0x1.b9391p-27f;
+    const float hi = f * c1, lo = fmaf(f, c2, fmaf(f, c1, -hi));
     const float nf = static_cast<float>(n);
-    const float p = nf * f, e = fmaf(nf, f, -p);
-    const float k = rintf(p * 0.15915494f);
-    float r = fmaf(-k, 0x1.921fb6p+2f, p);
-    r = fmaf(-k, -0x1.777a5cp-23f, r);
-    r = fmaf(-k, -0x1.ee59dap-48f, r);
+    const float p = nf * hi, e = fmaf(nf, lo, fmaf(nf, hi, -p));
+    const float r = (p - 2.0f * rintf(0.5f * p)) + e;  // half turns, within one of zero
     float s, c;
-    sincosf(r + e, &s, &c);
+    sincospif(r, &s, &c);
     return make_float2(c, s);
 }
 
@@ -138,127 +136,189 @@ __global__ void __launch_bounds__(128) rope_append_scalar_kernel(const __grid_co
     }
 }
 
-// Vector kernel: a lane holds 8 values of a head as two vectors of 4, chosen so that both members of
-// each rotated pair are its own: in halves, values 4i.. and half + 4i..; interleaved, or beyond the
-// rotary part, 8 neighbours. D / 8 lanes make a head. A CTA takes a few tokens: their cosines and
-// sines are formed once, in shared memory, and serve all heads of q and k.
-constexpr int kThreads = 256;
+// Vector kernel: a lane holds 2 V values of a head as two vectors, chosen so that both members of each
+// rotated pair are its own: in halves, values V i.. and half + V i..; interleaved, or beyond the
+// rotary part, 2 V neighbours. D / (2 V) lanes make a head (V = 8: 16-byte pieces of bf16). A warp
+// takes a token, or a share of its heads where tokens are few, on its own: it forms the token's
+// cosines and sines once, keeps those of its pairs in registers, and walks through the heads of q, k
+// and v by constant steps with the next vectors on their way. (One pair after the other, the places
+// found per head, and cosines shared by a CTA behind a barrier: 8192 tokens of 32 + 8 + 8 heads took
+// 64 us; this way 39.5, 5.1 TB/s. Bound by latency: five CTAs an SM hold 40 KB of vectors in flight.)
+constexpr int kThreads = 128;
 
-__device__ __forceinline__ uint32_t pack4_e4m3(const float (&v)[4]) {
-    return pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16;
+template <typename XT, int V>
+struct Piece;  // V consecutive values as loaded
+template <int V>
+struct Piece<float, V> {
+    float4 w[V / 4];
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + 4 * i);
+    }
+    __device__ __forceinline__ void widen(float (&v)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) { v[4 * i] = w[i].x; v[4 * i + 1] = w[i].y; v[4 * i + 2] = w[i].z; v[4 * i + 3] = w[i].w; }
+    }
+};
+template <int V>
+struct Piece<__nv_bfloat16, V> {
+    uint32_t w[V / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        if constexpr (V == 8) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x; w[1] = q.y;
+        }
+    }
+    __device__ __forceinline__ void widen(float (&v)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) unpack_bf16(w[i], v[2 * i], v[2 * i + 1]);
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[V]) {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) w[i] = pack_e4m3(v[4 * i], v[4 * i + 1]) | pack_e4m3(v[4 * i + 2], v[4 * i + 3]) << 16;
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-template <typename XT>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ AppendParams p) {
-    extern __shared__ __align__(16) float2 cs[];  // [tokens_per_cta][half]
+template <typename XT, int V>
+__global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int kDepth = sizeof(XT) == 2 ? 2 : 1;   // heads requested ahead
+    extern __shared__ __align__(16) float2 cs_all[];  // [warps][half]
     pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x * (kThreads / 32) + warp;
+    const int tok = unit / p.shares, share = unit - tok * p.shares;
+    const int lanes = 1 << p.lanes_log2, hpi = 32 >> p.lanes_log2;  // heads at a time
+    const int i = lane & (lanes - 1), sub = lane >> p.lanes_log2;
+    // offsets of the lane's two vectors
+    const bool turns = V * i < p.half, halves = turns && !p.interleaved, live = 2 * V * i < p.D;
+    const int oa = halves ? V * i : 2 * V * i, ob = halves ? p.half + V * i : 2 * V * i + V;
+    // this share's steps out of the token's: those of q, then of k, then of v
+    const int sq = (p.hq + hpi - 1) >> (5 - p.lanes_log2), sk = (p.hk + hpi - 1) >> (5 - p.lanes_log2), all = sq + 2 * sk;
+    const int begin = all * share / p.shares, end = all * (share + 1) / p.shares;
     pdl_wait();
-    const int tid = threadIdx.x;
-    const int t0 = blockIdx.x * p.tokens_per_cta;
-    const int tokens = min(p.tokens_per_cta, p.T - t0);
-    const int heads = p.hq + 2 * p.hk, lanes = 1 << p.lanes_log2;
-    const int i = tid & (lanes - 1);        // lane within the head
-    const bool live = 8 * i < p.D;
-    // offsets of the lane's two vectors, and its first rotated pair (-1: none)
-    int oa = 8 * i, ob = 8 * i + 4, pair = -1;
-    if (8 * i < 2 * p.half) {
-        pair = 4 * i;
-        if (!p.interleaved) { oa = 4 * i; ob = p.half + 4 * i; }
-    }
-    for (int j = tid; j < tokens * p.half; j += kThreads) {
-        const int n = p.positions[t0 + j / p.half];
-        float2 v = cos_sin(n < 0 ? 0 : n, p.inv_freq[j % p.half]);
-        cs[j] = make_float2(v.x * p.mscale, v.y * p.mscale);
-    }
-    __syncthreads();
-    const int step = kThreads >> p.lanes_log2;  // heads at a time
-    const int first = blockIdx.y * step + (tid >> p.lanes_log2), stride = gridDim.y * step;
-    // every lane of a warp passes through every turn: the norm's shuffles need them all
-    const int turns = (tokens * heads - blockIdx.y * step + stride - 1) / stride;
-    for (int k = 0, item = first; k < turns; ++k, item += stride) {
-        const bool in = item < tokens * heads && live;
-        const int tk = in ? item / heads : 0;
-        int h = in ? item - tk * heads : 0;
-        const int t = t0 + tk;
-        const int part = h < p.hq ? 0 : h < p.hq + p.hk ? 1 : 2;
-        h -= part == 0 ? 0 : part == 1 ? p.hq : p.hq + p.hk;
-        float a[4] = {}, b[4] = {};
-        if (in) {
-            const XT* x = static_cast<const XT*>(p.x[part]) + t * p.ts[part] + h * p.hs[part];
-            load_vec(x + oa, a);
-            load_vec(x + ob, b);
+    if (tok >= p.T) return;
+    const int n = p.positions[tok];
+    float2* const cs = cs_all + warp * p.half;
+    Place at{0, 0};
+    const bool placed = end > sq && place_of(p, tok, n, at);
+    float c[V], s[V];
+    if (begin < sq + sk && p.half > 0) {
+        for (int j = lane; j < p.half; j += 32) {
+            const float2 v = cos_sin(n < 0 ? 0 : n, p.inv_freq[j]);
+            cs[j] = make_float2(v.x * p.mscale, v.y * p.mscale);
         }
-        const void* w = part == 0 ? p.q_norm : part == 1 ? p.k_norm : nullptr;
-        if (p.q_norm || p.k_norm) {
-            float sum = 0.0f;
+        __syncwarp();
+        if (turns) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum = fmaf(a[e], a[e], fmaf(b[e], b[e], sum));
-            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (w && in) {
-                const float rstd = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-                float wa[4], wb[4];
-                if (p.norm_type == NVFP4_F32) {
-                    load_vec(static_cast<const float*>(w) + oa, wa);
-                    load_vec(static_cast<const float*>(w) + ob, wb);
-                } else {
-                    load_vec(static_cast<const __nv_bfloat16*>(w) + oa, wa);
-                    load_vec(static_cast<const __nv_bfloat16*>(w) + ob, wb);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { a[e] *= rstd * wa[e]; b[e] *= rstd * wb[e]; }
+            for (int e = 0; e < V; e += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(cs + V * i + e);
+                c[e] = v.x; s[e] = v.y; c[e + 1] = v.z; s[e + 1] = v.w;
             }
         }
-        if (!in) continue;
-        if (part < 2 && pair >= 0) {
-            float2 r[4];
+    }
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float4 v = *reinterpret_cast<const float4*>(cs + tk * p.half + pair + e);
-                r[e] = make_float2(v.x, v.y);
-                r[e + 1] = make_float2(v.z, v.w);
-            }
-            if (p.interleaved) {
-                auto turn = [](float& u, float& v, float2 c) {
-                    const float x = u * c.x - v * c.y;
-                    v = v * c.x + u * c.y;
-                    u = x;
-                };
-                turn(a[0], a[1], r[0]); turn(a[2], a[3], r[1]); turn(b[0], b[1], r[2]); turn(b[2], b[3], r[3]);
+    for (int part = 0; part < 3; ++part) {
+        const int first = part == 0 ? 0 : part == 1 ? sq : sq + sk, heads = part == 0 ? p.hq : p.hk;
+        const int from = max(begin, first), to = min(end, first + (part == 0 ? sq : sk));
+        if (from >= to || (part > 0 && !placed)) continue;
+        int h = (from - first) * hpi + sub;
+        const XT* x = static_cast<const XT*>(p.x[part]) + tok * p.ts[part] + h * p.hs[part];
+        const int64_t x_step = hpi * p.hs[part];
+        const void* const w = part == 0 ? p.q_norm : part == 1 ? p.k_norm : nullptr;
+        // lanes beyond the head hold zeros throughout: the norm's sum counts on it
+        Piece<XT, V> na[kDepth], nb[kDepth];
+        int ahead = h;
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d, ahead += hpi, x += x_step) {
+            na[d] = nb[d] = Piece<XT, V>{};
+            if (live && ahead < heads) { na[d].load(x + oa); nb[d].load(x + ob); }
+        }
+        float wa[V], wb[V];
+        if (part < 2 && w && live) {
+            if (p.norm_type == NVFP4_F32) {
+                Piece<float, V> q;
+                q.load(static_cast<const float*>(w) + oa); q.widen(wa);
+                q.load(static_cast<const float*>(w) + ob); q.widen(wb);
             } else {
+                Piece<__nv_bfloat16, V> q;
+                q.load(static_cast<const __nv_bfloat16*>(w) + oa); q.widen(wa);
+                q.load(static_cast<const __nv_bfloat16*>(w) + ob); q.widen(wb);
+            }
+        }
+        // the head's row in the output or the cache, bytes
+        const int64_t between = part == 0 ? p.D : static_cast<int64_t>(p.page) * p.D;
+        const int64_t row = (part == 0 ? static_cast<int64_t>(tok) * p.hq * p.D
+                                       : at.page * p.page_stride[part - 1] + static_cast<int64_t>(at.slot) * p.D) + h * between;
+        const int y_size = part > 0 && p.fp8 ? 1 : 2;
+        char* y = (part == 0 ? reinterpret_cast<char*>(p.q_out) : static_cast<char*>(p.cache[part - 1])) + row * y_size;
+        const int64_t y_step = hpi * between * y_size;
+        auto head = [&](Piece<XT, V>& ra, Piece<XT, V>& rb) {
+            float a[V], b[V];
+            ra.widen(a);
+            rb.widen(b);
+            if (live && ahead < heads) { ra.load(x + oa); rb.load(x + ob); }
+            ahead += hpi;
+            x += x_step;
+            if (part < 2 && w) {
+                float sum = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = a[e] * r[e].x - b[e] * r[e].y;
-                    b[e] = b[e] * r[e].x + a[e] * r[e].y;
-                    a[e] = x;
+                for (int e = 0; e < V; ++e) sum = fmaf(a[e], a[e], fmaf(b[e], b[e], sum));
+                for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float rstd = rsqrtf(fmaf(sum, p.one_over_d, p.eps));
+#pragma unroll
+                for (int e = 0; e < V; ++e) { a[e] *= rstd * wa[e]; b[e] *= rstd * wb[e]; }
+            }
+            if (part < 2 && turns) {
+                if (halves) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float u = a[e] * c[e] - b[e] * s[e];
+                        b[e] = b[e] * c[e] + a[e] * s[e];
+                        a[e] = u;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float* const u = 2 * e < V ? a + 2 * e : b + 2 * e - V;
+                        const float v = u[0] * c[e] - u[1] * s[e];
+                        u[1] = u[1] * c[e] + u[0] * s[e];
+                        u[0] = v;
+                    }
                 }
             }
-        }
-        const int n = p.positions[t];
-        if (part == 0) {
-            if (n < 0) {
+            if (part == 0 && n < 0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a[e] = b[e] = 0.0f;
+                for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
             }
-            __nv_bfloat16* to = p.q_out + (static_cast<int64_t>(t) * p.hq + h) * p.D;
-            store_vec(to + oa, a);
-            store_vec(to + ob, b);
-            continue;
-        }
-        Place at;
-        if (!place_of(p, t, n, at)) continue;
-        const int64_t to = at.page * p.page_stride[part - 1] + (static_cast<int64_t>(h) * p.page + at.slot) * p.D;
-        if (p.fp8) {
-            const float* sc = p.cache_scale[part - 1];
-            const float s = sc ? sc[h] : 1.0f;
+            if (live && h < heads) {
+                if (part > 0 && p.fp8) {
+                    const float* const sc = p.cache_scale[part - 1];
+                    const float inv = sc ? 1.0f / sc[h] : 1.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { a[e] /= s; b[e] /= s; }
-            uint8_t* c = static_cast<uint8_t*>(p.cache[part - 1]) + to;
-            *reinterpret_cast<uint32_t*>(c + oa) = pack4_e4m3(a);
-            *reinterpret_cast<uint32_t*>(c + ob) = pack4_e4m3(b);
-        } else {
-            __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.cache[part - 1]) + to;
-            store_vec(c + oa, a);
-            store_vec(c + ob, b);
+                    for (int e = 0; e < V; ++e) { a[e] *= inv; b[e] *= inv; }
+                    store_codes(reinterpret_cast<uint8_t*>(y) + oa, a);
+                    store_codes(reinterpret_cast<uint8_t*>(y) + ob, b);
+                } else {
+                    store_vec(reinterpret_cast<__nv_bfloat16*>(y) + oa, a);
+                    store_vec(reinterpret_cast<__nv_bfloat16*>(y) + ob, b);
+                }
+            }
+            h += hpi;
+            y += y_step;
+        };
+        for (int k = from; k < to; k += kDepth) {
+            head(na[0], nb[0]);
+            if constexpr (kDepth > 1) {
+                if (k + 1 < to) head(na[1], nb[1]);
+            }
         }
     }
 }
@@ -310,24 +370,35 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
     p.norm_type = a->norm_type; p.interleaved = a->interleaved; p.fp8 = a->cache_type == NVFP4_E4M3;
     p.mscale = a->mscale; p.eps = a->eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Vectors of 4 values: 8-byte pieces of bf16, 16-byte pieces of fp32, 4-byte pieces of codes.
-    const int xb = a->x_type == NVFP4_F32 ? 16 : 8, nb = p.norm_type == NVFP4_F32 ? 16 : 8;
-    const int cb = p.fp8 ? 4 : 8;
-    bool vec = p.D % 8 == 0 && p.D <= 256 && p.half % 4 == 0 && aligned(p.q_out, 8) && aligned(p.q_norm, nb) &&
-               aligned(p.k_norm, nb);
-    for (int i = 0; i < 3; ++i) vec = vec && aligned(p.x[i], xb) && p.ts[i] % 4 == 0 && p.hs[i] % 4 == 0;
-    for (int i = 0; i < 2; ++i) vec = vec && aligned(p.cache[i], cb) && p.page_stride[i] % 4 == 0;
-    if (vec && host_variant() != 1) {
-        while ((8 << p.lanes_log2) < p.D) ++p.lanes_log2;
-        const int step = kThreads >> p.lanes_log2, heads = p.hq + 2 * p.hk, sms = host_sm_count();
-        // Few tokens: one a CTA, its heads over several CTAs. Many: 4 a CTA share one barrier.
-        p.tokens_per_cta = p.T >= 8 * sms ? 4 : 1;
-        const int groups = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
-        int parts = p.T >= 2 * sms ? 1 : (heads + step - 1) / step;
-        const dim3 grid(groups, parts);
-        const size_t smem = static_cast<size_t>(p.tokens_per_cta) * p.half * sizeof(float2);
-        return a->x_type == NVFP4_F32 ? launch(rope_append_kernel<float>, grid, dim3(kThreads), smem, st, p)
-                                      : launch(rope_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), smem, st, p);
+    p.one_over_d = 1.0f / static_cast<float>(p.D);
+    // Whole vectors of V values on their boundaries, for V = 8, then 4; else a value per thread.
+    const int eb = type_bytes(a->x_type), nb = type_bytes(p.norm_type), cb = p.fp8 ? 1 : 2;
+    auto fits = [&](int v) {
+        auto on = [&](const void* q, int bytes) { return aligned(q, bytes < 16 ? bytes : 16); };
+        bool ok = p.D % (2 * v) == 0 && p.D <= 32 * 2 * v && p.half % v == 0 && on(p.q_out, 2 * v) && on(p.q_norm, nb * v) &&
+                  on(p.k_norm, nb * v);
+        for (int i = 0; i < 3; ++i) ok = ok && on(p.x[i], eb * v) && p.ts[i] % v == 0 && p.hs[i] % v == 0;
+        for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;
+        return ok;
+    };
+    const int v = host_variant() == 1 ? 0 : fits(8) ? 8 : fits(4) ? 4 : 0;
+    if (v) {
+        while ((2 * v << p.lanes_log2) < p.D) ++p.lanes_log2;
+        // A token's heads are shared among warps, down to one step each, until the SMs' warps are filled twice
+        // (8192 tokens, a warp each: 39.5 us; two warps each: 42.9; four: 44.5).
+        const int hpi = 32 >> p.lanes_log2, steps = (p.hq + hpi - 1) / hpi + 2 * ((p.hk + hpi - 1) / hpi);
+        const int64_t want = (40ll * host_sm_count() + p.T - 1) / p.T;
+        p.shares = static_cast<int>(want < 1 ? 1 : want < steps ? want : steps);
+        const int warps = kThreads / 32;
+        const int64_t ctas = (static_cast<int64_t>(p.T) * p.shares + warps - 1) / warps;
+        const dim3 grid(static_cast<unsigned>(ctas));
+        const size_t smem = static_cast<size_t>(warps) * p.half * sizeof(float2);
+        const bool f32 = a->x_type == NVFP4_F32;
+        if (v == 8)
+            return f32 ? launch(rope_append_kernel<float, 8>, grid, dim3(kThreads), smem, st, p)
+                       : launch(rope_append_kernel<__nv_bfloat16, 8>, grid, dim3(kThreads), smem, st, p);
+        return f32 ? launch(rope_append_kernel<float, 4>, grid, dim3(kThreads), smem, st, p)
+                   : launch(rope_append_kernel<__nv_bfloat16, 4>, grid, dim3(kThreads), smem, st, p);
     }
     const dim3 grid(p.T, p.hq + 2 * p.hk);
     return a->x_type == NVFP4_F32 ? launch(rope_append_scalar_kernel<float>, grid, dim3(128), p.D * 4, st, p)
