@@ -44,7 +44,6 @@ struct AttnParams {
     int page_tiles;             // 16-key blocks per page
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
     uint64_t wait_ns;           // budget of a wait for a copy
-    int min_units;              // units of work a CTA takes at least
     int q_vec;                  // q may be read 8 bytes at a time
 };
 
@@ -82,6 +81,7 @@ constexpr int kScalarWarps = 4;
 constexpr float kTiny = 7.52316385e-37f;  // 2^-120
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
 constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr int kAlignSlack = 3;  // units
 constexpr int kJoinOnce = 16;  // parts that one CTA joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
@@ -345,6 +345,7 @@ struct Run {
     int seq, head;                  // the item
     int item0, item_end;            // its units
     int first, last;                // the run's part of it
+    int cta0, parts, slot0;         // the CTAs that have a part of it: first, how many, the first's slot
     Span span;
 };
 
@@ -352,6 +353,26 @@ __device__ __forceinline__ int run_begin(int share, int extra, int cta) { return
 __device__ __forceinline__ int cta_of(const Run& r, int unit) {
     const int long_units = r.extra * (r.share + 1);
     return unit < long_units ? unit / (r.share + 1) : r.extra + (unit - long_units) / r.share;
+}
+// The item's CTAs where every CTA takes an equal run. The first one's part is its second segment unless
+// its run begins with the item.
+__device__ __forceinline__ void find_parts(Run& r) {
+    r.cta0 = cta_of(r, r.item0);
+    r.parts = cta_of(r, r.item_end - 1) - r.cta0 + 1;
+    r.slot0 = 2 * r.cta0 + (run_begin(r.share, r.extra, r.cta0) == r.item0 ? 0 : 1);
+}
+// Where the run starts: in sequence b, whose heads' units begin at `before`.
+__device__ __forceinline__ void enter_run(Run& r, int b, int before, const Span& sp, int cta) {
+    r.begin = run_begin(r.share, r.extra, cta);
+    r.end = run_begin(r.share, r.extra, cta + 1);
+    r.seq = b;
+    r.span = sp;
+    r.head = (r.begin - before) / sp.units;
+    r.item0 = before + r.head * sp.units;
+    r.item_end = r.item0 + sp.units;
+    r.first = r.begin;
+    r.last = min(r.item_end, r.end);
+    find_parts(r);
 }
 
 // Four values of a row gathered from parts, one part after the other.
@@ -386,8 +407,7 @@ struct JoinShared {
     int last;
 };
 
-// The parts of an item, as slots of the workspace in the CTAs' order. The first CTA's part is its
-// second segment unless its run begins with the item.
+// The parts of an item, as slots of the workspace in the CTAs' order.
 struct Parts {
     int slot0, cta0;
     __device__ __forceinline__ int slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
@@ -475,10 +495,8 @@ __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of
 // parts. Many parts meet in two steps, first groups of neighbours (by the last of each), then the
 // groups. Out of line, so that its registers are not the tile loop's.
 __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r, char* room, int room_bytes) {
-    const int cta0 = cta_of(r, r.item0), parts = cta_of(r, r.item_end - 1) - cta0 + 1;
-    Parts at;
-    at.cta0 = cta0;
-    at.slot0 = 2 * cta0 + (run_begin(r.share, r.extra, cta0) == r.item0 ? 0 : 1);
+    const int cta0 = r.cta0, parts = r.parts;
+    const Parts at{r.slot0, cta0};
     int* const done = p.counters + static_cast<int64_t>(r.seq) * p.hk + r.head;
     int size = parts;
     if (parts > kJoinOnce && parts * part_bytes(p) > room_bytes) {
@@ -521,8 +539,70 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map[tid])) : "memory");
     pdl_wait();
 
-    // --- the CTA's run of units: prefix sums of the sequences' unit counts
-    {
+    // --- the CTA's part of the work. All (sequence, kv head) items lie end to end in units; a CTA takes
+    // an equal run of them, or, where that costs little, an equal part of a single item, which
+    // saves it a second start and a second join (worth about kAlignSlack units).
+    Run run;
+    const int cta = blockIdx.x, grid = gridDim.x;
+    if (p.seqs <= 32) {
+        // every warp for itself, a sequence per lane
+        Span sp{};
+        if (lane < p.seqs) sp = span_of(p, length_of(p, lane), unit_keys, align);
+        auto prefix = [&](int v) {  // inclusive
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += w;
+            }
+            return v;
+        };
+        const int incl = prefix(sp.units), total = __shfl_sync(0xffffffffu, incl, 31) * p.hk;
+        const int least = (total + grid - 1) / grid;
+        int n = 0, before = 0;  // CTAs of an item of this lane's sequence; CTAs or units before the sequence
+        bool whole_items = false;
+        for (int load = least; load <= least + kAlignSlack && !whole_items; ++load) {
+            n = (sp.units + load - 1) / load;
+            whole_items = __reduce_add_sync(0xffffffffu, n) * p.hk <= grid;
+        }
+        bool here;
+        if (whole_items) {
+            before = (prefix(n) - n) * p.hk;
+            here = cta >= before && cta < before + n * p.hk;
+        } else {
+            run.share = total / grid;  // more units than CTAs, or a unit per CTA would have done
+            run.extra = total - run.share * grid;
+            before = (incl - sp.units) * p.hk;
+            const int begin = run_begin(run.share, run.extra, cta);
+            here = begin >= before && begin < before + sp.units * p.hk;
+        }
+        const uint32_t owner = __ballot_sync(0xffffffffu, here);
+        if (owner == 0) return;
+        const int b = __ffs(owner) - 1;
+        n = __shfl_sync(0xffffffffu, n, b);
+        before = __shfl_sync(0xffffffffu, before, b);
+        Span at;
+        at.n = __shfl_sync(0xffffffffu, sp.n, b);
+        at.lo = __shfl_sync(0xffffffffu, sp.lo, b);
+        at.hi_all = __shfl_sync(0xffffffffu, sp.hi_all, b);
+        at.lo_all = __shfl_sync(0xffffffffu, sp.lo_all, b);
+        at.units = __shfl_sync(0xffffffffu, sp.units, b);
+        if (whole_items) {
+            run.seq = b;
+            run.span = at;
+            run.head = (cta - before) / n;
+            run.cta0 = before + run.head * n;
+            run.parts = n;
+            run.slot0 = 2 * run.cta0;
+            const int part = cta - run.cta0, even = at.units / n, odd = at.units - even * n;
+            run.item0 = 0;
+            run.item_end = at.units;
+            run.begin = run.first = run_begin(even, odd, part);
+            run.end = run.last = run_begin(even, odd, part + 1);
+        } else {
+            enter_run(run, b, before, at, cta);
+        }
+        if (tid == 0) s_run = run;
+    } else {
         const int per = (p.seqs + kThreads - 1) / kThreads;
         int mine = 0;
         for (int i = 0; i < per; ++i) {
@@ -543,10 +623,11 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             total += s_scan[i];
         }
         total *= p.hk;
-        const int ctas = min(max(total / p.min_units, 1), static_cast<int>(gridDim.x));
-        if (static_cast<int>(blockIdx.x) >= ctas) return;
-        const int share = total / ctas, extra = total - share * ctas;
-        const int begin = run_begin(share, extra, blockIdx.x);
+        const int ctas = min(total, grid);
+        if (cta >= ctas) return;
+        run.share = total / ctas;
+        run.extra = total - run.share * ctas;
+        const int begin = run_begin(run.share, run.extra, cta);
         before *= p.hk;
         if (begin >= before && begin < before + mine * p.hk) {
             int b = tid * per;
@@ -556,20 +637,11 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 if (begin < before + sp.units * p.hk) break;
                 before += sp.units * p.hk;
             }
-            Run& r = s_run;
-            r.share = share;
-            r.extra = extra;
-            r.begin = begin;
-            r.end = run_begin(share, extra, blockIdx.x + 1);
-            r.seq = b;
-            r.head = (begin - before) / sp.units;
-            r.item0 = before + r.head * sp.units;
-            r.item_end = r.item0 + sp.units;
-            r.first = begin;
-            r.last = min(r.item_end, r.end);
-            r.span = sp;
+            enter_run(run, b, before, sp, cta);
+            s_run = run;
         }
         __syncthreads();
+        run = s_run;
     }
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (T::kStages * 2 * T::kPart);
@@ -586,8 +658,8 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         kRow == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4) : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8};
 
     for (;;) {
-        const int b = s_run.seq, h = s_run.head;
-        const Span sp = s_run.span;
+        const int b = run.seq, h = run.head;
+        const Span sp = run.span;
         // whole tiles stand in one page where pages are multiples of a tile
         const int base = sp.lo & ~(p.tall_box ? T::kKeys - 1 : 15);
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
@@ -595,8 +667,8 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
 
         // --- tiles of this warp: stream, stream + streams, ... of the run. A tile's first 16-key block
         // stands at block `slot` of the sequence's page `page`; both walk along with the tiles.
-        const int tile_end = (s_run.last - s_run.item0) * streams;
-        int tile = (s_run.first - s_run.item0) * streams + stream;
+        const int tile_end = (run.last - run.item0) * streams;
+        int tile = (run.first - run.item0) * streams + stream;
         const int step_page = streams * H / p.page_tiles, step_slot = streams * H % p.page_tiles;
         int next_page = ((base >> 4) + tile * H) / p.page_tiles, next_slot = ((base >> 4) + tile * H) % p.page_tiles;
         int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
@@ -1031,7 +1103,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             }
         __syncthreads();
         const Run r = s_run;
-        const bool direct = r.first == r.item0 && r.last == r.item_end;
+        const bool direct = r.parts == 1;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1);
         const int d = 4 * (tid & ((1 << p.quad_log2) - 1));
 #pragma unroll 1
@@ -1064,8 +1136,10 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             n.first = n.item0 = r.item_end;
             n.item_end = n.item0 + n.span.units;
             n.last = min(n.item_end, n.end);
+            find_parts(n);
         }
         __syncthreads();
+        run = s_run;
     }
 }
 
@@ -1215,7 +1289,6 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         p.wait_ns = host_wait_ns();
         while ((4 << p.quad_log2) < p.D) ++p.quad_log2;
         p.page_tiles = p.page / 16;
-        p.min_units = 1;
         p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         return p.fp8 ? dispatch_tile<true>(t, p, grid, st) : dispatch_tile<false>(t, p, grid, st);
