@@ -40,6 +40,9 @@ struct AttnParams {
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
     int wide_box, tall_box;     // one copy brings all of a block's boxes; all blocks of a tile
+    // A kv head's query rows are taken in `chunks` equal chunks of `chunk_rows` (the last may hold fewer),
+    // one where a CTA can hold them all; a (kv head, chunk) is a column of a sequence's items.
+    int chunks, chunk_rows, columns;
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
     int page_tiles;             // 16-key blocks per page
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
@@ -82,7 +85,7 @@ constexpr float kTiny = 7.52316385e-37f;  // 2^-120
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kAlignSlack = 3;  // units
-constexpr int kJoinOnce = 16;  // parts that one CTA joins in a single step
+constexpr int kJoinOnce = 32;  // parts times rows that a thread joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
 // any page size, any alignment.
@@ -385,14 +388,19 @@ struct Gathered {
         m = top;
         l *= keep;
         o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+        if (f != 0.0f) l = fmaf(ml.y, f, l);
+        weigh(f, v);
+    }
+    __device__ __forceinline__ void weigh(float f, float4 v) {
         if (f == 0.0f) return;  // nothing, not even 0 * NaN
-        l = fmaf(ml.y, f, l);
         o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y);
         o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
     }
 };
 
-__device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int row, int d, const Gathered& a) {
+__device__ __forceinline__ void store_out(const AttnParams& p, int b, int column, int chunk_row, int d, const Gathered& a) {
+    const int h = p.chunks == 1 ? column : column / p.chunks, row = (column - h * p.chunks) * p.chunk_rows + chunk_row;
+    if (row >= p.rows * p.group) return;  // the last chunk's padding
     const int m = row / p.group, head = h * p.group + row - m * p.group;
     const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
     const float inv = a.l == 0.0f ? 0.0f : (p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f) / a.l;
@@ -401,9 +409,9 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
     if (d == 0 && p.lse) p.lse[at] = a.l == 0.0f ? -INFINITY : (a.m + log2f(a.l)) * 0.6931471805599453f;
 }
 
-constexpr int kMaxTileRows = 128;  // query rows per kv head that any tile plan takes
+constexpr int kMaxChunkRows = 128;  // query rows of a CTA in any plan
 struct JoinShared {
-    float2 ml[kMaxTileRows];
+    float2 ml[kMaxChunkRows];
     int last;
 };
 
@@ -413,17 +421,25 @@ struct Parts {
     __device__ __forceinline__ int slot(int c) const { return c == 0 ? slot0 : 2 * (cta0 + c); }
 };
 
-__device__ __forceinline__ int part_bytes(const AttnParams& p) { return p.rows * p.group * (p.D * 4 + 8); }
+__device__ __forceinline__ int part_bytes(const AttnParams& p) { return p.chunk_rows * (p.D * 4 + 8); }
+
+// How many rows of a part a thread joins, one after the other.
+__device__ __forceinline__ int join_turns(const AttnParams& p) {
+    const int at_a_time = blockDim.x >> p.quad_log2;
+    return (p.chunk_rows + at_a_time - 1) / at_a_time;
+}
 
 // Joins parts first, first + step, ... (`count` of them): into the output, or (to >= 0) into the
 // workspace slot `to`, which may be the first part's own: a value is read and then replaced by one
-// thread, and (m, l) only after all have read them. Parts that fit into `room` (the rings' place) are
-// copied there all at once, so that joining costs one trip to L2; larger ones are read 8 at a time.
+// thread, and (m, l) only after all have read them. A thread reads 8 parts of a row at a time; where it
+// has several rows, and the parts fit into `room` (the rings' place), they are copied there all at
+// once instead, one trip to L2 for all rows. (One row a thread: 16 parts in 9.4 us a call against 9.9 through
+// shared memory; four rows: 25 against 20.)
 __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, char* room, int room_bytes, const Parts& parts,
                                            int first, int step, int count, int to, int b, int h) {
-    const int rows_all = p.rows * p.group, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
+    const int rows_all = p.chunk_rows, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
     const int o_bytes = rows_all * p.D * 4, ml_bytes = rows_all * 8;
-    const bool fits = count * part_bytes(p) <= room_bytes;
+    const bool fits = join_turns(p) > 1 && count * part_bytes(p) <= room_bytes;
     if (fits) {
         const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(room));
 #pragma unroll 1
@@ -497,13 +513,13 @@ __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of
 __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r, char* room, int room_bytes) {
     const int cta0 = r.cta0, parts = r.parts;
     const Parts at{r.slot0, cta0};
-    int* const done = p.counters + static_cast<int64_t>(r.seq) * p.hk + r.head;
+    int* const done = p.counters + static_cast<int64_t>(r.seq) * p.columns + r.head;
     int size = parts;
-    if (parts > kJoinOnce && parts * part_bytes(p) > room_bytes) {
-        size = kJoinOnce / 2;
+    if (parts > 4 && parts * join_turns(p) > kJoinOnce && (join_turns(p) == 1 || parts * part_bytes(p) > room_bytes)) {
+        size = 3;
         while (size * size < parts) ++size;
         const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
-        if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.hk + at.slot(first), count)) return;
+        if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.columns + at.slot(first), count)) return;
         join_parts(p, sh, room, room_bytes, at, first, 1, count, at.slot(first), r.seq, r.head);
     }
     const int groups = (parts + size - 1) / size, of = size < parts ? groups : parts;
@@ -529,7 +545,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = W / p.row_blocks;
-    const int rows_all = p.rows * p.group, row0 = rb * kRowsW;
+    const int rows_all = p.rows * p.group;
     const int unit_keys = streams * T::kKeys, align = p.tall_box ? T::kKeys : 16;
 
     pdl_launch_dependents();
@@ -556,24 +572,24 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             }
             return v;
         };
-        const int incl = prefix(sp.units), total = __shfl_sync(0xffffffffu, incl, 31) * p.hk;
+        const int incl = prefix(sp.units), total = __shfl_sync(0xffffffffu, incl, 31) * p.columns;
         const int least = (total + grid - 1) / grid;
         int n = 0, before = 0;  // CTAs of an item of this lane's sequence; CTAs or units before the sequence
         bool whole_items = false;
         for (int load = least; load <= least + kAlignSlack && !whole_items; ++load) {
             n = (sp.units + load - 1) / load;
-            whole_items = __reduce_add_sync(0xffffffffu, n) * p.hk <= grid;
+            whole_items = __reduce_add_sync(0xffffffffu, n) * p.columns <= grid;
         }
         bool here;
         if (whole_items) {
-            before = (prefix(n) - n) * p.hk;
-            here = cta >= before && cta < before + n * p.hk;
+            before = (prefix(n) - n) * p.columns;
+            here = cta >= before && cta < before + n * p.columns;
         } else {
             run.share = total / grid;  // more units than CTAs, or a unit per CTA would have done
             run.extra = total - run.share * grid;
-            before = (incl - sp.units) * p.hk;
+            before = (incl - sp.units) * p.columns;
             const int begin = run_begin(run.share, run.extra, cta);
-            here = begin >= before && begin < before + sp.units * p.hk;
+            here = begin >= before && begin < before + sp.units * p.columns;
         }
         const uint32_t owner = __ballot_sync(0xffffffffu, here);
         if (owner == 0) return;
@@ -622,20 +638,20 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             if (i < warp) before += s_scan[i];
             total += s_scan[i];
         }
-        total *= p.hk;
+        total *= p.columns;
         const int ctas = min(total, grid);
         if (cta >= ctas) return;
         run.share = total / ctas;
         run.extra = total - run.share * ctas;
         const int begin = run_begin(run.share, run.extra, cta);
-        before *= p.hk;
-        if (begin >= before && begin < before + mine * p.hk) {
+        before *= p.columns;
+        if (begin >= before && begin < before + mine * p.columns) {
             int b = tid * per;
             Span sp;
             for (;; ++b) {
                 sp = span_of(p, length_of(p, b), unit_keys, align);
-                if (begin < before + sp.units * p.hk) break;
-                before += sp.units * p.hk;
+                if (begin < before + sp.units * p.columns) break;
+                before += sp.units * p.columns;
             }
             enter_run(run, b, before, sp, cta);
             s_run = run;
@@ -658,7 +674,9 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         kRow == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4) : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8};
 
     for (;;) {
-        const int b = run.seq, h = run.head;
+        const int b = run.seq, h = p.chunks == 1 ? run.head : run.head / p.chunks;
+        const int row0 = (run.head - h * p.chunks) * p.chunk_rows + rb * kRowsW;  // this warp's first query row
+        const int rows_end = min(rows_all, (run.head - h * p.chunks + 1) * p.chunk_rows);
         const Span sp = run.span;
         // whole tiles stand in one page where pages are multiples of a tile
         const int base = sp.lo & ~(p.tall_box ? T::kKeys - 1 : 15);
@@ -735,7 +753,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             const int row = row0 + 8 * nt + g, m = row / p.group;
             const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.rows + m) * p.q_ts +
                                      static_cast<int64_t>(h * p.group + row - m * p.group) * p.q_hs;
-            const bool live = row < rows_all;
+            const bool live = row < rows_end;
 #pragma unroll
             for (int i = 0; i < T::kQ; ++i) {  // 4 values each, in the order of the keys' registers
                 const int d = F8 ? 16 * (t + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (t + 4 * (i >> 1)) + 4 * (i & 1);
@@ -894,7 +912,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int row = row0 + 8 * nt + 2 * t + c;
-                        const int hi = row < rows_all ? sp.hi_all + row / p.group : 0, lo = p.window > 0 ? hi - p.window : 0;
+                        const int hi = row < rows_end ? sp.hi_all + row / p.group : 0, lo = p.window > 0 ? hi - p.window : 0;
 #pragma unroll
                         for (int i = 0; i < H; ++i)
 #pragma unroll
@@ -1107,7 +1125,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1);
         const int d = 4 * (tid & ((1 << p.quad_log2) - 1));
 #pragma unroll 1
-        for (int row = tid >> p.quad_log2; row < rows_all; row += kThreads >> p.quad_log2) {
+        for (int row = tid >> p.quad_log2; row < p.chunk_rows; row += kThreads >> p.quad_log2) {
             if (d >= p.D) continue;
             Gathered a;
 #pragma unroll 1
@@ -1118,8 +1136,8 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             if (direct) {
                 store_out(p, r.seq, r.head, row, d, a);
             } else {
-                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * rows_all + row) * p.D + d), a.o);
-                if (d == 0) __stcg(p.part_ml + slot * rows_all + row, make_float2(a.m, a.l));
+                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * p.chunk_rows + row) * p.D + d), a.o);
+                if (d == 0) __stcg(p.part_ml + slot * p.chunk_rows + row, make_float2(a.m, a.l));
             }
         }
         if (!direct) finish_item(p, s_join, s_run, reinterpret_cast<char*>(smem), T::kMain);
@@ -1128,7 +1146,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         __syncthreads();  // and s_run and s_q are free
         if (tid == 0) {
             Run& n = s_run;
-            if (++n.head == p.hk) {
+            if (++n.head == p.columns) {
                 n.head = 0;
                 ++n.seq;
                 n.span = span_of(p, length_of(p, n.seq), unit_keys, align);
@@ -1155,15 +1173,18 @@ const bool g_registered = register_status(read_status);
 // padded to 64, 128 or 256 in registers, rows to blocks of 8 NT times the warps that share a tile.
 struct TilePlan {
     int dp = 0, nt = 1, row_blocks = 1, ctas_per_sm = 1, warps = 4;
+    int chunks = 1, chunk_rows = 0;  // of a kv head's query rows
 };
 bool plan_tile(int dim, int rows, TilePlan* out) {
     TilePlan t;
     if (dim > 256 || rows < 1) return false;
     t.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
     t.warps = t.dp == 256 ? 8 : 4;
-    t.nt = t.dp == 256 || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    while (t.row_blocks < t.warps && 8 * t.nt * t.row_blocks < rows) t.row_blocks *= 2;
-    if (8 * t.nt * t.row_blocks < rows) return false;
+    const int most = 8 * (t.dp == 256 ? 1 : 4) * t.warps;  // rows of a CTA
+    t.chunks = (rows + most - 1) / most;
+    t.chunk_rows = (rows + t.chunks - 1) / t.chunks;
+    t.nt = t.dp == 256 || t.chunk_rows <= 8 ? 1 : t.chunk_rows <= 16 ? 2 : 4;
+    while (8 * t.nt * t.row_blocks < t.chunk_rows) t.row_blocks *= 2;
     t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? 3 : 2;
     *out = t;
     return true;
@@ -1174,11 +1195,11 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 struct Workspace {
     int64_t part_o, part_ml, bytes;
 };
-Workspace workspace_of(int grid, int seqs, int rows_all, int kv_heads, int dim) {
+Workspace workspace_of(const TilePlan& t, int grid, int seqs, int kv_heads, int dim) {
     Workspace w;
-    w.part_o = align256((static_cast<int64_t>(seqs) * kv_heads + 2ll * grid) * 4);
-    w.part_ml = w.part_o + align256(2ll * grid * rows_all * dim * 4);
-    w.bytes = w.part_ml + align256(2ll * grid * rows_all * 8);
+    w.part_o = align256((static_cast<int64_t>(seqs) * kv_heads * t.chunks + 2ll * grid) * 4);
+    w.part_ml = w.part_o + align256(2ll * grid * t.chunk_rows * dim * 4);
+    w.bytes = w.part_ml + align256(2ll * grid * t.chunk_rows * 8);
     return w;
 }
 
@@ -1239,7 +1260,7 @@ extern "C" int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_hea
     TilePlan t;
     const int rows_all = kv_heads ? rows * (q_heads / kv_heads) : 0;
     if (!plan_tile(head_dim, rows_all, &t)) return 256;  // one CTA per row and head: nothing to join
-    return workspace_of(t.ctas_per_sm * sm_count(), seqs, rows_all, kv_heads, head_dim).bytes;
+    return workspace_of(t, t.ctas_per_sm * sm_count(), seqs, kv_heads, head_dim).bytes;
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* a, void* stream) {
@@ -1271,16 +1292,18 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     p.D = a->head_dim; p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
     p.window = a->window; p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
     const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
-    // units are counted in 31 bits: at least 16 keys each, one at least per sequence and head
-    const int64_t most_units = (static_cast<int64_t>(a->max_pages) * a->page_size / 16 + 2) * a->seqs * a->kv_heads;
     TilePlan t;
+    const bool tiles = host_variant() != 1 && plan_tile(p.D, rows_all, &t);
+    // units are counted in 31 bits: at least 16 keys each, one at least per sequence and column
+    const int64_t most_units = (static_cast<int64_t>(a->max_pages) * a->page_size / 16 + 2) * a->seqs * a->kv_heads * t.chunks;
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
-    if (host_variant() != 1 && most_units < (1ll << 31) && plan_tile(p.D, rows_all, &t) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
+    if (tiles && most_units < (1ll << 31) && p.page % 16 == 0 && p.D * es % 16 == 0 &&
         aligned(p.cache[0], 16) && aligned(p.cache[1], 16) && p.page_stride[0] * es % 16 == 0 && p.page_stride[1] * es % 16 == 0 &&
         aligned(p.out, 8) && p.pages > 0 && p.page_stride[0] > 0 && p.page_stride[1] > 0 &&
         p.page_stride[0] * es < (1ll << 40) && p.page_stride[1] * es < (1ll << 40)) {
         const int grid = t.ctas_per_sm * sm_count();
-        const Workspace w = workspace_of(grid, p.seqs, rows_all, p.hk, p.D);
+        const Workspace w = workspace_of(t, grid, p.seqs, p.hk, p.D);
+        p.chunks = t.chunks; p.chunk_rows = t.chunk_rows; p.columns = p.hk * t.chunks;
         char* base = static_cast<char*>(a->workspace);
         p.counters = reinterpret_cast<int*>(base);
         p.part_o = reinterpret_cast<float*>(base + w.part_o);

@@ -6,7 +6,7 @@
 //
 // The row stays in registers between the sum of squares and the store, so every operand is read
 // once and every result written once: the kernel is bound by that traffic for many rows and by one
-// chain of load, reduction and store for few.
+// chain of load, redmction and store for few.
 
 #include "ops_common.cuh"
 
@@ -35,13 +35,22 @@ struct NormParams {
     float shrink, mean_of;  // see mean_square below
 };
 
-// Magnitude bits order like the magnitudes themselves, with NaN above infinity: an integer
-// maximum therefore carries a NaN through to the scale, as the quotient's definition does.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger magnitude, NaN if either is: a NaN reaches the scale, as the quotient's definition wants.
+__device__ __forceinline__ float max_mag(float m, float v) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(v)));
+    return d;
+}
 
-__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
-    const float s = __uint_as_float(amax_bits) / 448.0f;
+__device__ __forceinline__ float scale_of(float amax) {
+    const float s = amax * (1.0f / 448.0f);
     return s < kScaleFloor ? kScaleFloor : s;  // NaN stays NaN
+}
+// 1 / s to a unit in the last place; s is 2^-64 or more.
+__device__ __forceinline__ float reciprocal(float s) {
+    float d;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(d) : "f"(s));
+    return d;
 }
 
 template <typename RT>
@@ -70,14 +79,15 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red, int row_i
     return s;
 }
 
-__device__ __forceinline__ uint32_t row_max(uint32_t v, int tpr, uint32_t* red, int row_in_cta) {
-    v = __reduce_max_sync(0xffffffffu, v);
+__device__ __forceinline__ float row_max(float v, int tpr, float* red, int row_in_cta) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_mag(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (tpr == 32) return v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpr >> 5, first = row_in_cta * warps;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    uint32_t m = 0;
-    for (int i = 0; i < warps; ++i) m = max(m, red[first + i]);
+    float m = 0.0f;
+    for (int i = 0; i < warps; ++i) m = max_mag(m, red[first + i]);
     return m;
 }
 
@@ -85,7 +95,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int tpr, uint32_t* red, 
 template <typename XT, typename RT, int CH, bool Q8>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormParams p) {
     __shared__ float red[32];
-    __shared__ uint32_t redu[32];
+    __shared__ float redm[32];
     pdl_launch_dependents();
     const int tpr = 1 << p.tpr_log2;
     const int row_in_cta = threadIdx.x >> p.tpr_log2, t = threadIdx.x & (tpr - 1);
@@ -98,6 +108,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const int c = t + j * tpr;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
         if (live && c < chunks) {
             load_vec(static_cast<const XT*>(p.x) + row * p.ldx + c * 8, h[j]);
             if constexpr (HasResidual<RT>::value) {
@@ -106,73 +118,82 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[j][i] += r[i];
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
         }
     }
+    auto load_weight = [&](int c, float (&v)[8]) {
+        if (p.w_type == NVFP4_F32) load_vec(static_cast<const float*>(p.weight) + c * 8, v);
+        else load_vec(static_cast<const __nv_bfloat16*>(p.weight) + c * 8, v);
+    };
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int c = t + j * tpr;
         if constexpr (HasResidual<RT>::value) {
+            const int c = t + j * tpr;
             if (live && c < chunks) store_vec(static_cast<RT*>(p.residual_out) + row * p.ldro + c * 8, h[j]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = add_square(h[j][i], p.shrink, sum);
     }
     const float rstd = rsqrtf(fmaf(row_sum(sum, tpr, red, row_in_cta), p.mean_of, p.eps));
-    uint32_t amax = 0;
+    float amax[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int c = t + j * tpr;
-        if (c < chunks) {
-            float w[8];
-            if (p.w_type == NVFP4_F32) load_vec(static_cast<const float*>(p.weight) + c * 8, w);
-            else load_vec(static_cast<const __nv_bfloat16*>(p.weight) + c * 8, w);
+        amax[j] = 0.0f;
+        if (t + j * tpr >= chunks) continue;  // h is zero there
+        // behind the sum: requested before it, the weights' registers cost more occupancy than their
+        // latency (8192 x 4096: 48 us)
+        float w[8];
+        load_weight(t + j * tpr, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[j][i] = h[j][i] * rstd * w[i];
-                if constexpr (Q8) amax = max(amax, mag(h[j][i]));
-            }
+        for (int i = 0; i < 8; ++i) {
+            h[j][i] = h[j][i] * rstd * w[i];
+            if constexpr (Q8) amax[j] = max_mag(amax[j], h[j][i]);
         }
     }
     if constexpr (!Q8) {
+        if (p.y_type == NVFP4_F32) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = t + j * tpr;
-            if (!live || c >= chunks) continue;
-            if (p.y_type == NVFP4_F32) store_vec(static_cast<float*>(p.y) + row * p.ldy + c * 8, h[j]);
-            else store_vec(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + c * 8, h[j]);
+            for (int j = 0; j < CH; ++j)
+                if (live && t + j * tpr < chunks) store_vec(static_cast<float*>(p.y) + row * p.ldy + (t + j * tpr) * 8, h[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (live && t + j * tpr < chunks) store_vec(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + (t + j * tpr) * 8, h[j]);
         }
         return;
     }
-    const bool by_row = p.group == p.cols;
-    if (by_row) {
-        amax = row_max(amax, tpr, redu, row_in_cta);
-        if (live && t == 0) p.scales[row] = scale_of(amax);
+    float inv[CH];
+    if (p.group == p.cols) {
+        float top = amax[0];
+#pragma unroll
+        for (int j = 1; j < CH; ++j) top = max_mag(top, amax[j]);
+        const float s = scale_of(row_max(top, tpr, redm, row_in_cta));
+        if (live && t == 0) p.scales[row] = s;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) inv[j] = reciprocal(s);
+    } else {
+        // a group of 16..256 columns is 2..32 neighbouring lanes
+        for (int o = 1; o < p.group >> 3; o <<= 1) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) amax[j] = max_mag(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], o));
+        }
+        const int lanes_log2 = __ffs(p.group >> 3) - 1;
+        float* const out = p.scales + row * (chunks >> lanes_log2);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = t + j * tpr;
+            const float s = scale_of(amax[j]);
+            inv[j] = reciprocal(s);
+            if (live && c < chunks && (c & ((p.group >> 3) - 1)) == 0) out[c >> lanes_log2] = s;
+        }
     }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const int c = t + j * tpr;
-        if (!by_row) {
-            // a group of 16..256 columns is 2..32 neighbouring lanes
-            amax = 0;
-            if (c < chunks) {
+        if (!live || c >= chunks) continue;
+        uint32_t q[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max(amax, mag(h[j][i]));
-            }
-            for (int o = 1; o < p.group >> 3; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (live && c < chunks && (c & ((p.group >> 3) - 1)) == 0)
-                p.scales[row * (p.cols / p.group) + c / (p.group >> 3)] = scale_of(amax);
-        }
-        const float inv = 1.0f / scale_of(amax);
-        if (live && c < chunks) {
-            uint32_t q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = pack_e4m3(h[j][2 * i] * inv, h[j][2 * i + 1] * inv);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.ldy + c * 8) =
-                make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-        }
+        for (int i = 0; i < 4; ++i) q[i] = pack_e4m3(h[j][2 * i] * inv[j], h[j][2 * i + 1] * inv[j]);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.ldy + c * 8) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
     }
 }
 
@@ -185,7 +206,7 @@ template <typename XT, typename RT>
 __global__ void __launch_bounds__(256) rms_norm_scalar_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ float h[];
     __shared__ float red[32];
-    __shared__ uint32_t redu[32];
+    __shared__ float redm[32];
     pdl_launch_dependents();
     pdl_wait();
     const int64_t row = blockIdx.x;
@@ -202,30 +223,29 @@ __global__ void __launch_bounds__(256) rms_norm_scalar_kernel(const __grid_const
         sum = add_square(v, p.shrink, sum);
     }
     const float rstd = rsqrtf(fmaf(row_sum(sum, n, red, 0), p.mean_of, p.eps));
-    uint32_t amax = 0;
+    float amax = 0.0f;
     for (int c = t; c < p.cols; c += n) {
         const float v = h[c] * rstd * load_typed(p.weight, p.w_type, c);
         h[c] = v;
-        amax = max(amax, mag(v));
+        amax = max_mag(amax, v);
         if (p.y_type == NVFP4_F32) static_cast<float*>(p.y)[row * p.ldy + c] = v;
         else if (p.y_type == NVFP4_BF16) static_cast<__nv_bfloat16*>(p.y)[row * p.ldy + c] = __float2bfloat16_rn(v);
     }
     if (p.y_type != NVFP4_E4M3) return;
+    uint8_t* const y = static_cast<uint8_t*>(p.y) + row * p.ldy;
     if (p.group == p.cols) {
-        const float s = scale_of(row_max(amax, n, redu, 0));
+        const float s = scale_of(row_max(amax, n, redm, 0)), inv = reciprocal(s);
         if (t == 0) p.scales[row] = s;
-        for (int c = t; c < p.cols; c += n)
-            static_cast<uint8_t*>(p.y)[row * p.ldy + c] = static_cast<uint8_t>(pack_e4m3(h[c] * (1.0f / s), 0.0f));
+        for (int c = t; c < p.cols; c += n) y[c] = static_cast<uint8_t>(pack_e4m3(h[c] * inv, 0.0f));
         return;
     }
     __syncthreads();  // h is complete; a warp takes a group
     for (int g = t >> 5; g < p.cols / p.group; g += n >> 5) {
-        uint32_t m = 0;
-        for (int c = g * p.group + (t & 31); c < (g + 1) * p.group; c += 32) m = max(m, mag(h[c]));
-        const float s = scale_of(__reduce_max_sync(0xffffffffu, m));
+        float m = 0.0f;
+        for (int c = g * p.group + (t & 31); c < (g + 1) * p.group; c += 32) m = max_mag(m, h[c]);
+        const float s = scale_of(row_max(m, 32, redm, 0)), inv = reciprocal(s);
         if ((t & 31) == 0) p.scales[row * (p.cols / p.group) + g] = s;
-        for (int c = g * p.group + (t & 31); c < (g + 1) * p.group; c += 32)
-            static_cast<uint8_t*>(p.y)[row * p.ldy + c] = static_cast<uint8_t>(pack_e4m3(h[c] * (1.0f / s), 0.0f));
+        for (int c = g * p.group + (t & 31); c < (g + 1) * p.group; c += 32) y[c] = static_cast<uint8_t>(pack_e4m3(h[c] * inv, 0.0f));
     }
 }
 
