@@ -43,6 +43,7 @@ struct AttnParams {
     // A kv head's query rows are taken in `chunks` equal chunks of `chunk_rows` (the last may hold fewer),
     // one where a CTA can hold them all; a (kv head, chunk) is a column of a sequence's items.
     int chunks, chunk_rows, columns;
+    uint32_t group_inv;         // 2^24 / group, rounded up
     int row_blocks;             // warps of a CTA that share a tile, each with its own query rows
     int page_tiles;             // 16-key blocks per page
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
@@ -85,6 +86,7 @@ constexpr float kTiny = 7.52316385e-37f;  // 2^-120
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kAlignSlack = 3;  // units
+constexpr int kMaxGroup = 1024;  // query heads per kv head: 8 group^2 < 2^24, see place_of_row
 constexpr int kJoinOnce = 32;  // parts times rows that a thread joins in a single step
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
@@ -150,7 +152,6 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
     }
     if (p.lse && threadIdx.x == 0) p.lse[t * p.hq + h] = total == 0.0f ? -INFINITY : top + logf(total);
 }
-
 
 // ------------------------------------------------------------------ tile kernel
 //
@@ -378,7 +379,46 @@ __device__ __forceinline__ void enter_run(Run& r, int b, int before, const Span&
     find_parts(r);
 }
 
-// Four values of a row gathered from parts, one part after the other.
+// The weights of a row's parts and its totals, for all rows at once: ml[part * step + row] is (m, l) and
+// becomes (weight, l), total[row] = (m, l) of the row. Lanes share a row's parts.
+__device__ __forceinline__ void weigh_parts(float2* ml, int step, int rows, int count, float2* total) {
+    int lanes_log2 = 0;
+    while (lanes_log2 < 5 && (1 << lanes_log2) < count) ++lanes_log2;
+    const int lanes = 1 << lanes_log2, c0 = threadIdx.x & (lanes - 1), apart = blockDim.x >> lanes_log2;
+#pragma unroll 1
+    for (int first = 0; first < rows; first += apart) {  // all lanes go through the shuffles
+        const int row = first + (threadIdx.x >> lanes_log2);
+        const bool in = row < rows;
+        float m = -INFINITY, l = 0.0f;
+        for (int c = c0; in && c < count; c += lanes) m = fmaxf(m, ml[c * step + row].x);
+        for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int c = c0; in && c < count; c += lanes) {
+            const float2 part = ml[c * step + row];
+            const float f = part_weight(part.x, part.y, m);
+            if (f != 0.0f) l = fmaf(part.y, f, l);
+            ml[c * step + row].x = f;
+        }
+        for (int o = 1; o < lanes; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (in && c0 == 0) total[row] = make_float2(m, l);
+    }
+}
+
+__device__ __forceinline__ void add_weighed(float4& o, float f, float4 v) {
+    const bool on = f != 0.0f;  // else nothing, not even 0 * NaN
+    o.x = fmaf(on ? v.x : 0.0f, f, o.x); o.y = fmaf(on ? v.y : 0.0f, f, o.y);
+    o.z = fmaf(on ? v.z : 0.0f, f, o.z); o.w = fmaf(on ? v.w : 0.0f, f, o.w);
+}
+// Four values of a row from its weighed parts, in order.
+__device__ __forceinline__ float4 gather(const float2* weight, int step, const char* o, int o_step, int count) {
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int c = 0; c < count; ++c) add_weighed(sum, weight[c * step].x, *reinterpret_cast<const float4*>(o + c * o_step));
+    return sum;
+}
+
+// The same from parts not weighed yet, one after the other: one trip to shared memory or L2, and
+// little code, which counts where every instruction is fetched cold (weighed first, a call with one row
+// took 0.7 us longer).
 struct Gathered {
     float m = -INFINITY, l = 0.0f;
     float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -388,25 +428,39 @@ struct Gathered {
         m = top;
         l *= keep;
         o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
-        if (f != 0.0f) l = fmaf(ml.y, f, l);
-        weigh(f, v);
-    }
-    __device__ __forceinline__ void weigh(float f, float4 v) {
-        if (f == 0.0f) return;  // nothing, not even 0 * NaN
+        if (f == 0.0f) return;
+        l = fmaf(ml.y, f, l);
         o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y);
         o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
     }
 };
 
-__device__ __forceinline__ void store_out(const AttnParams& p, int b, int column, int chunk_row, int d, const Gathered& a) {
+// Where a row of an item's column goes: the place of (sequence, row, query head) in out and lse; negative
+// for the last chunk's padding. Rows (fewer than 8 group) divide by the group through a product, too large by
+// row / 2^24 at most, which has to stay below 1 / group: 8 group^2 < 2^24.
+__device__ __forceinline__ int64_t place_of_row(const AttnParams& p, int b, int column, int chunk_row) {
     const int h = p.chunks == 1 ? column : column / p.chunks, row = (column - h * p.chunks) * p.chunk_rows + chunk_row;
-    if (row >= p.rows * p.group) return;  // the last chunk's padding
-    const int m = row / p.group, head = h * p.group + row - m * p.group;
-    const int64_t at = (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
-    const float inv = a.l == 0.0f ? 0.0f : (p.cache_scale[1] ? p.cache_scale[1][h] : 1.0f) / a.l;
-    *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
-        make_uint2(pack_bf16(a.o.x * inv, a.o.y * inv), pack_bf16(a.o.z * inv, a.o.w * inv));
-    if (d == 0 && p.lse) p.lse[at] = a.l == 0.0f ? -INFINITY : (a.m + log2f(a.l)) * 0.6931471805599453f;
+    if (row >= p.rows * p.group) return -1;
+    const int m = static_cast<int>(static_cast<uint32_t>(row) * p.group_inv >> 24), head = h * p.group + row - m * p.group;
+    return (static_cast<int64_t>(b) * p.rows + m) * p.hq + head;
+}
+__device__ __forceinline__ void store_out(const AttnParams& p, int64_t at, int d, float4 o, float l, float vscale) {
+    if (at < 0) return;
+    const float inv = l == 0.0f ? 0.0f : __fdividef(vscale, l);
+    *reinterpret_cast<uint2*>(p.out + at * p.D + d) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+__device__ __forceinline__ float log_sum(float2 ml) { return ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f; }
+// lse of all rows of an item's column from their totals.
+__device__ __forceinline__ void store_lse(const AttnParams& p, int b, int column, const float2* total) {
+    if (!p.lse) return;
+#pragma unroll 1
+    for (int row = threadIdx.x; row < p.chunk_rows; row += blockDim.x) {
+        const int64_t at = place_of_row(p, b, column, row);
+        if (at >= 0) p.lse[at] = log_sum(total[row]);
+    }
+}
+__device__ __forceinline__ float value_scale(const AttnParams& p, int column) {
+    return p.cache_scale[1] ? p.cache_scale[1][p.chunks == 1 ? column : column / p.chunks] : 1.0f;
 }
 
 constexpr int kMaxChunkRows = 128;  // query rows of a CTA in any plan
@@ -436,7 +490,7 @@ __device__ __forceinline__ int join_turns(const AttnParams& p) {
 // once instead, one trip to L2 for all rows. (One row a thread: 16 parts in 9.4 us a call against 9.9 through
 // shared memory; four rows: 25 against 20.)
 __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, char* room, int room_bytes, const Parts& parts,
-                                           int first, int step, int count, int to, int b, int h) {
+                                           int first, int step, int count, int to, int b, int column) {
     const int rows_all = p.chunk_rows, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
     const int o_bytes = rows_all * p.D * 4, ml_bytes = rows_all * 8;
     const bool fits = join_turns(p) > 1 && count * part_bytes(p) <= room_bytes;
@@ -455,17 +509,24 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, 
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
     }
+    const float vscale = value_scale(p, column);
+    if (fits) {
+        float2* const ml = reinterpret_cast<float2*>(room + count * o_bytes);
+        weigh_parts(ml, rows_all, rows_all, count, sh.ml);
+        __syncthreads();
+#pragma unroll 2
+        for (int row = threadIdx.x >> p.quad_log2; row < rows_all; row += blockDim.x >> p.quad_log2) {
+            if (d >= p.D) continue;
+            const float4 o = gather(ml + row, rows_all, room + (row * p.D + d) * 4, o_bytes, count);
+            if (to < 0) store_out(p, place_of_row(p, b, column, row), d, o, sh.ml[row].y, vscale);
+            else __stcg(reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(to) * rows_all + row) * p.D + d), o);
+        }
+    } else {
 #pragma unroll 1
-    for (int row = threadIdx.x >> p.quad_log2; row < rows_all; row += blockDim.x >> p.quad_log2) {
-        if (d >= p.D) continue;
-        float* const po = p.part_o + row * p.D + d;
-        Gathered a;
-        if (fits) {
-            const float2* const ml = reinterpret_cast<const float2*>(room + count * o_bytes) + row;
-            const char* const o = room + (row * p.D + d) * 4;
-#pragma unroll 4
-            for (int c = 0; c < count; ++c) a.add(ml[c * rows_all], *reinterpret_cast<const float4*>(o + c * o_bytes));
-        } else {
+        for (int row = threadIdx.x >> p.quad_log2; row < rows_all; row += blockDim.x >> p.quad_log2) {
+            if (d >= p.D) continue;
+            float* const po = p.part_o + row * p.D + d;
+            Gathered a;
 #pragma unroll 1
             for (int c = 0; c < count; c += 8) {
                 float4 v[8];
@@ -480,15 +541,22 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, 
                 for (int j = 0; j < 8; ++j)
                     if (c + j < count) a.add(ml[j], v[j]);
             }
+            if (to < 0) {
+                const int64_t at = place_of_row(p, b, column, row);
+                store_out(p, at, d, a.o, a.l, vscale);
+                if (d == 0 && p.lse && at >= 0) p.lse[at] = log_sum(make_float2(a.m, a.l));
+            } else {
+                __stcg(reinterpret_cast<float4*>(po + static_cast<int64_t>(to) * rows_all * p.D), a.o);
+                if (d == 0) sh.ml[row] = make_float2(a.m, a.l);
+            }
         }
-        if (to < 0) {
-            store_out(p, b, h, row, d, a);
-        } else {
-            __stcg(reinterpret_cast<float4*>(po + static_cast<int64_t>(to) * rows_all * p.D), a.o);
-            if (d == 0) sh.ml[row] = make_float2(a.m, a.l);
-        }
+        if (to < 0) return;
+        __syncthreads();
     }
-    if (to < 0) return;
+    if (to < 0) {
+        store_lse(p, b, column, sh.ml);
+        return;
+    }
     __syncthreads();
     for (int row = threadIdx.x; row < rows_all; row += blockDim.x) __stcg(p.part_ml + to * rows_all + row, sh.ml[row]);
 }
@@ -537,6 +605,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     float* const smem = reinterpret_cast<float*>(smem_raw + (-static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u));
     __shared__ __align__(8) uint64_t s_bar[W][T::kStages][2];
     __shared__ int s_scan[W];
+    __shared__ float s_f[8 * NT * W];  // rows' factors (not kQRegs)
     __shared__ Run s_run;
     __shared__ JoinShared s_join;
     float* s_o = smem;                                        // merge, in the rings' place: [W][kRowsW][kOStride]
@@ -573,11 +642,14 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             return v;
         };
         const int incl = prefix(sp.units), total = __shfl_sync(0xffffffffu, incl, 31) * p.columns;
-        const int least = (total + grid - 1) / grid;
+        // An item of few units is not split where a join takes longer than they do. us split and not: 2
+        // units of one row 8.8 and 7.0, 5 units of one row 8.7 and 9.8, of two 11.1 and 12.0, of four
+        // 13.3 and 12.5, of eight 21.8 and 20.2 (rows that a thread joins).
+        const int least = (total + grid - 1) / grid, alone = min(2 + join_turns(p), 6);
         int n = 0, before = 0;  // CTAs of an item of this lane's sequence; CTAs or units before the sequence
         bool whole_items = false;
         for (int load = least; load <= least + kAlignSlack && !whole_items; ++load) {
-            n = (sp.units + load - 1) / load;
+            n = sp.units <= alone ? sp.units > 0 : (sp.units + load - 1) / load;
             whole_items = __reduce_add_sync(0xffffffffu, n) * p.columns <= grid;
         }
         bool here;
@@ -746,27 +818,56 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         };
         look_up(tile);
 
-        // --- query rows as the scores' B operand: loaded here, put to use behind the first requests
-        uint2 raw[NT][T::kQ];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + 8 * nt + g, m = row / p.group;
+        // --- query rows as the scores' B operand
+        auto load_q = [&](int nt, uint2 (&raw)[T::kQ]) {
+            const int row = row0 + 8 * nt + g, m = static_cast<int>(static_cast<uint32_t>(row) * p.group_inv >> 24);
             const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.rows + m) * p.q_ts +
                                      static_cast<int64_t>(h * p.group + row - m * p.group) * p.q_hs;
             const bool live = row < rows_end;
 #pragma unroll
             for (int i = 0; i < T::kQ; ++i) {  // 4 values each, in the order of the keys' registers
                 const int d = F8 ? 16 * (t + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (t + 4 * (i >> 1)) + 4 * (i & 1);
-                raw[nt][i] = make_uint2(0, 0);
+                raw[i] = make_uint2(0, 0);
                 if (live && d < p.D) {
                     if (p.q_vec) {
-                        raw[nt][i] = *reinterpret_cast<const uint2*>(q + d);
+                        raw[i] = *reinterpret_cast<const uint2*>(q + d);
                     } else {
                         const uint16_t* w = reinterpret_cast<const uint16_t*>(q + d);
-                        raw[nt][i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+                        raw[i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                     }
                 }
             }
+        };
+        // The factor from scores to base-2 units is made positive (its sign goes to q), so that the maximum
+        // can be taken over raw scores; a zero becomes 2^-126, or masked scores would be NaN.
+        auto convert_q = [&](uint2 (&raw)[T::kQ]) {
+            float f = p.scale * 1.4426950408889634f * kscale;
+            const uint32_t flip = f < 0.0f ? 0x80008000u : 0u;
+            f = fabsf(f);
+            if constexpr (F8) {
+                uint32_t tops = 0;  // magnitudes, two a word
+#pragma unroll
+                for (int i = 0; i < T::kQ; ++i) tops = __vmaxu2(__vmaxu2(tops, raw[i].x & 0x7fff7fffu), raw[i].y & 0x7fff7fffu);
+                uint32_t top = max(tops & 0xffffu, tops >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // (an infinity's exponent leaves the finite values next to it below 2^15 too)
+                const int up = top == 0 ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+                const float mul = __int_as_float((127 + up) << 23);
+                f *= __int_as_float((127 - up) << 23);
+                auto narrow = [&](uint32_t w) { return pack_f16(bf16_lo(w) * mul, bf16_hi(w) * mul); };
+#pragma unroll
+                for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(narrow(raw[i].x), narrow(raw[i].y));
+            }
+#pragma unroll
+            for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(raw[i].x ^ flip, raw[i].y ^ flip);
+            return f < 1.1754943508e-38f ? 1.1754943508e-38f : f;
+        };
+        uint2 qf[T::kQRegs ? NT : 1][T::kQ];
+        float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
+        if constexpr (T::kQRegs) {  // on their way while the first tiles are requested
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) load_q(nt, qf[nt]);
         }
 #pragma unroll
         for (int st = 0; st < T::kStages; ++st) {
@@ -780,53 +881,33 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 look_up(tl + streams);
             }
         }
-        uint2 qf[T::kQRegs ? NT : 1][T::kQRegs ? T::kQ : 1];
-        float zf[NT][2];  // what turns a score into base-2 units, for rows 2t, 2t + 1 of each block
+        if constexpr (T::kQRegs) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // The factor from scores to base-2 units is made positive (its sign goes to q), so that the
-            // maximum can be taken over raw scores; a zero becomes 2^-126, or masked scores would be NaN.
-            float f = p.scale * 1.4426950408889634f * kscale;
-            const uint32_t flip = f < 0.0f ? 0x80008000u : 0u;
-            f = fabsf(f);
-            if constexpr (F8) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < T::kQ; ++i)
-                    top = max(max(max(top, raw[nt][i].x & 0x7fffu), max(raw[nt][i].x >> 16 & 0x7fffu, raw[nt][i].y & 0x7fffu)),
-                              raw[nt][i].y >> 16 & 0x7fffu);
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const bool plain = top == 0 || top >= 0x7f80u;
-                const int up = plain ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
-                const float mul = __int_as_float((127 + up) << 23);
-                f *= __int_as_float((127 - up) << 23);
-                auto narrow = [&](uint32_t w) {  // values beyond f16 (next to an infinity) stay finite
-                    float v[2] = {bf16_lo(w) * mul, bf16_hi(w) * mul};
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (fabsf(v[e]) < INFINITY) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
-                    return pack_f16(v[0], v[1]);
-                };
-#pragma unroll
-                for (int i = 0; i < T::kQ; ++i) raw[nt][i] = make_uint2(narrow(raw[nt][i].x), narrow(raw[nt][i].y));
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f = convert_q(qf[nt]);
+                zf[nt][0] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t) : f;
+                zf[nt][1] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t + 4) : f;
             }
-            if (f < 1.1754943508e-38f) f = 1.1754943508e-38f;
+        } else {  // the warps that share the rows share the work
+#pragma unroll 1
+            for (int nt = stream; nt < NT; nt += streams) {
+                load_q(nt, qf[0]);
+                const float f = convert_q(qf[0]);
+                if (t == 0) s_f[(rb * NT + nt) * 8 + g] = f;
 #pragma unroll
-            for (int i = 0; i < T::kQ; ++i) raw[nt][i] = make_uint2(raw[nt][i].x ^ flip, raw[nt][i].y ^ flip);
-            zf[nt][0] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t) : f;
-            zf[nt][1] = F8 ? __shfl_sync(0xffffffffu, f, 8 * t + 4) : f;
+                for (int i = 0; i < T::kQ; ++i) s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane] = qf[0][i];
+            }
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < T::kQ; ++i) {
-                if constexpr (T::kQRegs) qf[nt][i] = raw[nt][i];
-                else if (stream == 0) s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane] = raw[nt][i];
+            for (int nt = 0; nt < NT; ++nt) {
+                zf[nt][0] = s_f[(rb * NT + nt) * 8 + 2 * t];
+                zf[nt][1] = s_f[(rb * NT + nt) * 8 + 2 * t + 1];
             }
         }
         auto query = [&](int nt, int i) {
             if constexpr (T::kQRegs) return qf[nt][i];
             else return s_q[((rb * NT + nt) * T::kQ + i) * 32 + lane];
         };
-        if constexpr (!T::kQRegs) __syncthreads();
 
         float o[NT][T::kMT][4], mx[NT][2], l[NT][2];
 #pragma unroll
@@ -1122,22 +1203,24 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
         __syncthreads();
         const Run r = s_run;
         const bool direct = r.parts == 1;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1);
-        const int d = 4 * (tid & ((1 << p.quad_log2) - 1));
+        const float vscale = value_scale(p, r.head);
+        const int apart = p.row_blocks * kRowsW;
+        const int64_t slot_row = (2 * static_cast<int64_t>(blockIdx.x) + (r.first == r.begin ? 0 : 1)) * p.chunk_rows;
+        const int d = 4 * (tid & ((1 << p.quad_log2) - 1)), row1 = tid >> p.quad_log2;
 #pragma unroll 1
-        for (int row = tid >> p.quad_log2; row < p.chunk_rows; row += kThreads >> p.quad_log2) {
-            if (d >= p.D) continue;
+        for (int row = row1; row < p.chunk_rows; row += kThreads >> p.quad_log2) {
+            if (d >= p.D) break;
+            const float4* const o = reinterpret_cast<const float4*>(s_o + row * T::kOStride + d);
             Gathered a;
 #pragma unroll 1
-            for (int st = 0; st < streams; ++st) {
-                const int w = st * p.row_blocks * kRowsW + row;
-                a.add(s_ml[w], *reinterpret_cast<const float4*>(s_o + w * T::kOStride + d));
-            }
+            for (int st = 0; st < streams; ++st) a.add(s_ml[st * apart + row], o[st * apart * (T::kOStride / 4)]);
             if (direct) {
-                store_out(p, r.seq, r.head, row, d, a);
+                const int64_t at = place_of_row(p, r.seq, r.head, row);
+                store_out(p, at, d, a.o, a.l, vscale);
+                if (d == 0 && p.lse && at >= 0) p.lse[at] = log_sum(make_float2(a.m, a.l));
             } else {
-                __stcg(reinterpret_cast<float4*>(p.part_o + (slot * p.chunk_rows + row) * p.D + d), a.o);
-                if (d == 0) __stcg(p.part_ml + slot * p.chunk_rows + row, make_float2(a.m, a.l));
+                __stcg(reinterpret_cast<float4*>(p.part_o + (slot_row + row) * p.D + d), a.o);
+                if (d == 0) __stcg(p.part_ml + slot_row + row, make_float2(a.m, a.l));
             }
         }
         if (!direct) finish_item(p, s_join, s_run, reinterpret_cast<char*>(smem), T::kMain);
@@ -1167,7 +1250,6 @@ cudaError_t read_status(int* bits) {
     return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(int));
 }
 const bool g_registered = register_status(read_status);
-
 
 // The tile kernel's instance for a head size and number of query rows per kv head: the head is
 // padded to 64, 128 or 256 in registers, rows to blocks of 8 NT times the warps that share a tile.
@@ -1293,7 +1375,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     p.window = a->window; p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
     const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
     TilePlan t;
-    const bool tiles = host_variant() != 1 && plan_tile(p.D, rows_all, &t);
+    const bool tiles = host_variant() != 1 && p.group <= kMaxGroup && plan_tile(p.D, rows_all, &t);
     // units are counted in 31 bits: at least 16 keys each, one at least per sequence and column
     const int64_t most_units = (static_cast<int64_t>(a->max_pages) * a->page_size / 16 + 2) * a->seqs * a->kv_heads * t.chunks;
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
@@ -1310,6 +1392,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         p.part_ml = reinterpret_cast<float2*>(base + w.part_ml);
         p.row_blocks = t.row_blocks;
         p.wait_ns = host_wait_ns();
+        p.group_inv = static_cast<uint32_t>(((1 << 24) + p.group - 1) / p.group);
         while ((4 << p.quad_log2) < p.D) ++p.quad_log2;
         p.page_tiles = p.page / 16;
         p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;

@@ -44,10 +44,7 @@ def _load():
     """Loads the binding and gives it the loaded library's entry points."""
     global _native
     lib = _nv.library()
-    path = _build.BINDING_PATH
-    if not os.path.exists(path):
-        raise RuntimeError(f"decode operators' binding not found at {path}; run "
-                           "`python -m nvfp4_weight_only_gemv_gb300.build`")
+    path = _build.build_binding()  # built with the library; here where that was another's
     loader = importlib.machinery.ExtensionFileLoader("_decode_ops", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_decode_ops", path, loader=loader))
     loader.exec_module(module)

@@ -421,6 +421,11 @@ def test_paged_attention_many_rows_and_odd_heads(rows, hq, hk, D):
         _check_attend([260, 3, 77], rows, hq, hk, D, cache, 16, seed=hq)
 
 
+@pytest.mark.parametrize("rows,hq", [(8, 1024), (2, 1025), (8, 1500)])
+def test_paged_attention_many_heads_per_kv_head(rows, hq):
+    _check_attend([40, 3], rows, hq, 1, 64, BF16, 16)
+
+
 def test_paged_attention_many_sequences():
     lengths = [(i * 37) % 150 for i in range(700)]
     _check_attend(lengths, 1, 4, 1, 64, BF16, 16, seed=3)
