@@ -56,7 +56,7 @@ typedef enum {
     NVFP4_OK = 0,
     NVFP4_ERR_NULL = 1,        /* a required pointer is NULL */
     NVFP4_ERR_SHAPE = 2,       /* M > 8, negative size, K % 16 != 0, top_k/T/E invalid */
-    NVFP4_ERR_ALIGN = 3,       /* an FFN workspace not 256-byte aligned (other misalignment runs
+    NVFP4_ERR_ALIGN = 3,       /* an FFN or attention workspace not 256-byte aligned (other misalignment runs
                                   the byte-load kernel) */
     NVFP4_ERR_DTYPE = 4,       /* y_type is not one of nvfp4_out_t */
     NVFP4_ERR_UNSUPPORTED = 5, /* a size beyond what any kernel here can take */
@@ -279,8 +279,8 @@ typedef enum {
  * Root-mean-square norm of rows:
  *     h = x + residual (fp32),  residual_out = h in the residual's type,
  *     y = h / sqrt(mean(h^2) + eps) * weight                     (fp32, the unrounded h)
- * y is f32, bf16 or E4M3. E4M3: code = E4M3(y / s) to nearest even with s = max(max|y| / 448, 2^-64)
- * over the row (group = 0; scales [rows]) or over each `group` columns, a power of two from 16 to
+ * y is f32, bf16 or E4M3. E4M3: code = E4M3(y / s) to nearest even (the quotient to 2^-22) with s =
+ * max(max|y| / 448, 2^-64) over the row (group = 0; scales [rows]) or over each `group` columns, a power of two from 16 to
  * 256 that divides cols (scales [rows, cols / group]); a NaN makes its scale NaN.
  * residual may be NULL (no addition, residual_out unused). residual_out may be the residual
  * itself and y may be x where type and row pitch agree. Row pitches ld* are in elements.
@@ -310,7 +310,7 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  *     the head's values from 2 * rotary_half on pass through.
  * q_out [tokens, q_heads, head_dim] bf16 receives q (q = NULL: no queries). k and v go to row
  * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale), to
- * nearest even, clamped to +-448. Long-context scalings of the frequencies are the caller's, in
+ * nearest even (the quotient to 2^-22), clamped to +-448; scales are positive normal numbers. Long-context scalings of the frequencies are the caller's, in
  * inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
  * row is zero. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
  * nothing. Two tokens of one call at the same sequence and position leave either's values.

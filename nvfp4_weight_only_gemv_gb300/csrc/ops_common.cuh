@@ -68,17 +68,12 @@ __device__ __forceinline__ void load_f32(const float* p, float (&v)[N]) {
 }
 __device__ __forceinline__ void unpack_bf16(uint32_t u, float& a, float& b) { a = bf16_lo(u); b = bf16_hi(u); }
 
-// Eight or four consecutive values of an aligned row, widened.
+// Eight consecutive values of an aligned row, widened.
 __device__ __forceinline__ void load_vec(const float* p, float (&v)[8]) { load_f32(p, v); }
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[4]) { load_f32(p, v); }
 __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[8]) {
     const uint4 q = *reinterpret_cast<const uint4*>(p);
     unpack_bf16(q.x, v[0], v[1]); unpack_bf16(q.y, v[2], v[3]);
     unpack_bf16(q.z, v[4], v[5]); unpack_bf16(q.w, v[6], v[7]);
-}
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[4]) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    unpack_bf16(q.x, v[0], v[1]); unpack_bf16(q.y, v[2], v[3]);
 }
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }

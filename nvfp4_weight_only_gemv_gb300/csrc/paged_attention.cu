@@ -308,11 +308,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return d;
 }
 
-__device__ __forceinline__ float2 f16x2_f32(uint32_t v) {
-    return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(v & 0xffffu))),
-                       __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16))));
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -741,82 +736,108 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     // j ^ (r >> 1 & 3).
     constexpr int kRow = T::kBoxBytes;
     const uint32_t k_off = kRow == 128 ? g * 128 + ((t ^ g) << 4) : g * 64 + ((t ^ (g >> 1 & 3)) << 4);
-    const uint32_t v_off[2] = {
-        kRow == 128 ? 2 * t * 128 + ((g ^ 2 * t) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8,
-        kRow == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4) : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8};
+    auto v_piece = [&](int r) -> uint32_t {
+        return kRow == 128 ? r * 128 + ((g ^ r) << 4) : r * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    };
+    const uint32_t v_off[2] = {v_piece(2 * t), v_piece(2 * t + 1)};
+
+    // --- the ring's state. Tiles of this warp: stream, stream + streams, ... of the run's part of an item. A
+    // tile's first 16-key block stands at block `slot` of the sequence's page `page`; both walk along.
+    Span sp;
+    int h, base;                    // the item's kv head, the first tile's first key
+    const int32_t* pages;
+    int tile, tile_end;
+    const int step_page = streams * H / p.page_tiles, step_slot = streams * H % p.page_tiles;
+    int next_page = 0, next_slot = 0;
+    int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
+    int at[H], next_at[H];          // the block's first key in its page
+    uint32_t bad = 0, bads = 0;     // blocks whose page id is out of range: requested tile; tiles in the ring
+
+    // looks up the tile after the requested one
+    auto look_up = [&](int tl) {
+        int pg = next_page, sl = next_slot;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            if (i > 0 && p.tall_box) break;
+            next_id[i] = 0;
+            if (tl < tile_end && base + tl * T::kKeys + 16 * i < sp.n) next_id[i] = pages[pg];
+            next_at[i] = 16 * sl;
+            if (++sl == p.page_tiles) { sl = 0; ++pg; }
+        }
+        next_slot += step_slot;
+        next_page += step_page;
+        if (next_slot >= p.page_tiles) { next_slot -= p.page_tiles; ++next_page; }
+    };
+    auto take = [&]() {
+        bad = 0;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            if (i > 0 && p.tall_box) break;
+            id[i] = next_id[i];
+            at[i] = next_at[i];
+            if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
+                if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                id[i] = 0;
+                bad |= p.tall_box ? (1u << H) - 1 : 1u << i;
+            }
+        }
+    };
+    // copies K (which = 0) or V of the taken tile to a stage; every lane is through with its last use
+    auto request = [&](uint32_t stage, int which) {
+        __syncwarp();
+        const uint32_t bar = bars + 16 * stage + 8 * which, to = ring + (2 * stage + which) * T::kPart;
+        if (lane == 0) {
+            const uint64_t pol = evict_first();
+            barrier_expect(bar, T::kPart);
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int x = 0; x < T::kBoxes; ++x)
+                    if ((i == 0 || !p.tall_box) && (x == 0 || !p.wide_box))
+                        copy_box(to + (i * T::kBoxes + x) * T::kBox, &p.map[which], x * (T::kBoxBytes / T::kES), at[i], h, id[i], bar, pol);
+        }
+    };
+    auto enter_item = [&]() {
+        sp = run.span;
+        h = p.chunks == 1 ? run.head : run.head / p.chunks;
+        // whole tiles stand in one page where pages are multiples of a tile
+        base = sp.lo & ~(p.tall_box ? T::kKeys - 1 : 15);
+        pages = p.table + run.seq * p.table_stride;
+        tile_end = (run.last - run.item0) * streams;
+        tile = (run.first - run.item0) * streams + stream;
+        next_page = ((base >> 4) + tile * H) / p.page_tiles;
+        next_slot = ((base >> 4) + tile * H) % p.page_tiles;
+        bads = 0;
+        look_up(tile);
+    };
+    auto fill_ring = [&]() {
+#pragma unroll
+        for (int st = 0; st < T::kStages; ++st) {
+            const int tl = tile + st * streams;
+            if (tl < tile_end && !dead) {
+                take();
+                const uint32_t stage = cur + st < T::kStages ? cur + st : cur + st - T::kStages;
+                request(stage, 0);
+                request(stage, 1);
+                bads |= bad << 8 * st;
+                look_up(tl + streams);
+            }
+        }
+    };
 
     for (;;) {
-        const int b = run.seq, h = p.chunks == 1 ? run.head : run.head / p.chunks;
+        const int b = run.seq;
+        enter_item();
         const int row0 = (run.head - h * p.chunks) * p.chunk_rows + rb * kRowsW;  // this warp's first query row
         const int rows_end = min(rows_all, (run.head - h * p.chunks + 1) * p.chunk_rows);
-        const Span sp = run.span;
-        // whole tiles stand in one page where pages are multiples of a tile
-        const int base = sp.lo & ~(p.tall_box ? T::kKeys - 1 : 15);
         const float kscale = p.cache_scale[0] ? p.cache_scale[0][h] : 1.0f;
-        const int32_t* const pages = p.table + b * p.table_stride;
-
-        // --- tiles of this warp: stream, stream + streams, ... of the run. A tile's first 16-key block
-        // stands at block `slot` of the sequence's page `page`; both walk along with the tiles.
-        const int tile_end = (run.last - run.item0) * streams;
-        int tile = (run.first - run.item0) * streams + stream;
-        const int step_page = streams * H / p.page_tiles, step_slot = streams * H % p.page_tiles;
-        int next_page = ((base >> 4) + tile * H) / p.page_tiles, next_slot = ((base >> 4) + tile * H) % p.page_tiles;
-        int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
-        int at[H], next_at[H];          // the block's first key in its page
         int k_taken = 0;                // the wait that failed was for V: this tile's K had come
-        uint32_t bad = 0, bads = 0;     // blocks whose page id is out of range: requested tile; tiles in the ring
-
-        // looks up the tile after the requested one
-        auto look_up = [&](int tl) {
-            int pg = next_page, sl = next_slot;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if (i > 0 && p.tall_box) break;
-                next_id[i] = 0;
-                if (tl < tile_end && base + tl * T::kKeys + 16 * i < sp.n) next_id[i] = pages[pg];
-                next_at[i] = 16 * sl;
-                if (++sl == p.page_tiles) { sl = 0; ++pg; }
-            }
-            next_slot += step_slot;
-            next_page += step_page;
-            if (next_slot >= p.page_tiles) { next_slot -= p.page_tiles; ++next_page; }
-        };
-        auto take = [&]() {
-            bad = 0;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if (i > 0 && p.tall_box) break;
-                id[i] = next_id[i];
-                at[i] = next_at[i];
-                if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
-                    if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
-                    id[i] = 0;
-                    bad |= p.tall_box ? (1u << H) - 1 : 1u << i;
-                }
-            }
-        };
-        // copies K (which = 0) or V of the taken tile to a stage; every lane is through with its last use
-        auto request = [&](uint32_t stage, int which) {
-            __syncwarp();
-            const uint32_t bar = bars + 16 * stage + 8 * which, to = ring + (2 * stage + which) * T::kPart;
-            if (lane == 0) {
-                const uint64_t pol = evict_first();
-                barrier_expect(bar, T::kPart);
-#pragma unroll
-                for (int i = 0; i < H; ++i)
-#pragma unroll
-                    for (int x = 0; x < T::kBoxes; ++x)
-                        if ((i == 0 || !p.tall_box) && (x == 0 || !p.wide_box))
-                            copy_box(to + (i * T::kBoxes + x) * T::kBox, &p.map[which], x * (T::kBoxBytes / T::kES), at[i], h, id[i], bar, pol);
-            }
-        };
         auto arrived = [&](int which) { return barrier_wait(bars + 16 * cur + 8 * which, parity, p.wait_ns); };
         // every key of the tile is there for every row
         auto whole = [&](int tl) {
             const int key = base + tl * T::kKeys;
             return key >= sp.lo_all && key + T::kKeys <= sp.hi_all;
         };
-        look_up(tile);
 
         // --- query rows as the scores' B operand
         auto load_q = [&](int nt, uint2 (&raw)[T::kQ]) {
@@ -869,18 +890,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) load_q(nt, qf[nt]);
         }
-#pragma unroll
-        for (int st = 0; st < T::kStages; ++st) {
-            const int tl = tile + st * streams;
-            if (tl < tile_end && !dead) {
-                take();
-                const uint32_t stage = cur + st < T::kStages ? cur + st : cur + st - T::kStages;
-                request(stage, 0);
-                request(stage, 1);
-                bads |= bad << 8 * st;
-                look_up(tl + streams);
-            }
-        }
+        fill_ring();
         if constexpr (T::kQRegs) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -918,6 +928,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
+        const bool was_dead = dead;
         for (; tile < tile_end && !dead; tile += streams) {
             // --- scores
             if (!arrived(0)) { dead = true; break; }
@@ -1167,7 +1178,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             }
             if (++cur == T::kStages) { cur = 0; parity ^= 1; }
         }
-        if (dead && tile < tile_end) {
+        if (dead && !was_dead) {
             // the result is unspecified, but no copy may outlive the CTA: what was requested and has not
             // been waited for is K of this tile or of the one after the ring's, and all the ring's V
             if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_TIMEOUT);

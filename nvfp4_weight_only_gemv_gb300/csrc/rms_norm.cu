@@ -3,10 +3,11 @@
 //   h = x + residual          (fp32; residual_out = h in the residual's type)
 //   y = h / sqrt(mean(h^2) + eps) * weight
 //   E4M3 output: code = E4M3(y / s), s = max(max|y| / 448, 2^-64) per row or per group of columns
+//                (y times 1 / s, both in fp32: the quotient to 2^-22)
 //
 // The row stays in registers between the sum of squares and the store, so every operand is read
 // once and every result written once: the kernel is bound by that traffic for many rows and by one
-// chain of load, redmction and store for few.
+// chain of load, reduction and store for few.
 
 #include "ops_common.cuh"
 
@@ -32,7 +33,7 @@ struct NormParams {
     int rows, cols, group;  // group: columns per scale
     int tpr_log2;           // threads per row (vector kernel)
     float eps;
-    float shrink, mean_of;  // see mean_square below
+    float shrink, mean_of;  // see add_square
 };
 
 // The larger magnitude, NaN if either is: a NaN reaches the scale, as the quotient's definition wants.
