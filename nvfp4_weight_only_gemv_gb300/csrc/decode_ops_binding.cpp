@@ -61,9 +61,9 @@ struct Refused {};
     throw Refused{};
 }
 
-struct Checker {
+struct Checks {
     int dev = -2;  // the current CUDA device; no tensor is on -2
-    Checker() {
+    Checks() {
         c10::DeviceIndex current = 0;
         if (c10::cuda::GetDevice(&current) == cudaSuccess) dev = current;
     }
@@ -139,7 +139,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
 // (x, weight, eps, residual, residual_out, out, scales, group, stream)
 PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> int {
-        const Checker c;
+        const Checks c;
         nvfp4_rms_norm_args g{};
         const at::Tensor& x = c.any(a[0], "x", kWide, 2);
         g.rows = size32(x.size(0), "x");
@@ -180,7 +180,7 @@ struct Caches {
     const at::Tensor& k;
     const at::Tensor& v;
 };
-Caches caches(const Checker& c, PyObject* ko, PyObject* vo) {
+Caches caches(const Checks& c, PyObject* ko, PyObject* vo) {
     const at::Tensor& k = c.any(ko, "k_cache", kCache, 4);
     const at::Tensor& v = c.any(vo, "v_cache", kind(k), 4);
     same_shape(v, k, "v_cache", "k_cache");
@@ -195,7 +195,7 @@ Caches caches(const Checker& c, PyObject* ko, PyObject* vo) {
 //  k_norm, eps, k_scale, v_scale, out, stream)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 18, [&]() -> int {
-        const Checker c;
+        const Checks c;
         nvfp4_rope_append_args g{};
         const at::Tensor& k = c.any(a[1], "k", kWide, 3);
         const at::Tensor& v = c.any(a[2], "v", kind(k), 3);
@@ -263,7 +263,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (q, k_cache, v_cache, page_table, lengths, scale, window, k_scale, v_scale, workspace, out, lse, stream)
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 13, [&]() -> int {
-        const Checker c;
+        const Checks c;
         nvfp4_paged_attention_args g{};
         const at::Tensor& q = c.any(a[0], "q", kBf16, 3);
         const Caches cache = caches(c, a[1], a[2]);
