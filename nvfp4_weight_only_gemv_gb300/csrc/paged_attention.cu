@@ -556,6 +556,50 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, JoinShared& sh, 
     for (int row = threadIdx.x; row < rows_all; row += blockDim.x) __stcg(p.part_ml + to * rows_all + row, sh.ml[row]);
 }
 
+// The same for parts that do not fit into `room` at once, where a thread has more than 4 rows: as many rows
+// of all parts as do fit, turn by turn. us a call, read and this way: 64 rows of 128 values (16 a thread),
+// 300 keys 47.8 and 34.8, 20000 keys 84 and 79; E4M3, rows of 256 values 50.8 and 35.8, 121 and 106. With
+// two rows a thread it is slower: 1200 keys 12.6 and 14.4. Out of line: inside the common join it cost an E4M3 batch 2.5 %.
+__device__ __noinline__ void join_in_turns(const AttnParams& p, JoinShared& sh, char* room, int room_bytes, const Parts& parts,
+                                           int first, int step, int count, int to, int b, int column) {
+    const int rows_all = p.chunk_rows, quad = threadIdx.x & ((1 << p.quad_log2) - 1), d = 4 * quad;
+    const float vscale = value_scale(p, column);
+    const int fit = room_bytes / (count * (p.D * 4 + 8)), turns = (rows_all + fit - 1) / fit, most = (rows_all + turns - 1) / turns;
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(room));
+#pragma unroll 1
+    for (int row0 = 0; row0 < rows_all; row0 += most) {
+        const int rows = min(most, rows_all - row0), o_bytes = rows * p.D * 4, ml_bytes = rows * 8;
+#pragma unroll 1
+        for (int c = 0; c < count; ++c) {
+            const int64_t from = static_cast<int64_t>(parts.slot(first + c * step)) * rows_all + row0;
+            const char* const o = reinterpret_cast<const char*>(p.part_o + from * p.D);
+            const char* const ml = reinterpret_cast<const char*>(p.part_ml + from);
+            for (int i = 16 * threadIdx.x; i < o_bytes; i += 16 * blockDim.x)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + c * o_bytes + i), "l"(o + i) : "memory");
+            for (int i = 8 * threadIdx.x; i < ml_bytes; i += 8 * blockDim.x)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + count * o_bytes + c * ml_bytes + i), "l"(ml + i) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        float2* const ml = reinterpret_cast<float2*>(room + count * o_bytes);
+        weigh_parts(ml, rows, rows, count, sh.ml + row0);
+        __syncthreads();
+#pragma unroll 2
+        for (int row = threadIdx.x >> p.quad_log2; row < rows; row += blockDim.x >> p.quad_log2) {
+            if (d >= p.D) continue;
+            const float4 o = gather(ml + row, rows, room + (row * p.D + d) * 4, o_bytes, count);
+            if (to < 0) store_out(p, place_of_row(p, b, column, row0 + row), d, o, sh.ml[row0 + row].y, vscale);
+            else __stcg(reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(to) * rows_all + row0 + row) * p.D + d), o);
+        }
+        if (row0 + most < rows_all) __syncthreads();
+    }
+    if (to < 0) {
+        store_lse(p, b, column, sh.ml);
+        return;
+    }
+    for (int row = threadIdx.x; row < rows_all; row += blockDim.x) __stcg(p.part_ml + to * rows_all + row, sh.ml[row]);
+}
+
 // True in the CTA that is the last of `of` to come by `counter`, which it leaves at zero. The CTA's
 // stores come before its arrival, and the other CTAs' before what the last one reads.
 __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of) {
@@ -578,15 +622,22 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
     const Parts at{r.slot0, cta0};
     int* const done = p.counters + static_cast<int64_t>(r.seq) * p.columns + r.head;
     int size = parts;
+    auto join = [&](int first, int step, int count, int to) {
+        const int a_row = count * (p.D * 4 + 8);
+        if (join_turns(p) > 4 && p.chunk_rows * a_row > room_bytes && a_row <= room_bytes)
+            join_in_turns(p, sh, room, room_bytes, at, first, step, count, to, r.seq, r.head);
+        else
+            join_parts(p, sh, room, room_bytes, at, first, step, count, to, r.seq, r.head);
+    };
     if (parts > 4 && parts * join_turns(p) > kJoinOnce && (join_turns(p) == 1 || parts * part_bytes(p) > room_bytes)) {
         size = 3;
         while (size * size < parts) ++size;
         const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
         if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.columns + at.slot(first), count)) return;
-        join_parts(p, sh, room, room_bytes, at, first, 1, count, at.slot(first), r.seq, r.head);
+        join(first, 1, count, at.slot(first));
     }
     const int groups = (parts + size - 1) / size, of = size < parts ? groups : parts;
-    if (arrive_last(sh, done, of)) join_parts(p, sh, room, room_bytes, at, 0, size < parts ? size : 1, of, -1, r.seq, r.head);
+    if (arrive_last(sh, done, of)) join(0, size < parts ? size : 1, of, -1);
 }
 
 template <int DP, int NT, bool F8>
