@@ -356,8 +356,9 @@ nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream)
  * Scores and sums are fp32; weights enter the tensor cores with 16 bits (bf16 cache) or 11 (E4M3
  * cache).
  *   workspace: nvfp4_attention_workspace_bytes(...) bytes of device memory, 256-byte aligned. Its
- *   counters must be zero before its first use and every call leaves them at zero. Calls that
- *   share a workspace must be ordered.
+ *   counters must be zero before its first use and every call leaves them at zero; they stand at the
+ *   same place for all sizes, so calls of different sizes may share a workspace that is large enough
+ *   for each. Calls that share one must be ordered.
  * rows 1..8, head_dim <= 512, max_pages * page_size <= 2^24.
  */
 typedef struct {

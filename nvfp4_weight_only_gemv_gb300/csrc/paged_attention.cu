@@ -36,7 +36,7 @@ struct AttnParams {
     int seqs, rows, hq, hk, group, D, pages, max_pages, page, window, fp8;
     float scale;
     // tile kernel
-    int* counters;              // workspace: arrivals per (sequence, kv head), then per part; zero between calls
+    int* counters;              // workspace: arrivals, two per slot of a part: see kCtasPerSm; zero between calls
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
     float2* part_ml;            // workspace: (m, l) [2 * grid][rows * group]
     int wide_box, tall_box;     // one copy brings all of a block's boxes; all blocks of a tile
@@ -88,6 +88,10 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kAlignSlack = 3;  // units
 constexpr int kMaxGroup = 1024;  // query heads per kv head: 8 group^2 < 2^24, see place_of_row
 constexpr int kJoinOnce = 32;  // parts times rows that a thread joins in a single step
+// The most CTAs an SM takes in any plan. A CTA has two slots for parts, and a slot two counters: of the item and of
+// the group of parts that it is the first of (an item that is cut is the only one to have its first
+// part there). So the counters' extent is the device's alone, and every shape finds them at zero.
+constexpr int kCtasPerSm = 3;
 
 // One CTA per (query row, query head); each warp takes every fourth key. Any head size up to 512,
 // any page size, any alignment.
@@ -204,7 +208,7 @@ struct TileShape {
     static constexpr int kMT = DP / 16;                    // 16-dim blocks of O
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
-    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? 3 : 2;  // per SM
+    static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? kCtasPerSm : 2;  // per SM
     static constexpr bool kQRegs = NT * DP <= 256;
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
     static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
@@ -620,7 +624,7 @@ __device__ __forceinline__ bool arrive_last(JoinShared& sh, int* counter, int of
 __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, const Run& r, char* room, int room_bytes) {
     const int cta0 = r.cta0, parts = r.parts;
     const Parts at{r.slot0, cta0};
-    int* const done = p.counters + static_cast<int64_t>(r.seq) * p.columns + r.head;
+    int* const done = p.counters + 2 * at.slot(0);
     int size = parts;
     auto join = [&](int first, int step, int count, int to) {
         const int a_row = count * (p.D * 4 + 8);
@@ -633,7 +637,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
         size = 3;
         while (size * size < parts) ++size;
         const int first = (static_cast<int>(blockIdx.x) - cta0) / size * size, count = min(size, parts - first);
-        if (!arrive_last(sh, p.counters + static_cast<int64_t>(p.seqs) * p.columns + at.slot(first), count)) return;
+        if (!arrive_last(sh, p.counters + 2 * at.slot(first) + 1, count)) return;
         join(first, 1, count, at.slot(first));
     }
     const int groups = (parts + size - 1) / size, of = size < parts ? groups : parts;
@@ -1329,7 +1333,7 @@ bool plan_tile(int dim, int rows, TilePlan* out) {
     t.chunk_rows = (rows + t.chunks - 1) / t.chunks;
     t.nt = t.dp == 256 || t.chunk_rows <= 8 ? 1 : t.chunk_rows <= 16 ? 2 : 4;
     while (8 * t.nt * t.row_blocks < t.chunk_rows) t.row_blocks *= 2;
-    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? 3 : 2;
+    t.ctas_per_sm = t.dp == 256 ? 1 : t.nt * t.dp <= 128 ? kCtasPerSm : 2;
     *out = t;
     return true;
 }
@@ -1339,9 +1343,10 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 struct Workspace {
     int64_t part_o, part_ml, bytes;
 };
-Workspace workspace_of(const TilePlan& t, int grid, int seqs, int kv_heads, int dim) {
+Workspace workspace_of(const TilePlan& t, int sms, int dim) {
     Workspace w;
-    w.part_o = align256((static_cast<int64_t>(seqs) * kv_heads * t.chunks + 2ll * grid) * 4);
+    const int grid = t.ctas_per_sm * sms;
+    w.part_o = align256(4ll * kCtasPerSm * sms * 4);
     w.part_ml = w.part_o + align256(2ll * grid * t.chunk_rows * dim * 4);
     w.bytes = w.part_ml + align256(2ll * grid * t.chunk_rows * 8);
     return w;
@@ -1404,7 +1409,7 @@ extern "C" int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_hea
     TilePlan t;
     const int rows_all = kv_heads ? rows * (q_heads / kv_heads) : 0;
     if (!plan_tile(head_dim, rows_all, &t)) return 256;  // one CTA per row and head: nothing to join
-    return workspace_of(t, t.ctas_per_sm * sm_count(), seqs, kv_heads, head_dim).bytes;
+    return workspace_of(t, sm_count(), head_dim).bytes;
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* a, void* stream) {
@@ -1446,7 +1451,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         aligned(p.out, 8) && p.pages > 0 && p.page_stride[0] > 0 && p.page_stride[1] > 0 &&
         p.page_stride[0] * es < (1ll << 40) && p.page_stride[1] * es < (1ll << 40)) {
         const int grid = t.ctas_per_sm * sm_count();
-        const Workspace w = workspace_of(t, grid, p.seqs, p.hk, p.D);
+        const Workspace w = workspace_of(t, sm_count(), p.D);
         p.chunks = t.chunks; p.chunk_rows = t.chunk_rows; p.columns = p.hk * t.chunks;
         char* base = static_cast<char*>(a->workspace);
         p.counters = reinterpret_cast<int*>(base);

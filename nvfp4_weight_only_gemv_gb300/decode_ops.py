@@ -169,8 +169,8 @@ def attention_workspace_bytes(seqs: int, rows: int, q_heads: int, kv_heads: int,
 
 
 def attention_workspace(seqs: int, rows: int, q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
-    """A zeroed workspace for paged_attention (uint8). Reuse it: every call leaves its counters at
-    zero. Calls that share one must be ordered."""
+    """A zeroed workspace for paged_attention (uint8). Reuse it, also for other sizes that need no more
+    bytes: every call leaves its counters at zero. Calls that share one must be ordered."""
     n = attention_workspace_bytes(seqs, rows, q_heads, kv_heads, head_dim)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 

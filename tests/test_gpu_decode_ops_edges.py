@@ -1,0 +1,45 @@
+"""Where the decode step's operators can go wrong beyond single calls of ordinary sizes and values.
+
+Tolerances come from the arithmetic, before any run, with the units of test_gpu_decode_ops.
+"""
+import math
+
+import pytest
+import torch
+
+import nvfp4_weight_only_gemv_gb300 as nv
+from test_gpu_decode_ops import BF16, DEV, FP8, _attend_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- one workspace, several shapes
+
+def _shape(lengths, rows, hq, hk, D, cache, seed):
+    q, kc, vc, table, ln, ks, vs = _attend_inputs(lengths, rows, hq, hk, D, cache, 16, seed)
+
+    def call(ws):
+        out, lse = torch.full_like(q, math.nan), torch.full((q.shape[0], hq), math.nan, device=DEV)
+        nv.paged_attention(q, kc, vc, table, ln, k_scale=ks, v_scale=vs, workspace=ws, out=out, lse=lse)
+        return out, lse
+
+    return call, nv.attention_workspace_bytes(len(lengths), rows, hq, hk, D)
+
+
+@pytest.mark.parametrize("a,b", [
+    # as many parts as there are CTAs: 3, 2 and 1 of them an SM
+    (([20000], 4, 32, 8, 128, BF16), ([20000], 1, 32, 8, 128, BF16)),
+    (([9000], 8, 16, 2, 64, BF16), ([9000], 1, 4, 1, 256, FP8)),
+    # few items, then many: a batch that grows and shrinks
+    (([3000], 1, 32, 8, 128, FP8), ([200 + i for i in range(128)], 1, 32, 8, 128, FP8)),
+    (([700] * 3, 2, 64, 1, 64, BF16), ([150] * 40, 8, 16, 2, 128, BF16)),
+])
+def test_attention_workspace_serves_every_shape(a, b):
+    calls = [_shape(*a, seed=3), _shape(*b, seed=4)]
+    want = [call(torch.zeros(n, dtype=torch.uint8, device=DEV)) for call, n in calls]
+    ws = torch.zeros(max(n for _, n in calls), dtype=torch.uint8, device=DEV)
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        got = calls[i][0](ws)
+        for g, w in zip(got, want[i]):
+            assert torch.equal(g, w), f"shape {i}: {int(torch.isnan(g).sum())} values were never written"
+    assert nv.device_status() == 0
