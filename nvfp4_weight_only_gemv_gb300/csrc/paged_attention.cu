@@ -1439,7 +1439,10 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     p.q_ts = a->q_token_stride; p.q_hs = a->q_head_stride;
     p.seqs = a->seqs; p.rows = a->rows; p.hq = a->q_heads; p.hk = a->kv_heads; p.group = a->q_heads / a->kv_heads;
     p.D = a->head_dim; p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
-    p.window = a->window; p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
+    // no row stands further than that from its sequence's first key, and the kernels may subtract it in 32 bits
+    const int64_t reach = static_cast<int64_t>(a->max_pages) * a->page_size + kMaxRows;
+    p.window = static_cast<int>(a->window < reach ? a->window : reach);
+    p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
     const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
     TilePlan t;
     const bool tiles = host_variant() != 1 && p.group <= kMaxGroup && plan_tile(p.D, rows_all, &t);

@@ -43,3 +43,18 @@ def test_attention_workspace_serves_every_shape(a, b):
         for g, w in zip(got, want[i]):
             assert torch.equal(g, w), f"shape {i}: {int(torch.isnan(g).sum())} values were never written"
     assert nv.device_status() == 0
+
+
+# --------------------------------------------------------------------------- windows without an end
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("rows", [4, 8])
+def test_the_widest_window_is_no_window(rows, page, cache):
+    # sequences shorter than the rows too: their first row stands at a position below zero
+    q, kc, vc, table, ln, ks, vs = _attend_inputs([0, 1, 300, rows - 1], rows, 8, 2, 128, cache, page, 9)
+    want = nv.paged_attention(q, kc, vc, table, ln, k_scale=ks, v_scale=vs)
+    for window in (2 ** 31 - 1, 2 ** 31 - rows, 1 << 24, 300):
+        got = nv.paged_attention(q, kc, vc, table, ln, window=window, k_scale=ks, v_scale=vs)
+        assert torch.equal(got, want), window
+    assert nv.device_status() == 0
