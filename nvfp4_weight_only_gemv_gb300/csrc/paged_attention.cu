@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t
 }
 
 constexpr int kScalarWarps = 4;
-constexpr float kTiny = 7.52316385e-37f;  // 2^-120
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kAlignSlack = 3;  // units
@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 // Next to bf16 values they enter the products as two bf16 numbers, 16 bits in all: rounded to one,
 // the output was 1.35 times as far from 64 bits as fp32's, and the second product costs nothing that
 // can be measured (131071 keys: 88.9 us with one, 88.7 with two). The first is rounded down and the
-// second kept above zero, so that an infinite value stays infinite. Next to E4M3 values they are f16,
-// at most 2^8 and far inside its range, 11 bits against the values' 4.
+// second kept at 2^-126 or more, so that an infinite value stays infinite; that is as much as exp2's
+// flush of smaller weights to zero takes away. Both are zero where the weight is, or a masked key's value
+// would reach the row. Next to E4M3 values they are f16, at most 2^8 and far inside its range, 11 bits
+// against the values' 4.
 //
 // The kernel is bound by the cache's bytes.
 //
@@ -1120,8 +1122,9 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                         } else {
                             const uint32_t word = pack_bf16_down(e[2 * r], e[2 * r + 1]);
                             pb[i][nt][r] = transpose8x8(word);
-                            pl[i][nt][r] = transpose8x8(pack_bf16(fmaxf(e[2 * r] - bf16_lo(word), kTiny),
-                                                                  fmaxf(e[2 * r + 1] - bf16_hi(word), kTiny)));
+                            // weights are zero or 2^-126 and more
+                            pl[i][nt][r] = transpose8x8(pack_bf16(fmaxf(e[2 * r] - bf16_lo(word), fminf(e[2 * r], kTiny)),
+                                                                  fmaxf(e[2 * r + 1] - bf16_hi(word), fminf(e[2 * r + 1], kTiny))));
                         }
                     }
                 }

@@ -58,3 +58,38 @@ def test_the_widest_window_is_no_window(rows, page, cache):
         got = nv.paged_attention(q, kc, vc, table, ln, window=window, k_scale=ks, v_scale=vs)
         assert torch.equal(got, want), window
     assert nv.device_status() == 0
+
+
+# ------------------------------------------------------------- what a row does not see, finite
+
+@pytest.mark.parametrize("window", [0, 24])
+@pytest.mark.parametrize("rows,D", [(4, 128), (8, 64), (2, 256)])
+@pytest.mark.parametrize("value", [3e38, -3e38])
+def test_huge_values_behind_the_mask_do_not_reach_a_row(rows, D, window, value):
+    # the newest key (and, with a window, old ones) hold the largest values: rows that do not see them
+    # are, bit for bit, as without
+    n, page, hk = 61, 16, 2
+    q, kc, vc, table, ln, _, _ = _attend_inputs([n], rows, 8, hk, D, BF16, page, 21)
+    clean = nv.paged_attention(q, kc, vc, table, ln, window=window)
+    old = [n - 1] + ([n - rows - 23, n - 26] if window else [])
+    for j in old:
+        vc[int(table[0, j // page]), :, j % page] = value
+    got = nv.paged_attention(q, kc, vc, table, ln, window=window)
+    for r in range(rows):
+        at = n - rows + r
+        if not any(j <= at and (not window or j > at - window) for j in old):
+            assert torch.equal(got[r], clean[r]), (r, float((got[r].float() - clean[r].float()).abs().max()))
+    assert nv.device_status() == 0
+
+
+def test_huge_values_under_a_vanished_weight():
+    # a key 200 nats below the others weighs e^-200 = 0 in fp32, and 3e38 times that is nothing
+    n, D = 40, 64
+    q, kc, vc, table, ln, _, _ = _attend_inputs([n], 1, 2, 1, D, BF16, 16, 5)
+    q.fill_(1.0)
+    p, s = int(table[0, 1]), 4
+    kc[p, 0, s] = -25.0  # -25 * 64 / 8 = -200
+    vc[p, 0, s] = 3e38
+    got = nv.paged_attention(q, kc, vc, table, ln)
+    vc[p, 0, s] = 0.0
+    assert torch.equal(got, nv.paged_attention(q, kc, vc, table, ln))
