@@ -354,7 +354,7 @@ nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream)
  * see never reach it, whatever they hold. A length outside [0, max_pages * page_size] or a page
  * outside [0, pages) sets NVFP4_DEV_BAD_PAGE; the length is clamped, the page's keys are not read.
  * Scores and sums are fp32; weights enter the tensor cores with 16 bits (bf16 cache) or 11 (E4M3
- * cache).
+ * cache; below 2^-21 of the row's largest, with an error of 2^-32 of it).
  *   workspace: nvfp4_attention_workspace_bytes(...) bytes of device memory, 256-byte aligned. Its
  *   counters must be zero before its first use and every call leaves them at zero; they stand at the
  *   same place for all sizes, so calls of different sizes may share a workspace that is large enough

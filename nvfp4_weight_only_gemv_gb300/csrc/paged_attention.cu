@@ -84,6 +84,7 @@ __device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t
 constexpr int kScalarWarps = 4;
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 constexpr float kSlack = 8.0f; // how far a score may pass the reference maximum, in powers of two
+constexpr float kLift = 7.0f;  // powers of two that f16 weights are raised by
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kAlignSlack = 3;  // units
 constexpr int kMaxGroup = 1024;  // query heads per kv head: 8 group^2 < 2^24, see place_of_row
@@ -189,8 +190,10 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
 // can be measured (131071 keys: 88.9 us with one, 88.7 with two). The first is rounded down and the
 // second kept at 2^-126 or more, so that an infinite value stays infinite; that is as much as exp2's
 // flush of smaller weights to zero takes away. Both are zero where the weight is, or a masked key's value
-// would reach the row. Next to E4M3 values they are f16, at most 2^8 and far inside its range, 11 bits
-// against the values' 4.
+// would reach the row. Next to E4M3 values they are f16, 11 bits against the values' 4, and times 2^7:
+// at most 2^15, inside f16's range, and at least 2^7 where a score is the reference, so that a weight is
+// off by no more than 2^-32 of the largest where f16's steps of 2^-24 end. (Not raised, the tail behind a key
+// 2^26 times as heavy was lost from the sums of the values and not from l.)
 //
 // The kernel is bound by the cache's bytes.
 //
@@ -652,6 +655,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
     using T = TileShape<DP, NT, F8>;
     constexpr int H = T::kHalves, W = T::kWarps, kThreads = W * 32;
     constexpr int kRowsW = 8 * NT;
+    constexpr float lift = F8 ? kLift : 0.0f;
     extern __shared__ uint8_t smem_raw[];
     // rings [W][kStages][K, V], on a boundary of the swizzle's pattern; then s_q
     float* const smem = reinterpret_cast<float*>(smem_raw + (-static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u));
@@ -1107,7 +1111,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
             uint32_t pb[H][NT][2], pl[H][NT][2];  // weights; bf16: their first and last 8 bits
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0], m1 = mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1];
+                const float m0 = (mx[nt][0] == -INFINITY ? 0.0f : mx[nt][0]) - lift, m1 = (mx[nt][1] == -INFINITY ? 0.0f : mx[nt][1]) - lift;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     float e[4];
@@ -1261,7 +1265,7 @@ paged_attention_tile_kernel(const __grid_constant__ TileParams p) {
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 const int r = 8 * nt + 2 * t + c;
-                if (g == 0) s_ml[warp * kRowsW + r] = make_float2(mx[nt][c], v);
+                if (g == 0) s_ml[warp * kRowsW + r] = make_float2(mx[nt][c] - lift, v);  // what l and o refer to
 #pragma unroll
                 for (int x = 0; x < T::kMT / 2; ++x) {
                     const int d = !F8 ? 64 * (x >> 1) + 8 * g + 4 * (x & 1) : DP == 64 ? 8 * g + 4 * x : 128 * (x >> 2) + 16 * g + 4 * (x & 3);

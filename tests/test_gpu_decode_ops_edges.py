@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import nvfp4_weight_only_gemv_gb300 as nv
-from test_gpu_decode_ops import BF16, DEV, FP8, _attend_inputs
+from test_gpu_decode_ops import BF16, DEV, FP8, U16, U32, _attend_inputs, _gen, _randn, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,41 @@ def test_huge_values_under_a_vanished_weight():
     got = nv.paged_attention(q, kc, vc, table, ln)
     vc[p, 0, s] = 0.0
     assert torch.equal(got, nv.paged_attention(q, kc, vc, table, ln))
+
+
+# --------------------------------------------------------------------- weights far below the largest
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("rows,group,D", [(1, 4, 128), (4, 1, 64), (8, 4, 128), (2, 1, 256)])
+def test_a_long_tail_behind_one_heavy_key(cache, rows, group, D):
+    # one key outweighs each other by 2^26 and holds zeros: the output is the tail's alone. So many items that a
+    # warp takes a good part of one. A weight is off by 2^-15 of itself (two bf16 numbers) or 2^-11
+    # (f16), and, f16, by half a step of 2^-24 where the largest is at least 2^7: 2^-32 of the largest.
+    n, page, hk, seqs = 4000, 16, 64, 8
+    g = _gen(n + D + rows)
+    kc, vc = nv.kv_cache(n // page, hk, page, D, cache)
+    kc.copy_((_randn(kc.shape, g) * 0.02).to(cache))
+    vc.copy_((0.5 + torch.rand(vc.shape, generator=g, device=DEV)).to(cache))
+    kc[0, :, 5] = torch.full((D,), 18.0 / D ** 0.5, device=DEV).to(cache)  # 26 log 2 = 18.02
+    vc[0, :, 5] = torch.zeros(D, device=DEV).to(cache)
+    q = torch.ones((seqs * rows, hk * group, D), dtype=BF16, device=DEV)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).expand(seqs, -1)
+    ln = torch.full((seqs,), n, dtype=torch.int32, device=DEV)
+    lse = torch.empty((seqs * rows, hk * group), device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, ln, lse=lse)
+    assert nv.device_status() == 0
+    got, lse = got.view(seqs, rows, hk, group, D), lse.view(seqs, rows, hk, group)
+    keys, vals = (c.double().transpose(0, 1).reshape(hk, n, D) for c in (kc, vc))
+    for r in range(rows):
+        hi = n - rows + r + 1
+        z = keys[:, :hi].sum(dim=2) * D ** -0.5  # every query is ones
+        p = torch.softmax(z, 1)
+        ref = torch.einsum("hk,hkd->hd", p, vals[:, :hi])  # no value is below zero: also the sum of magnitudes
+        # fp32 dot products, and at most hi / 16 terms of a sum in a row
+        dz = float((D + 8) * U32 * keys[:, :hi].abs().sum(dim=2).max() * D ** -0.5) + float(z.abs().max()) * 4 * U32
+        tol = ref * (U16 + 2 * dz + (2.0 ** -15 if cache is BF16 else 2.0 ** -11) + (hi / 16 + 16) * U32)
+        if cache is FP8:
+            tol = tol + 2.0 ** -32 * vals[:, :hi].sum(dim=1)
+        _within(got[:, r], ref[None, :, None].expand(seqs, -1, group, -1), tol[None, :, None], "out")
+        want = torch.logsumexp(z, dim=1)[None, :, None].expand(seqs, -1, group)
+        _within(lse[:, r], want, dz + (hi / 16 + 16) * U32 + want.abs() * 4 * U32, "lse")
