@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import nvfp4_weight_only_gemv_gb300 as nv
-from test_gpu_decode_ops import BF16, DEV, FP8, U16, U32, _attend_inputs, _gen, _randn, _within
+from test_gpu_decode_ops import BF16, DEV, FP8, U16, U32, _attend_inputs, _check_attend, _gen, _randn, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,22 @@ def test_a_long_tail_behind_one_heavy_key(cache, rows, group, D):
         _within(got[:, r], ref[None, :, None].expand(seqs, -1, group, -1), tol[None, :, None], "out")
         want = torch.logsumexp(z, dim=1)[None, :, None].expand(seqs, -1, group)
         _within(lse[:, r], want, dz + (hi / 16 + 16) * U32 + want.abs() * 4 * U32, "lse")
+
+
+# ------------------------------------------------------------------- CTAs that take several items
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("rows,hq,hk,D", [(1, 8, 8, 128), (4, 32, 8, 128), (8, 32, 8, 128), (8, 16, 8, 64), (1, 8, 8, 64),
+                                          (4, 16, 8, 256), (8, 40, 4, 128), (3, 64, 4, 96)])
+def test_ctas_that_walk_through_items(cache, rows, hq, hk, D):
+    # more (sequence, kv head) items than whole ones fit the CTAs, of unequal lengths: runs begin and end
+    # inside items, and a CTA's rings, query rows and joins follow one another; up to 32 sequences
+    # and beyond take their schedule on different ways
+    for seqs in (32, 33):
+        _check_attend([(1000 + 397 * i) % 2100 for i in range(seqs)], rows, hq, hk, D, cache, 32 if seqs == 32 else 16, seed=rows + D)
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("rows", [1, 8])
+def test_ctas_that_walk_through_windows(cache, rows):
+    _check_attend([(500 + 1237 * i) % 5000 for i in range(30)], rows, 32, 8, 128, cache, 16, window=1500, seed=rows)
