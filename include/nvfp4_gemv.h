@@ -309,9 +309,9 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  *     n * inv_freq[i]: (a, b) -> (a c - b s, b c + a s) with c, s = mscale * cos, sin;
  *     the head's values from 2 * rotary_half on pass through.
  * q_out [tokens, q_heads, head_dim] bf16 receives q (q = NULL: no queries). k and v go to row
- * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale), to
- * nearest even (the quotient to 2^-22), clamped to +-448; scales are positive normal numbers. Long-context scalings of the frequencies are the caller's, in
- * inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
+ * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale) (an fp32
+ * quotient, to nearest even, clamped to +-448; scales are positive). Long-context scalings of the
+ * frequencies are the caller's, in inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
  * row is zero. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
  * nothing. Two tokens of one call at the same sequence and position leave either's values.
  * q, k, v: [tokens, heads, head_dim] with unit stride inside a head and the given strides between

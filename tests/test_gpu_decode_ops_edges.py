@@ -150,3 +150,30 @@ def test_ctas_that_walk_through_items(cache, rows, hq, hk, D):
 @pytest.mark.parametrize("rows", [1, 8])
 def test_ctas_that_walk_through_windows(cache, rows):
     _check_attend([(500 + 1237 * i) % 5000 for i in range(30)], rows, 32, 8, 128, cache, 16, window=1500, seed=rows)
+
+
+# ---------------------------------------------------------------------------------- 8-bit appends
+
+@pytest.mark.parametrize("variant", [0, 1])
+def test_appended_codes_are_the_quotients(variant):
+    # values at and beside the middle of two codes, where a quotient off by a unit takes the other one; scales
+    # down to the smallest
+    g = _gen(77)
+    T, hk, D = 64, 16, 128
+    scale = torch.rand(hk, generator=g, device=DEV) * 0.9 + 0.05
+    scale[3], scale[7] = 2.0 ** -126, 2.0 ** -140
+    mid = torch.tensor([(8 + m + 0.5) / 8 * 2.0 ** e for m in range(8) for e in range(-6, 8)], device=DEV)
+    x = mid[torch.randint(len(mid), (T, hk, D), generator=g, device=DEV)] * scale[:, None]
+    kc, vc = nv.kv_cache(4, hk, 16, D, FP8)
+    table = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    nv.set_variant(variant)
+    try:
+        nv.rope_append(None, x, -x, pos, torch.empty(0, device=DEV), kc, vc, table, k_scale=scale, v_scale=scale)
+    finally:
+        nv.set_variant(0)
+    want = (x / scale[:, None]).clamp(-448, 448)
+    for c, ref in ((kc, want), (vc, -want)):
+        rows = c.transpose(1, 2).reshape(T, hk, D)
+        assert torch.equal(rows.view(torch.uint8), ref.to(FP8).view(torch.uint8)), int((rows.float() != ref.to(FP8).float()).sum())
+    assert nv.device_status() == 0
