@@ -153,6 +153,23 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _on_stream(stream, call, *args, **kwargs):
+    """call(...) with ``stream`` (a torch stream or a handle) as the current stream: what the call allocates
+    is then memory whose earlier uses come before it in that stream, and a workspace's next user there
+    comes after it. New tensors that it returns are marked as used by the caller's stream too."""
+    caller = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (handle 0 is the default stream; an ExternalStream of 0 would be a new one)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        got = call(*args, **kwargs)
+    given = {id(a) for a in (*args, *kwargs.values())}
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and id(t) not in given:
+            t.record_stream(caller)
+    return got
+
+
 def _need(t: torch.Tensor, name: str, dtype, ndim: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

@@ -84,6 +84,9 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out
     type. ``out`` (or ``out_dtype``) is float32, bfloat16 or float8_e4m3fn; 8-bit rows come with
     float32 ``scales`` [rows, 1], or [rows, cols / group] for ``group`` columns each (a power of two,
     16 to 256). Rows may be strided. Returns RMSNormOut(y, residual, scales)."""
+    if stream is not None and (out is None or (residual is not None and residual_out is None) or
+                               (scales is None and getattr(out, "dtype", None) is _E4M3)):
+        return _nv._on_stream(stream, rms_norm, x, weight, eps, residual, residual_out, out, out_dtype, scales, group)
     if out is None:
         out = _like(x, "x", out_dtype)
     if residual_out is None and residual is not None:
@@ -149,6 +152,10 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_
     turns the first 2 * half values of a head, in halves or ``interleaved`` pairs; mscale multiplies
     cos and sin (rope_frequencies gives both). q_norm, k_norm [D]: root-mean-square norm of each
     head first. k_scale, v_scale float32 [kv_heads]: what an 8-bit cache's values are divided by."""
+    if stream is not None and out is None:
+        return _nv._on_stream(stream, rope_append, q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_ids,
+                              interleaved=interleaved, mscale=mscale, q_norm=q_norm, k_norm=k_norm, eps=eps,
+                              k_scale=k_scale, v_scale=v_scale)
     if out is None and q is not None:
         out = _like(q, "q", _BF16)
     if stream is not None:
@@ -197,6 +204,9 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     the log of each row's sum of exponentials. ``workspace``: a uint8 tensor zeroed before its first
     use, of at least attention_workspace_bytes; None allocates one for this call. Returns bfloat16
     like q; rows that see no key are zero (lse -inf)."""
+    if stream is not None and (out is None or workspace is None):
+        return _nv._on_stream(stream, paged_attention, q, k_cache, v_cache, page_table, lengths, scale, window=window,
+                              k_scale=k_scale, v_scale=v_scale, workspace=workspace, out=out, lse=lse)
     if out is None:
         out = _like(q, "q", _BF16)
     if workspace is None:

@@ -177,3 +177,58 @@ def test_appended_codes_are_the_quotients(variant):
         rows = c.transpose(1, 2).reshape(T, hk, D)
         assert torch.equal(rows.view(torch.uint8), ref.to(FP8).view(torch.uint8)), int((rows.float() != ref.to(FP8).float()).sum())
     assert nv.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------ other streams
+
+def _owner(t):
+    """The stream whose memory pool a tensor's block belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_call_on_another_stream_does_not_use_the_current_one(handle):
+    # the current stream is busy and its pool's free blocks are full of ones: a workspace zeroed there would be
+    # ready after the kernel on the side stream had counted in it
+    q, kc, vc, table, ln, _, _ = _attend_inputs([3000, 30], 1, 8, 2, 128, BF16, 16, 7)
+    x, r, w = q.view(2, -1), q.view(2, -1).clone(), torch.ones(1024, device=DEV)
+    pos, freq = ln - 1, torch.empty(0, device=DEV)
+    k = q[:, :2].contiguous()
+    want = nv.paged_attention(q, kc, vc, table, ln)
+    normed = nv.rms_norm(x, w, residual=r, out_dtype=FP8)
+    nv.rope_append(q, k, k, pos, freq, kc.clone(), vc.clone(), table)  # a kernel's first launch may wait for the device
+    side = torch.cuda.Stream()
+    on = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    n = nv.attention_workspace_bytes(2, 1, 8, 2, 128)
+    blocks = [torch.full((n,), 0xff, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    del blocks
+    torch.cuda._sleep(200_000_000)  # 0.1 s of the current stream
+    got = nv.paged_attention(q, kc, vc, table, ln, stream=on)
+    norm2 = nv.rms_norm(x, w, residual=r, out_dtype=FP8, stream=on)
+    turned = nv.rope_append(q, k, k, pos, freq, kc, vc, table, stream=on)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query(), "waited for the current stream"
+    for t in (got, *norm2, turned):
+        assert _owner(t) == side.cuda_stream
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(turned, q)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(norm2, normed))
+    assert nv.device_status() == 0
+
+
+def test_a_call_on_another_stream_keeps_what_it_is_given():
+    q, kc, vc, table, ln, _, _ = _attend_inputs([300, 30], 1, 8, 2, 128, BF16, 16, 7)
+    want = nv.paged_attention(q, kc, vc, table, ln)
+    side, ws = torch.cuda.Stream(), nv.attention_workspace(2, 1, 8, 2, 128)
+    torch.cuda.synchronize()
+    for kw in (dict(), dict(workspace=ws), dict(out=torch.empty_like(q)), dict(workspace=ws, out=torch.empty_like(q))):
+        got = nv.paged_attention(q, kc, vc, table, ln, stream=side, **kw)
+        side.synchronize()
+        assert torch.equal(got, want) and (got is kw["out"] if "out" in kw else _owner(got) == side.cuda_stream)
+    got = nv.paged_attention(q, kc, vc, table, ln, stream=0)  # the default stream's handle
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and _owner(got) == 0
