@@ -218,6 +218,8 @@ def _ptr(t):
 def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, out=None,
          out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """y[M, N] = g * dequant(w, s) @ x^T on the current (or given) CUDA stream."""
+    if stream is not None and out is None:
+        return _on_stream(stream, gemv, w, s, g, x, None, out_dtype)
     _need(w, "w", torch.uint8, 2)
     _need(s, "s", torch.uint8, 2)
     _need(x, "x", torch.bfloat16, 2)
@@ -236,6 +238,8 @@ def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, out=None,
 def gemv_gate_up(wg, sg, gg, wu, su, gu, x, out=None, out_dtype=torch.float32,
                  stream=None) -> torch.Tensor:
     """y[M, 2N] = [gg * W_gate . x | gu * W_up . x] in one launch."""
+    if stream is not None and out is None:
+        return _on_stream(stream, gemv_gate_up, wg, sg, gg, wu, su, gu, x, None, out_dtype)
     for t, n in ((wg, "w_gate"), (wu, "w_up")):
         _need(t, n, torch.uint8, 2)
     for t, n in ((sg, "s_gate"), (su, "s_up")):
@@ -259,6 +263,8 @@ def gemv_gate_up_swiglu(wg, sg, gg, wu, su, gu, x, clamp_limit: float = float("i
                         out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y[M, N] = silu(c(gg * W_gate . x)) * c(gu * W_up . x), c = clamp to [-clamp_limit,
     clamp_limit] (inf: none), in one launch; the gate|up product is never written."""
+    if stream is not None and out is None:
+        return _on_stream(stream, gemv_gate_up_swiglu, wg, sg, gg, wu, su, gu, x, clamp_limit, None, out_dtype)
     for t, n in ((wg, "w_gate"), (wu, "w_up")):
         _need(t, n, torch.uint8, 2)
     for t, n in ((sg, "s_gate"), (su, "s_up")):
@@ -299,6 +305,8 @@ def ffn_swiglu(wg, sg, gg, wu, su, gu, wd, sd, gd, x, clamp_limit: float = float
     wg, wu uint8 [I, H/2], sg, su [I, H/16]; wd [H, I/2], sd [H, I/16]; x bf16 [M, H]; y [M, H].
     ``workspace`` (from ffn_workspace) holds the launch's counters and h (bf16 [M, I] at byte
     2048); None allocates a zeroed one for this call. Calls sharing a workspace must be ordered."""
+    if stream is not None and (out is None or workspace is None):
+        return _on_stream(stream, ffn_swiglu, wg, sg, gg, wu, su, gu, wd, sd, gd, x, clamp_limit, workspace, out, out_dtype)
     for t, n in ((wg, "w_gate"), (wu, "w_up"), (wd, "w_down")):
         _need(t, n, torch.uint8, 2)
     for t, n in ((sg, "s_gate"), (su, "s_up"), (sd, "s_down")):
@@ -329,6 +337,8 @@ def ffn_swiglu_static(wg, sg, gg, wu, su, gu, wd, sd, gd, x, clamp_limit: float 
                       out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """ffn_swiglu with the library's own 256 KB device array as the workspace (nothing allocated
     by the caller). Calls on a device share that array: they must not overlap in time."""
+    if stream is not None and out is None:
+        return _on_stream(stream, ffn_swiglu_static, wg, sg, gg, wu, su, gu, wd, sd, gd, x, clamp_limit, None, out_dtype)
     for t, n in ((wg, "w_gate"), (wu, "w_up"), (wd, "w_down")):
         _need(t, n, torch.uint8, 2)
     for t, n in ((sg, "s_gate"), (su, "s_up"), (sd, "s_down")):
@@ -358,6 +368,8 @@ def moe_gemv(w, s, gs, ids, x, x_per_slot: bool, top_k: int, out=None, out_dtype
     x bf16 [T, K] (x_per_slot False) or [T*top_k, K] (True). ``status`` is an optional
     int32 CUDA tensor of one element that receives device status bits.
     """
+    if stream is not None and out is None:
+        return _on_stream(stream, moe_gemv, w, s, gs, ids, x, x_per_slot, top_k, None, out_dtype, status)
     _need(w, "w", torch.uint8, 3)
     _need(s, "s", torch.uint8, 3)
     _need(gs, "global_scales", torch.float32, 1)
@@ -420,6 +432,8 @@ def gemv_sdict(w: torch.Tensor, idx: torch.Tensor, sdict: torch.Tensor, g: float
                out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """gemv with dictionary scales: w uint8 [N, K/2], idx uint8 index plane [sdict_plane_bytes(N, K)],
     sdict uint8 [32] E4M3 codes."""
+    if stream is not None and out is None:
+        return _on_stream(stream, gemv_sdict, w, idx, sdict, g, x, None, out_dtype)
     _need(w, "w", torch.uint8, 2)
     _need(idx, "idx", torch.uint8, 1)
     _need(sdict, "sdict", torch.uint8, 1)
@@ -440,6 +454,8 @@ def gemv_sdict(w: torch.Tensor, idx: torch.Tensor, sdict: torch.Tensor, g: float
 def moe_gemv_sdict(w, idx, sdict, gs, ids, x, x_per_slot: bool, top_k: int, out=None, out_dtype=torch.float32,
                    status=None, stream=None) -> torch.Tensor:
     """moe_gemv with dictionary scales: idx uint8 [E, sdict_plane_bytes(N, K)], sdict uint8 [E, 32]."""
+    if stream is not None and out is None:
+        return _on_stream(stream, moe_gemv_sdict, w, idx, sdict, gs, ids, x, x_per_slot, top_k, None, out_dtype, status)
     _need(w, "w", torch.uint8, 3)
     _need(idx, "idx", torch.uint8, 2)
     _need(sdict, "sdict", torch.uint8, 2)
