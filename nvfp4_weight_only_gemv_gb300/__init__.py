@@ -120,11 +120,11 @@ def library(build_if_missing: bool = True):
     with _lock:
         if _lib is None:
             path = library_path()
-            if build_if_missing and path == _build.LIB_PATH and (_build.is_stale() or _build.binding_is_stale()):
+            if build_if_missing and path == _build.LIB_PATH and _build.is_stale():
                 try:
-                    _build.build()
+                    _build.build_library()
                 except RuntimeError:
-                    if not os.path.exists(path) or not os.path.exists(_build.BINDING_PATH):
+                    if not os.path.exists(path):
                         raise
             if not os.path.exists(path):
                 raise RuntimeError(f"NVFP4 GEMV CUDA library not found at {path}; run "

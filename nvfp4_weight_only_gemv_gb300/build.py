@@ -96,12 +96,18 @@ def _compile(out: str, extra: tuple = (), verbose: bool = False) -> None:
                 os.remove(f)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library and the Python binding of the decode operators, where they are missing or
-    older than their sources; return the library's path."""
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile the library if it is missing or older than its sources; return its path."""
     if force or is_stale():
         os.makedirs(LIB_DIR, exist_ok=True)
         _compile(LIB_PATH, verbose=verbose)
+    return LIB_PATH
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile the library and the Python binding of the decode operators, where they are missing or
+    older than their sources; return the library's path."""
+    build_library(force, verbose)
     build_binding(force)
     return LIB_PATH
 

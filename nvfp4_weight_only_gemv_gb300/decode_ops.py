@@ -44,7 +44,12 @@ def _load():
     """Loads the binding and gives it the loaded library's entry points."""
     global _native
     lib = _nv.library()
-    path = _build.build_binding()  # built with the library; here where that was another's
+    path = _build.BINDING_PATH
+    try:
+        _build.build_binding()
+    except RuntimeError:  # as for the library: one that is only older than its source serves
+        if not os.path.exists(path):
+            raise
     loader = importlib.machinery.ExtensionFileLoader("_decode_ops", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_decode_ops", path, loader=loader))
     loader.exec_module(module)

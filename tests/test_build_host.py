@@ -1,0 +1,71 @@
+"""What loads when only a part of the compiled files is there, in a copy of the package without a compiler."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+import nvfp4_weight_only_gemv_gb300 as nv
+from nvfp4_weight_only_gemv_gb300 import build
+
+NO_COMPILER = """
+import nvfp4_weight_only_gemv_gb300.build as b
+def missing():
+    raise RuntimeError("nvcc not found")
+b.nvcc_path = missing
+import nvfp4_weight_only_gemv_gb300 as nv, torch
+assert nv.__file__.startswith({root!r}), nv.__file__
+"""
+
+
+@pytest.fixture
+def copy(tmp_path):
+    """run(code): runs code in a copy of the package that has the library, without a compiler."""
+    nv.library()
+    name = os.path.basename(build.PKG_DIR)
+    skip = shutil.ignore_patterns("__pycache__", "_decode_ops*", "*.tmp*")
+    shutil.copytree(build.PKG_DIR, tmp_path / name, ignore=skip)
+    shutil.copytree(os.path.join(build.ROOT, "include"), tmp_path / "include")
+
+    def run(code):
+        env = {k: v for k, v in os.environ.items() if k != "PYTHONPATH"}
+        return subprocess.run([sys.executable, "-c", NO_COMPILER.format(root=str(tmp_path)) + code], cwd=tmp_path, env=env,
+                              capture_output=True, text=True, timeout=250)
+
+    run.root, run.package = tmp_path, tmp_path / name
+    return run
+
+
+def test_the_products_load_without_the_decode_operators_binding(copy):
+    out = copy("nv.library(); print(nv.describe_plan_host('dense', 1, 4096, 4096))")
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert out.stdout.strip()
+
+
+def test_the_decode_operators_name_what_is_missing(copy):
+    out = copy("""
+try:
+    nv.rms_norm(torch.zeros(1, 8), torch.ones(8))
+except RuntimeError as e:
+    print(e)
+""")
+    assert out.returncode == 0 and "nvcc not found" in out.stdout, out.stderr[-2000:]
+
+
+def test_an_older_library_serves_where_no_compiler_is(copy):
+    os.utime(copy.root / "include" / "nvfp4_gemv.h")  # every compiled file is now stale
+    out = copy("print(nv.describe_plan_host('dense', 1, 4096, 4096))")
+    assert out.returncode == 0, out.stderr[-2000:]
+
+
+def test_an_older_binding_serves_where_no_compiler_is(copy):
+    shutil.copy2(build.build_binding(), copy.package / "_build")
+    os.utime(copy.root / "include" / "nvfp4_gemv.h")
+    out = copy("""
+try:
+    nv.rms_norm(torch.zeros(1, 8), torch.ones(8))
+except ValueError as e:
+    print(e)
+""")
+    assert out.returncode == 0 and "CUDA tensor" in out.stdout, out.stderr[-2000:]
