@@ -15,7 +15,6 @@ BINDING = os.path.join(PKG_DIR, "csrc", "decode_ops_binding.cpp")
 SOURCES = (SRC, *OPERATORS, os.path.join(PKG_DIR, "csrc", "ops_common.cuh"), HEADER)
 LIB_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(LIB_DIR, "libnvfp4gemv.so")
-BINDING_PATH = os.path.join(LIB_DIR, "_decode_ops.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -40,7 +39,13 @@ def is_stale() -> bool:
     return not os.path.exists(LIB_PATH) or newest_source() > os.path.getmtime(LIB_PATH)
 
 
-def binding_command(out: str = BINDING_PATH) -> list:
+def binding_path() -> str:
+    """The binding's file, named after what it is compiled against: this torch and this Python."""
+    import torch
+    return os.path.join(LIB_DIR, f"_decode_ops.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def binding_command(out: str) -> list:
     """The Python module that checks the decode operators' tensors, built against the installed torch."""
     import torch
     root = os.path.dirname(torch.__file__)
@@ -56,20 +61,22 @@ def binding_command(out: str = BINDING_PATH) -> list:
 
 
 def binding_is_stale() -> bool:
-    return not os.path.exists(BINDING_PATH) or max(map(os.path.getmtime, (BINDING, HEADER))) > os.path.getmtime(BINDING_PATH)
+    path = binding_path()
+    return not os.path.exists(path) or max(map(os.path.getmtime, (BINDING, HEADER))) > os.path.getmtime(path)
 
 
 def build_binding(force: bool = False) -> str:
+    path = binding_path()
     if not force and not binding_is_stale():
-        return BINDING_PATH
+        return path
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = binding_command(tmp)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def _compile(out: str, extra: tuple = (), verbose: bool = False) -> None:

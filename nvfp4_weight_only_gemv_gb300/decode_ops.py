@@ -44,7 +44,7 @@ def _load():
     """Loads the binding and gives it the loaded library's entry points."""
     global _native
     lib = _nv.library()
-    path = _build.BINDING_PATH
+    path = _build.binding_path()
     try:
         _build.build_binding()
     except RuntimeError:  # as for the library: one that is only older than its source serves

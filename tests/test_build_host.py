@@ -69,3 +69,19 @@ except ValueError as e:
     print(e)
 """)
     assert out.returncode == 0 and "CUDA tensor" in out.stdout, out.stderr[-2000:]
+
+
+def test_a_binding_for_another_torch_or_python_does_not_serve(monkeypatch):
+    import sysconfig
+
+    import torch
+    build.build_binding()
+    assert not build.binding_is_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0+other")
+        assert build.binding_is_stale()
+    with monkeypatch.context() as m:
+        known = sysconfig.get_config_var
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-39-other" if name == "SOABI" else known(name))
+        assert build.binding_is_stale()
+    assert not build.binding_is_stale()
