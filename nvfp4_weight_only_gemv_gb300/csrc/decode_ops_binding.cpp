@@ -113,6 +113,11 @@ float real(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw Refused{};
     return static_cast<float>(v);
 }
+int truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v;
+}
 int size32(int64_t v, const char* name) {
     if (v > INT32_MAX) refuse(PyExc_ValueError, "%s is too large", name);
     return static_cast<int>(v);
@@ -253,7 +258,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.pages = size32(cache.k.size(0), "k_cache");
         g.max_pages = size32(table.size(1), "page_table");
         g.page_size = size32(cache.k.size(2), "k_cache");
-        g.interleaved = PyObject_IsTrue(a[9]);
+        g.interleaved = truth(a[9]);
         g.mscale = real(a[10]);
         g.eps = real(a[13]);
         return g_rope_append(&g, c.stream(a[17]));

@@ -232,3 +232,16 @@ def test_a_call_on_another_stream_keeps_what_it_is_given():
     got = nv.paged_attention(q, kc, vc, table, ln, stream=0)  # the default stream's handle
     torch.cuda.synchronize()
     assert torch.equal(got, want) and _owner(got) == 0
+
+
+# ---------------------------------------------------------------------------------------- refusals
+
+def test_rope_append_refuses_what_has_no_truth_value():
+    k = torch.ones((2, 2, 64), device=DEV)
+    kc, vc = nv.kv_cache(2, 2, 16, 64)
+    table = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    pos, freq = torch.tensor([0, 1], dtype=torch.int32, device=DEV), torch.ones(32, device=DEV)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        nv.rope_append(None, k, k, pos, freq, kc, vc, table, interleaved=torch.tensor([True, False]))
+    torch.cuda.synchronize()
+    assert not kc.any() and not vc.any()
