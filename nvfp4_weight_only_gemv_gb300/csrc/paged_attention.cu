@@ -1431,7 +1431,9 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     if (a->head_dim > kMaxDim || a->q_heads > 65535 || static_cast<int64_t>(a->seqs) * a->rows > (1 << 30) ||
         static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))
         return NVFP4_ERR_UNSUPPORTED;
-    if (!a->q || !a->k_cache || !a->v_cache || !a->page_table || !a->lengths || !a->out || !a->workspace)
+    // an empty cache or table is nowhere
+    if (!a->q || (a->pages && (!a->k_cache || !a->v_cache)) || (a->max_pages && !a->page_table) || !a->lengths || !a->out ||
+        !a->workspace)
         return NVFP4_ERR_NULL;
     if (!aligned(a->workspace, 256)) return NVFP4_ERR_ALIGN;
     if (a->workspace_bytes < nvfp4_attention_workspace_bytes(a->seqs, a->rows, a->q_heads, a->kv_heads, a->head_dim))

@@ -368,8 +368,8 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))
         return NVFP4_ERR_UNSUPPORTED;
     if (!a->positions || (a->rotary_half && !a->inv_freq) || (hq && !a->q_out) ||
-        (a->kv_heads && (!a->k || !a->v || !a->k_cache || !a->v_cache || !a->page_table)))
-        return NVFP4_ERR_NULL;
+        (a->kv_heads && (!a->k || !a->v || (a->pages && (!a->k_cache || !a->v_cache)) || (a->max_pages && !a->page_table))))
+        return NVFP4_ERR_NULL;  // (an empty cache or table is nowhere)
     if (a->kv_heads && (a->seqs == 0 || (!a->seq_ids && a->tokens % a->seqs))) return NVFP4_ERR_SHAPE;
     AppendParams p{};
     p.x[0] = a->q; p.x[1] = a->k; p.x[2] = a->v;

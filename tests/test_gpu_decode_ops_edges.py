@@ -245,3 +245,24 @@ def test_rope_append_refuses_what_has_no_truth_value():
         nv.rope_append(None, k, k, pos, freq, kc, vc, table, interleaved=torch.tensor([True, False]))
     torch.cuda.synchronize()
     assert not kc.any() and not vc.any()
+
+
+# ------------------------------------------------------------------------------ nothing cached yet
+
+@pytest.mark.parametrize("pages,max_pages", [(0, 0), (0, 3), (4, 0)])
+@pytest.mark.parametrize("cache", [BF16, FP8])
+def test_an_empty_cache_or_table(pages, max_pages, cache):
+    D, ws = 64, nv.attention_workspace(2, 2, 4, 2, 64)
+    kc, vc = nv.kv_cache(pages, 2, 16, D, cache)
+    table = torch.zeros((2, max_pages), dtype=torch.int32, device=DEV)
+    q, ln = torch.ones((4, 4, D), dtype=BF16, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    lse = torch.full((4, 4), math.nan, device=DEV)
+    out = nv.paged_attention(q, kc, vc, table, ln, workspace=ws, lse=lse)
+    assert not out.any() and bool((lse == -math.inf).all()) and nv.device_status() == 0
+    # padding is appended nowhere, a token without a place is reported
+    k, freq = torch.ones((2, 2, D), dtype=BF16, device=DEV), torch.ones(32, device=DEV)
+    for at, status in ((-1, 0), (0, nv.DEV_BAD_PAGE)):
+        pos = torch.full((2,), at, dtype=torch.int32, device=DEV)
+        nv.rope_append(q[:2], k, k, pos, freq, kc, vc, table)
+        assert nv.device_status() == status
+    assert not kc.float().any() and not vc.float().any()
