@@ -266,3 +266,36 @@ def test_an_empty_cache_or_table(pages, max_pages, cache):
         nv.rope_append(q[:2], k, k, pos, freq, kc, vc, table)
         assert nv.device_status() == status
     assert not kc.float().any() and not vc.float().any()
+
+
+# ---------------------------------------------------------------------- precision of the weights
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weights_carry_their_bits(D, cache):
+    # two keys of nearly the same score with values 1 and -1: the output, (1 - e) / (1 + e) for a weight e of the
+    # second, is a small difference that shows e's own rounding, 2^-16 (two bf16 numbers) or 2^-12 (f16) at most
+    H = 64
+    kc, vc = nv.kv_cache(1, 1, 16, D, cache)
+    kc[0, 0, :2, 0] = torch.tensor([1.0, 0.875], device=DEV).to(cache)
+    vc[0, 0, 0], vc[0, 0, 1] = (torch.full((D,), v, device=DEV).to(cache) for v in (1.0, -1.0))
+    q = torch.zeros((1, H, D), dtype=BF16, device=DEV)
+    q[0, :, 0] = torch.linspace(0.05, 0.4, H, device=DEV).to(BF16)
+    table, ln = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.full((1,), 2, dtype=torch.int32, device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, ln, 1.0)[0].double()
+    e = torch.exp(-0.125 * q[0, :, 0].double())[:, None]
+    ref = (1 - e) / (1 + e)
+    # an error x of e moves the output by 2 x / (1 + e)^2 < 0.6 x; scores and exp2 are good to 2^-21
+    bits = 16 if cache is BF16 else 12
+    tol = ref * U16 / 2 + 0.6 * (2.0 ** -bits + 2.0 ** -21)
+    _within(got, ref.expand(-1, D), tol)
+    # what one bf16 number a weight would give is outside
+    rough = e.to(BF16).double()
+    off = ((1 - rough) / (1 + rough) - ref).abs()
+    assert bool((off > tol).any())
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8])
+@pytest.mark.parametrize("rows,hq,hk,window", [(1, 8, 2, 0), (4, 8, 1, 0), (3, 4, 2, 70000)])
+def test_a_long_context(cache, rows, hq, hk, window):
+    _check_attend([131071, 40000], rows, hq, hk, 128, cache, 64, window=window, seed=rows)
