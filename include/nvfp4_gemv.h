@@ -279,9 +279,9 @@ typedef enum {
  * Root-mean-square norm of rows:
  *     h = x + residual (fp32),  residual_out = h in the residual's type,
  *     y = h / sqrt(mean(h^2) + eps) * weight                     (fp32, the unrounded h)
- * y is f32, bf16 or E4M3. E4M3: code = E4M3(y / s) to nearest even (the quotient to 2^-22) with s =
- * max(max|y| / 448, 2^-64) over the row (group = 0; scales [rows]) or over each `group` columns, a power of two from 16 to
- * 256 that divides cols (scales [rows, cols / group]); a NaN makes its scale NaN.
+ * y is f32, bf16 or E4M3. E4M3: code = E4M3(y / s) (an fp32 quotient, to nearest even) with s =
+ * max(max|y| / 448, 2^-64) over the row (group = 0; scales [rows]) or over each `group` columns, a power
+ * of two from 16 to 256 that divides cols (scales [rows, cols / group]); a NaN makes its scale NaN.
  * residual may be NULL (no addition, residual_out unused). residual_out may be the residual
  * itself and y may be x where type and row pitch agree. Row pitches ld* are in elements.
  * 0 <= cols <= 32768. Rows on 16-byte boundaries and cols % 8 == 0 take the vector kernel.

@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
     return d;
 }
 
+// A quotient x / s from q = x * inv, inv near 1 / s: q put right by its remainder (P. Markstein, IBM J. Res. Dev.
+// 34, 1990). What is stored as E4M3 gets the codes of an fp32 quotient this way (tested against it), at two
+// products a value: q alone took the other code for values beside the middle of two.
+__device__ __forceinline__ float put_right(float q, float x, float s, float inv) { return fmaf(fmaf(-q, s, x), inv, q); }
+
 template <int N>
 __device__ __forceinline__ void load_f32(const float* p, float (&v)[N]) {
 #pragma unroll

@@ -187,13 +187,10 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[V]) {
     else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-// x / s for E4M3 from inv = 1 / s, the same codes as of an fp32 quotient (tested against it): the product, put
-// right by its remainder (P. Markstein, IBM J. Res. Dev. 34, 1990). The product alone took the other code for
-// values beside the middle of two; a division per value took 8192 tokens of 32 + 8 + 8 heads from 45.7 to 49.8 us, this
-// does not. A quotient of 512 and more only has to stay beyond 448, infinities with it.
+// x / s for E4M3 from inv = 1 / s. A quotient of 512 and more only has to stay beyond 448, infinities with it. (A
+// division per value took 8192 tokens of 32 + 8 + 8 heads from 45.7 to 49.8 us, this does not.)
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
-    const float q = fminf(fmaxf(x * inv, -512.0f), 512.0f);
-    return fmaf(fmaf(-q, s, x), inv, q);
+    return put_right(fminf(fmaxf(x * inv, -512.0f), 512.0f), x, s, inv);
 }
 
 template <typename XT, int V>

@@ -299,3 +299,34 @@ def test_weights_carry_their_bits(D, cache):
 @pytest.mark.parametrize("rows,hq,hk,window", [(1, 8, 2, 0), (4, 8, 1, 0), (3, 4, 2, 70000)])
 def test_a_long_context(cache, rows, hq, hk, window):
     _check_attend([131071, 40000], rows, hq, hk, 128, cache, 64, window=window, seed=rows)
+
+
+# ------------------------------------------------------------------------------------ 8-bit norms
+
+@pytest.mark.parametrize("pitch", [0, 3])
+@pytest.mark.parametrize("rows,cols,group", [(4096, 4096, 128), (4096, 4096, 0), (3, 4096, 16), (60, 30016, 0)])
+def test_normed_codes_are_the_quotients(rows, cols, group, pitch):
+    # the same rows in fp32, divided by the scales that came with the codes; both kernels
+    g = _gen(rows + cols + group)
+    x = _randn((rows, cols + pitch), g)[:, pitch:]
+    w = 1 + 0.2 * _randn((cols,), g)
+    got = nv.rms_norm(x, w, out_dtype=FP8, group=group)
+    y = nv.rms_norm(x, w, out_dtype=torch.float32).y.view(rows, -1, group or cols)
+    top = y.abs().amax(dim=2).double() / 448
+    _within(got.scales, top, top * 2 * U32, "scales")  # 1 / 448 is rounded, and the product
+    want = (y / got.scales[..., None]).to(FP8).view(rows, cols)
+    assert torch.equal(got.y.view(torch.uint8), want.view(torch.uint8)), int((got.y.float() != want.float()).sum())
+
+
+def test_normed_codes_beside_infinities():
+    # a weight that overflows one value: the row's scale is infinite, what is finite over it is zero
+    x, w = torch.ones((2, 64), device=DEV), torch.ones(64, device=DEV)
+    x[1] = 2.0 ** 40
+    w[5] = 3e38
+    x[:, 5] = 2 * x[:, 5]
+    for cols in (64, 63):
+        got = nv.rms_norm(x[:, :cols].contiguous(), w[:cols].contiguous(), 0.0, out_dtype=FP8)
+        y = nv.rms_norm(x[:, :cols].contiguous(), w[:cols].contiguous(), 0.0, out_dtype=torch.float32).y
+        want = (y / got.scales).to(FP8).float()
+        assert bool(torch.isinf(got.scales).all()) and bool(torch.isinf(y[:, 5]).all())
+        assert torch.equal(torch.isnan(got.y.float()), torch.isnan(want)) and torch.equal(got.y.float().nan_to_num(), want.nan_to_num())
