@@ -58,7 +58,7 @@ typedef enum {
     NVFP4_ERR_SHAPE = 2,       /* M > 8, negative size, K % 16 != 0, top_k/T/E invalid */
     NVFP4_ERR_ALIGN = 3,       /* an FFN or attention workspace not 256-byte aligned (other misalignment runs
                                   the byte-load kernel) */
-    NVFP4_ERR_DTYPE = 4,       /* y_type is not one of nvfp4_out_t */
+    NVFP4_ERR_DTYPE = 4,       /* y_type is not one of nvfp4_out_t; scales next to a bf16 cache */
     NVFP4_ERR_UNSUPPORTED = 5, /* a size beyond what any kernel here can take */
     NVFP4_ERR_CUDA = 6,        /* the CUDA runtime reported an error (see nvfp4_last_cuda_error) */
     NVFP4_ERR_TIMEOUT = 7      /* reported by nvfp4_device_status(): a device wait timed out */
@@ -267,7 +267,7 @@ int nvfp4_sdict_encode(const uint8_t* scales, int N, int K, uint8_t* plane_out, 
  * page; page p starts page_stride elements times p after the base (so both may be halves of one
  * allocation). page_table [seqs, table_stride] int32 names the pages of each sequence in order;
  * entries past a sequence's length are not read. Values are bf16, or E4M3 codes that stand for
- * code * scale[kv_head] (k_scale, v_scale [kv_heads] f32; NULL = 1).
+ * code * scale[kv_head] (k_scale, v_scale [kv_heads] f32; NULL = 1, as a bf16 cache wants it).
  */
 typedef enum {
     NVFP4_F32 = 0,

@@ -91,8 +91,10 @@ struct Checks {
         if (t.size(0) != n) refuse(PyExc_ValueError, "%s must have %s%lld values (got %lld)", name, "", n, t.size(0));
         return t;
     }
-    const float* head_scale(PyObject* o, const char* name, long long heads) const {
-        return o == Py_None ? nullptr : static_cast<const float*>(vector(o, name, kF32, heads).data_ptr());
+    const float* head_scale(PyObject* o, const char* name, const at::Tensor& cache) const {
+        if (o == Py_None) return nullptr;
+        if (kind(cache) != kE4m3) refuse(PyExc_ValueError, "%s belongs to a float8_e4m3fn cache", name);
+        return static_cast<const float*>(vector(o, name, kF32, cache.size(1)).data_ptr());
     }
     void* stream(PyObject* o) const {
         if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
@@ -250,8 +252,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.rotary_half = size32(freq.size(0), "inv_freq");
         g.k_cache = cache.k.data_ptr(); g.v_cache = cache.v.data_ptr();
         g.k_page_stride = cache.k.stride(0); g.v_page_stride = cache.v.stride(0);
-        g.k_scale = c.head_scale(a[14], "k_scale", g.kv_heads);
-        g.v_scale = c.head_scale(a[15], "v_scale", g.kv_heads);
+        g.k_scale = c.head_scale(a[14], "k_scale", cache.k);
+        g.v_scale = c.head_scale(a[15], "v_scale", cache.v);
         g.page_table = static_cast<const int32_t*>(table.data_ptr());
         g.table_stride = table.stride(0);
         g.x_type = code(k); g.cache_type = code(cache.k);
@@ -299,8 +301,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.q_token_stride = q.stride(0); g.q_head_stride = q.stride(1);
         g.k_cache = cache.k.data_ptr(); g.v_cache = cache.v.data_ptr();
         g.k_page_stride = cache.k.stride(0); g.v_page_stride = cache.v.stride(0);
-        g.k_scale = c.head_scale(a[7], "k_scale", g.kv_heads);
-        g.v_scale = c.head_scale(a[8], "v_scale", g.kv_heads);
+        g.k_scale = c.head_scale(a[7], "k_scale", cache.k);
+        g.v_scale = c.head_scale(a[8], "v_scale", cache.v);
         g.page_table = static_cast<const int32_t*>(table.data_ptr());
         g.table_stride = table.stride(0);
         g.lengths = static_cast<const int32_t*>(lengths.data_ptr());

@@ -1426,7 +1426,9 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     if (!sizes_ok(a->seqs, a->rows, a->q_heads, a->kv_heads, a->head_dim) || a->pages < 0 || a->max_pages < 0 ||
         a->page_size < 1 || a->window < 0)
         return NVFP4_ERR_SHAPE;
-    if (a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3) return NVFP4_ERR_DTYPE;
+    if ((a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3) ||
+        (a->cache_type == NVFP4_BF16 && (a->k_scale || a->v_scale)))
+        return NVFP4_ERR_DTYPE;
     if (a->seqs == 0 || a->rows == 0 || a->q_heads == 0 || a->head_dim == 0) return NVFP4_OK;
     if (a->head_dim > kMaxDim || a->q_heads > 65535 || static_cast<int64_t>(a->seqs) * a->rows > (1 << 30) ||
         static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))

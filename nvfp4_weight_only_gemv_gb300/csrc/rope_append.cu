@@ -358,6 +358,7 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         !(a->eps >= 0.0f))
         return NVFP4_ERR_SHAPE;
     if ((a->x_type != NVFP4_F32 && a->x_type != NVFP4_BF16) || (a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3) ||
+        (a->cache_type == NVFP4_BF16 && (a->k_scale || a->v_scale)) ||
         ((a->q_norm || a->k_norm) && a->norm_type != NVFP4_F32 && a->norm_type != NVFP4_BF16))
         return NVFP4_ERR_DTYPE;
     if (a->tokens == 0 || a->head_dim == 0 || hq + a->kv_heads == 0) return NVFP4_OK;

@@ -247,6 +247,16 @@ def test_rope_append_refuses_what_has_no_truth_value():
     assert not kc.any() and not vc.any()
 
 
+def test_scales_next_to_a_bf16_cache_are_refused():
+    q, kc, vc, table, ln, _, _ = _attend_inputs([5, 6], 1, 4, 2, 64, BF16, 16, 8)
+    one = torch.ones(2, device=DEV)
+    for kw in (dict(k_scale=one), dict(v_scale=one)):
+        with pytest.raises(ValueError, match="float8"):
+            nv.paged_attention(q, kc, vc, table, ln, **kw)
+        with pytest.raises(ValueError, match="float8"):
+            nv.rope_append(q, q[:, :2], q[:, :2], ln - 1, torch.ones(32, device=DEV), kc, vc, table, **kw)
+
+
 # ------------------------------------------------------------------------------ nothing cached yet
 
 @pytest.mark.parametrize("pages,max_pages", [(0, 0), (0, 3), (4, 0)])
