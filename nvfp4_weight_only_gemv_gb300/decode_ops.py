@@ -16,6 +16,7 @@ import importlib.util
 import math
 import os
 import struct
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -43,6 +44,13 @@ class _Unbound:
 def _load():
     """Loads the binding and gives it the loaded library's entry points."""
     global _native
+    with _load_lock:
+        if isinstance(_native, _Unbound):  # else another thread was first
+            _native = _bound()
+        return _native
+
+
+def _bound():
     lib = _nv.library()
     path = _build.binding_path()
     try:
@@ -55,11 +63,11 @@ def _load():
     loader.exec_module(module)
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                   for f in (lib.nvfp4_rms_norm, lib.nvfp4_rope_append, lib.nvfp4_paged_attention)))
-    _native = module
     return module
 
 
 _native = _Unbound()
+_load_lock = threading.Lock()
 
 
 class RMSNormOut(NamedTuple):

@@ -85,3 +85,29 @@ def test_a_binding_for_another_torch_or_python_does_not_serve(monkeypatch):
         m.setattr(sysconfig, "get_config_var", lambda name: "cpython-39-other" if name == "SOABI" else known(name))
         assert build.binding_is_stale()
     assert not build.binding_is_stale()
+
+
+def test_threads_build_the_binding_once(monkeypatch):
+    import threading
+    import time
+
+    from nvfp4_weight_only_gemv_gb300 import decode_ops
+    build.build_binding()
+    inside, most, calls = [0], [0], [0]
+
+    def slow(force=False):
+        inside[0] += 1
+        calls[0] += 1
+        most[0] = max(most[0], inside[0])
+        time.sleep(0.2)
+        inside[0] -= 1
+        return build.binding_path()
+
+    monkeypatch.setattr(build, "build_binding", slow)
+    monkeypatch.setattr(decode_ops, "_native", decode_ops._Unbound())
+    threads = [threading.Thread(target=decode_ops._load) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert most[0] == 1 and calls[0] == 1
