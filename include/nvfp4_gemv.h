@@ -312,7 +312,7 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale) (an fp32
  * quotient, to nearest even, clamped to +-448; scales are positive). Long-context scalings of the
  * frequencies are the caller's, in inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
- * row is zero. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
+ * row is zero. Positions are below 2^24 (beyond it, a call without keys rounds them to fp32). A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
  * nothing. Two tokens of one call at the same sequence and position leave either's values.
  * q, k, v: [tokens, heads, head_dim] with unit stride inside a head and the given strides between
  * tokens and heads. head_dim <= 1024, 2 * rotary_half <= head_dim, max_pages * page_size <= 2^24.

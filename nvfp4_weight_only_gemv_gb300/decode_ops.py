@@ -27,8 +27,8 @@ from . import build as _build
 
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 
-# the C structs nvfp4_rms_norm_args, nvfp4_rope_append_args and nvfp4_paged_attention_args, for
-# callers that go to the C ABI through the ctypes library
+# the C structs nvfp4_rms_norm_args, nvfp4_rope_append_args and nvfp4_paged_attention_args as bytes, for
+# the C entry points called through the ctypes library (the tests of their checks do)
 _NORM = struct.Struct("@6P4q7if").pack
 _APPEND = struct.Struct("@14P9q13i2f4x").pack
 _ATTEND = struct.Struct("@10P6q10if4x").pack
