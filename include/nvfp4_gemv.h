@@ -268,11 +268,18 @@ int nvfp4_sdict_encode(const uint8_t* scales, int N, int K, uint8_t* plane_out, 
  * allocation). page_table [seqs, table_stride] int32 names the pages of each sequence in order;
  * entries past a sequence's length are not read. Values are bf16, or E4M3 codes that stand for
  * code * scale[kv_head] (k_scale, v_scale [kv_heads] f32; NULL = 1, as a bf16 cache wants it).
+ *
+ * Or they are held in 4 bits (NVFP4_E2M1): head_dim and page_size are multiples of 16, and every 16 keys of
+ * a kv head are a record of 9 * head_dim bytes, first their E2M1 codes [16][head_dim / 2] (element 2j in the
+ * low nibble of byte j), then the E4M3 scales of 16 elements each, [head_dim / 16][16]: key i's scale of
+ * elements 16c .. 16c + 15 is byte 8 * head_dim + 16 c + i. A page holds [kv_heads][page_size / 16] records;
+ * page strides count bytes. An element stands for code * block scale * scale[kv_head].
  */
 typedef enum {
     NVFP4_F32 = 0,
     NVFP4_BF16 = 1,
-    NVFP4_E4M3 = 2
+    NVFP4_E4M3 = 2,
+    NVFP4_E2M1 = 3             /* a cache of 4 bits only */
 } nvfp4_type;
 
 /*
@@ -310,7 +317,9 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  *     the head's values from 2 * rotary_half on pass through.
  * q_out [tokens, q_heads, head_dim] bf16 receives q (q = NULL: no queries). k and v go to row
  * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale) (an fp32
- * quotient, to nearest even, clamped to +-448; scales are positive). Long-context scalings of the
+ * quotient, to nearest even, clamped to +-448; scales are positive). A cache of 4 bits: of 16 elements t = value / scale
+ * the block scale is b = E4M3(max|t| / 6), the codes E2M1(t / b), all fp32 quotients, to nearest even, beyond the
+ * types' largest to the largest; b = 0 gives zeros, a NaN makes b NaN. Long-context scalings of the
  * frequencies are the caller's, in inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
  * row is zero. Positions are below 2^24 (beyond it, a call without keys rounds them to fp32). A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
  * nothing. Two tokens of one call at the same sequence and position leave either's values.
@@ -343,6 +352,32 @@ typedef struct {
 nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream);
 
 /*
+ * Reads rows of the cache back as bf16: for token t at position positions[t] of sequence seq_ids[t] (as
+ * nvfp4_rope_append places it), k_out and v_out [tokens, kv_heads, head_dim] receive what the cache holds there:
+ * the value, or code * scale, or code * block scale * scale, rounded once. For a program's own attention over a
+ * prompt, which then sees the keys that later steps will see, and to move a cache. A negative position is padding
+ * and gives zeros. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and gives zeros. Strides,
+ * limits and layouts as nvfp4_rope_append.
+ */
+typedef struct {
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* positions;
+    const int32_t* seq_ids;
+    const int32_t* page_table;
+    void* k_out;
+    void* v_out;
+    int64_t k_page_stride, v_page_stride, table_stride;
+    int32_t cache_type;
+    int32_t tokens, seqs, kv_heads, head_dim;
+    int32_t pages, max_pages, page_size;
+} nvfp4_cache_read_args;
+
+nvfp4_status nvfp4_cache_read(const nvfp4_cache_read_args* args, void* stream);
+
+/*
  * Attention of each sequence's newest `rows` tokens over its cached keys and values. With n =
  * lengths[b] (these tokens included), query row r of sequence b stands at position n - rows + r
  * and sees the keys j <= that position, with window > 0 only the last `window` of them:
@@ -353,7 +388,7 @@ nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream)
  * sequence), or whose scores are all -inf, gives zeros and lse = -inf. Keys that a row does not
  * see never reach it, whatever they hold. A length outside [0, max_pages * page_size] or a page
  * outside [0, pages) sets NVFP4_DEV_BAD_PAGE; the length is clamped, the page's keys are not read.
- * Scores and sums are fp32; weights enter the tensor cores with 16 bits (bf16 cache) or 11 (E4M3
+ * Scores and sums are fp32; weights enter the tensor cores with 16 bits (bf16 cache) or 11 (E4M3 or E2M1
  * cache; below 2^-21 of the row's largest, with an error of 2^-32 of it).
  *   workspace: nvfp4_attention_workspace_bytes(...) bytes of device memory, 256-byte aligned. Its
  *   counters must be zero before its first use and every call leaves them at zero; they stand at the
@@ -381,6 +416,20 @@ typedef struct {
 } nvfp4_paged_attention_args;
 
 nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* args, void* stream);
+
+/*
+ * The same attention with other scores. With s_j = scale * q . k_j, position i of the query row and its head h:
+ *     z_j = softcap * tanh(s_j / softcap)  (softcap = 0: s_j)  - slopes[h] * (i - j)  (slopes NULL: no bias)
+ * take the place of s_j in out and lse. softcap is 0 or between 2^-40 and 2^40 (else NVFP4_ERR_SHAPE); slopes
+ * [q_heads] f32, finite, of either sign. scores = NULL, or neither form asked for: nvfp4_paged_attention.
+ */
+typedef struct {
+    const float* slopes;
+    float softcap;
+} nvfp4_attention_scores;
+
+nvfp4_status nvfp4_paged_attention_scored(const nvfp4_paged_attention_args* args, const nvfp4_attention_scores* scores,
+                                          void* stream);
 
 /* Bytes of workspace nvfp4_paged_attention needs on the current device for these sizes (any
  * lengths); -1 for sizes that the call refuses. */

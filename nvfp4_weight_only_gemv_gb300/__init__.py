@@ -27,7 +27,7 @@ __all__ = ["gemv", "gemv_gate_up", "gemv_gate_up_swiglu", "ffn_swiglu", "ffn_swi
            "sdict_plane_bytes", "sdict_encode", "device_status", "set_wait_budget_ns",
            "set_variant", "set_pdl", "fp32_fallbacks", "phase_trace", "describe_plan", "describe_plan_host", "library", "library_path", "NVFP4Error",
            "rms_norm", "RMSNormOut", "rope_append", "rope_frequencies", "paged_attention", "attention_workspace",
-           "attention_workspace_bytes", "kv_cache",
+           "attention_workspace_bytes", "kv_cache", "cache_read",
            "OUT_F32", "OUT_BF16", "DEV_TIMEOUT", "DEV_BAD_EXPERT", "DEV_INTERNAL", "DEV_BAD_PAGE"]
 
 OUT_F32 = 0
@@ -103,10 +103,12 @@ def _declare(lib):
     lib.nvfp4_sdict_encode.restype = i32
     lib.nvfp4_phase_trace.argtypes = [vp, i32, vp]
     lib.nvfp4_phase_trace.restype = i32
-    for name in ("nvfp4_rms_norm", "nvfp4_rope_append", "nvfp4_paged_attention"):
+    for name in ("nvfp4_rms_norm", "nvfp4_rope_append", "nvfp4_cache_read", "nvfp4_paged_attention"):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.c_char_p, vp]  # the argument struct's bytes
         fn.restype = i32
+    lib.nvfp4_paged_attention_scored.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]
+    lib.nvfp4_paged_attention_scored.restype = i32
     lib.nvfp4_attention_workspace_bytes.argtypes = [i32] * 5
     lib.nvfp4_attention_workspace_bytes.restype = ctypes.c_int64
     lib.nvfp4_version.argtypes = []
@@ -553,5 +555,5 @@ def describe_plan_host(kind: str, M: int, N: int, K: int, T: int = 0, top_k: int
     return buf.value.decode()
 
 
-from .decode_ops import (RMSNormOut, attention_workspace, attention_workspace_bytes, kv_cache,  # noqa: E402
+from .decode_ops import (RMSNormOut, attention_workspace, attention_workspace_bytes, cache_read, kv_cache,  # noqa: E402
                          paged_attention, rms_norm, rope_append, rope_frequencies)

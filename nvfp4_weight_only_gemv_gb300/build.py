@@ -9,7 +9,7 @@ import sysconfig
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRC = os.path.join(PKG_DIR, "csrc", "nvfp4_gemv.cu")
-OPERATORS = tuple(os.path.join(PKG_DIR, "csrc", f) for f in ("rms_norm.cu", "rope_append.cu", "paged_attention.cu"))
+OPERATORS = tuple(os.path.join(PKG_DIR, "csrc", f) for f in ("rms_norm.cu", "rope_append.cu", "cache_read.cu", "paged_attention.cu"))
 HEADER = os.path.join(ROOT, "include", "nvfp4_gemv.h")
 BINDING = os.path.join(PKG_DIR, "csrc", "decode_ops_binding.cpp")
 SOURCES = (SRC, *OPERATORS, os.path.join(PKG_DIR, "csrc", "ops_common.cuh"), HEADER)

@@ -1,0 +1,167 @@
+// Rows of a paged cache read back as bf16.
+//
+// For token t at position n = positions[t]: out[t, h] = bf16(code * block scale * scale[h]) (E2M1),
+// bf16(code * scale[h]) (E4M3) or the value (bf16) of row n % page of page table[seq][n / page].
+//
+// Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens.
+
+#include "ops_common.cuh"
+
+namespace nvfp4 {
+namespace {
+
+using namespace ops;
+
+__device__ int g_read_status;
+
+struct ReadParams {
+    const void* cache[2];    // k, v
+    const float* cache_scale[2];
+    const int32_t* positions;
+    const int32_t* seq_ids;  // NULL: token t belongs to sequence t / per_seq
+    const int32_t* table;
+    __nv_bfloat16* out[2];
+    int64_t page_stride[2], table_stride;
+    int64_t pieces;          // of all tokens
+    int T, hk, D, seqs, per_seq, pages, max_pages, page, cache_type;
+    int head_pieces;         // of a head
+};
+
+// One thread takes V neighbouring values of a row: 16 where rows are whole blocks on their boundaries, else one.
+template <int V>
+__global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__ ReadParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+    if (at >= p.pieces) return;
+    const int per_token = 2 * p.hk * p.head_pieces;
+    const int t = static_cast<int>(at / per_token);
+    int i = static_cast<int>(at - static_cast<int64_t>(t) * per_token);
+    const int which = i >= p.hk * p.head_pieces;
+    i -= which * p.hk * p.head_pieces;
+    const int h = i / p.head_pieces, d = (i - h * p.head_pieces) * V;
+    __nv_bfloat16* const out = p.out[which] + (static_cast<int64_t>(t) * p.hk + h) * p.D + d;
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.0f;
+    const int n = p.positions[t];
+    int64_t page = -1;
+    if (n >= 0) {
+        const int seq = p.seq_ids ? p.seq_ids[t] : t / p.per_seq, pi = n / p.page;
+        if (seq >= 0 && seq < p.seqs && pi < p.max_pages) page = p.table[seq * p.table_stride + pi];
+        if (page < 0 || page >= p.pages) {
+            page = -1;
+            atomicOr(&g_read_status, NVFP4_DEV_BAD_PAGE);
+        }
+    }
+    if (page >= 0) {
+        const int slot = n % p.page;
+        const float scale = p.cache_scale[which] ? p.cache_scale[which][h] : 1.0f;
+        if (p.cache_type == NVFP4_E2M1) {
+            const int64_t record = static_cast<int64_t>(h) * (p.page / kRecordKeys) + slot / kRecordKeys;
+            const uint8_t* const rec = static_cast<const uint8_t*>(p.cache[which]) + page * p.page_stride[which] + record * record_bytes(p.D);
+            const int key = slot % kRecordKeys;
+            const uint8_t* const codes = rec + key * (p.D / 2) + d / 2;
+            const float block = e4m3_value(rec[8 * p.D + d / 16 * kRecordKeys + key]);
+            uint32_t h2[4];
+            if constexpr (V == 16) {
+                const uint2 w = *reinterpret_cast<const uint2*>(codes);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    e2m1x8_f16x2(half ? w.y : w.x, h2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[e]));
+                        v[8 * half + 2 * e] = f.x * block * scale;
+                        v[8 * half + 2 * e + 1] = f.y * block * scale;
+                    }
+                }
+            } else {
+                e2m1x8_f16x2(*codes, h2);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[0]));
+                v[0] = (d & 1 ? f.y : f.x) * block * scale;
+            }
+        } else {
+            const int64_t from = page * p.page_stride[which] + (static_cast<int64_t>(h) * p.page + slot) * p.D + d;
+            if (p.cache_type == NVFP4_E4M3) {
+                const uint8_t* const codes = static_cast<const uint8_t*>(p.cache[which]) + from;
+                if constexpr (V == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = e4m3_value((e < 4 ? w.x : e < 8 ? w.y : e < 12 ? w.z : w.w) >> 8 * (e & 3)) * scale;
+                } else {
+                    v[0] = e4m3_value(*codes) * scale;
+                }
+            } else {  // as it stands
+                const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(p.cache[which]) + from;
+                if constexpr (V == 16) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(x), b = *reinterpret_cast<const uint4*>(x + 8);
+                    *reinterpret_cast<uint4*>(out) = a;
+                    *reinterpret_cast<uint4*>(out + 8) = b;
+                } else {
+                    *out = *x;
+                }
+                return;
+            }
+        }
+    }
+    if constexpr (V == 16) {
+        float lo[8], hi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { lo[e] = v[e]; hi[e] = v[8 + e]; }
+        store_vec(out, lo);
+        store_vec(out + 8, hi);
+    } else {
+        *out = __float2bfloat16_rn(v[0]);
+    }
+}
+
+cudaError_t read_status(int* bits) {
+    const int zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_read_status, sizeof(int));
+    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_read_status, &zero, sizeof(int));
+}
+const bool g_registered = register_status(read_status);
+
+}  // namespace
+}  // namespace nvfp4
+
+extern "C" nvfp4_status nvfp4_cache_read(const nvfp4_cache_read_args* a, void* stream) {
+    using namespace nvfp4;
+    using namespace nvfp4::ops;
+    if (!a) return NVFP4_ERR_NULL;
+    if (a->tokens < 0 || a->kv_heads < 0 || a->head_dim < 0 || a->seqs < 0 || a->pages < 0 || a->max_pages < 0 || a->page_size < 1)
+        return NVFP4_ERR_SHAPE;
+    if ((a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3 && a->cache_type != NVFP4_E2M1) ||
+        (a->cache_type == NVFP4_BF16 && (a->k_scale || a->v_scale)))
+        return NVFP4_ERR_DTYPE;
+    if (a->cache_type == NVFP4_E2M1 && (a->head_dim % 16 || a->page_size % kRecordKeys)) return NVFP4_ERR_SHAPE;
+    if (a->tokens == 0 || a->kv_heads == 0 || a->head_dim == 0) return NVFP4_OK;
+    if (a->head_dim > 1024 || a->kv_heads > 32767 || static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))
+        return NVFP4_ERR_UNSUPPORTED;
+    // an empty cache or table is nowhere
+    if (!a->positions || !a->k_out || !a->v_out || (a->pages && (!a->k_cache || !a->v_cache)) || (a->max_pages && !a->page_table))
+        return NVFP4_ERR_NULL;
+    if (a->seqs == 0 || (!a->seq_ids && a->tokens % a->seqs)) return NVFP4_ERR_SHAPE;
+    ReadParams p{};
+    p.cache[0] = a->k_cache; p.cache[1] = a->v_cache;
+    p.cache_scale[0] = a->k_scale; p.cache_scale[1] = a->v_scale;
+    p.positions = a->positions; p.seq_ids = a->seq_ids; p.table = a->page_table;
+    p.out[0] = static_cast<__nv_bfloat16*>(a->k_out); p.out[1] = static_cast<__nv_bfloat16*>(a->v_out);
+    p.page_stride[0] = a->k_page_stride; p.page_stride[1] = a->v_page_stride; p.table_stride = a->table_stride;
+    p.T = a->tokens; p.hk = a->kv_heads; p.D = a->head_dim; p.seqs = a->seqs;
+    p.per_seq = (a->tokens + a->seqs - 1) / a->seqs;
+    p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size; p.cache_type = a->cache_type;
+    // 16 values a thread: pieces of 8 (E2M1) or 16 bytes on their boundaries
+    const int piece = p.cache_type == NVFP4_E2M1 ? 8 : 16, elements = p.cache_type == NVFP4_BF16 ? 8 : piece;
+    bool wide = host_variant() != 1 && p.D % 16 == 0;
+    for (int i = 0; i < 2; ++i)
+        wide = wide && aligned(p.cache[i], piece) && p.page_stride[i] % elements == 0 && aligned(p.out[i], 16);
+    p.head_pieces = wide ? p.D / 16 : p.D;
+    p.pieces = 2ll * p.T * p.hk * p.head_pieces;
+    const int64_t ctas = (p.pieces + 127) / 128;
+    if (ctas > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(ctas));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return wide ? launch(cache_read_kernel<16>, grid, dim3(128), 0, st, p) : launch(cache_read_kernel<1>, grid, dim3(128), 0, st, p);
+}

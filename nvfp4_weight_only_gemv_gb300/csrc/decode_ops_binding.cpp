@@ -21,12 +21,14 @@ namespace {
 
 using RmsNorm = nvfp4_status (*)(const nvfp4_rms_norm_args*, void*);
 using RopeAppend = nvfp4_status (*)(const nvfp4_rope_append_args*, void*);
-using PagedAttention = nvfp4_status (*)(const nvfp4_paged_attention_args*, void*);
+using CacheRead = nvfp4_status (*)(const nvfp4_cache_read_args*, void*);
+using PagedAttention = nvfp4_status (*)(const nvfp4_paged_attention_args*, const nvfp4_attention_scores*, void*);
 RmsNorm g_rms_norm = nullptr;
 RopeAppend g_rope_append = nullptr;
+CacheRead g_cache_read = nullptr;
 PagedAttention g_paged_attention = nullptr;
 
-enum : unsigned { kF32 = 1, kBf16 = 2, kE4m3 = 4, kI32 = 8, kU8 = 16, kWide = kF32 | kBf16, kCache = kBf16 | kE4m3 };
+enum : unsigned { kF32 = 1, kBf16 = 2, kE4m3 = 4, kI32 = 8, kU8 = 16, kWide = kF32 | kBf16, kCache = kBf16 | kE4m3 | kU8 };
 
 unsigned kind(const at::Tensor& t) {
     switch (t.scalar_type()) {
@@ -48,7 +50,7 @@ const char* names_of(unsigned kinds) {
         case kI32: return "torch.int32";
         case kU8: return "torch.uint8";
         case kWide: return "torch.float32 or torch.bfloat16";
-        case kCache: return "torch.bfloat16 or torch.float8_e4m3fn";
+        case kCache: return "torch.bfloat16, torch.float8_e4m3fn or torch.uint8 (4 bits)";
         default: return "torch.float32, torch.bfloat16 or torch.float8_e4m3fn";
     }
 }
@@ -93,7 +95,7 @@ struct Checks {
     }
     const float* head_scale(PyObject* o, const char* name, const at::Tensor& cache) const {
         if (o == Py_None) return nullptr;
-        if (kind(cache) != kE4m3) refuse(PyExc_ValueError, "%s belongs to a float8_e4m3fn cache", name);
+        if (kind(cache) == kBf16) refuse(PyExc_ValueError, "%s belongs to a float8_e4m3fn or 4-bit cache", name);
         return static_cast<const float*>(vector(o, name, kF32, cache.size(1)).data_ptr());
     }
     void* stream(PyObject* o) const {
@@ -186,6 +188,8 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 struct Caches {
     const at::Tensor& k;
     const at::Tensor& v;
+    int type;
+    int64_t head_dim;
 };
 Caches caches(const Checks& c, PyObject* ko, PyObject* vo) {
     const at::Tensor& k = c.any(ko, "k_cache", kCache, 4);
@@ -195,7 +199,11 @@ Caches caches(const Checks& c, PyObject* ko, PyObject* vo) {
     for (const at::Tensor* t : {&k, &v})
         if (t->numel() && ((page > 1 && t->stride(2) != dim) || (heads > 1 && t->stride(1) != page * dim)))
             refuse(PyExc_ValueError, "%s must be contiguous inside a page", t == &k ? "k_cache" : "v_cache");
-    return {k, v};
+    if (kind(k) != kU8) return {k, v, code(k), dim};
+    // records of 16 keys and 9 head_dim bytes
+    if (dim % 9) refuse(PyExc_ValueError, "%s hold 9 bytes for 16 values of a head: %s%lld bytes do not divide", "4-bit caches", "", dim);
+    if (page % 16) refuse(PyExc_ValueError, "%s have pages of a multiple of 16 keys%s (got %lld)", "4-bit caches", "", page);
+    return {k, v, NVFP4_E2M1, dim / 9 * 16};
 }
 
 // (q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_ids, interleaved, mscale, q_norm,
@@ -211,7 +219,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.tokens = size32(k.size(0), "k");
         g.kv_heads = size32(k.size(1), "k");
         g.head_dim = size32(k.size(2), "k");
-        if (cache.k.size(1) != g.kv_heads || cache.k.size(3) != g.head_dim)
+        if (cache.k.size(1) != g.kv_heads || cache.head_dim != g.head_dim)
             refuse(PyExc_ValueError, "%s do not have the heads of k", "the caches");
         const at::Tensor& pos = c.vector(a[3], "positions", kI32, g.tokens);
         const at::Tensor& freq = c.whole(a[4], "inv_freq", kF32, 1);
@@ -256,7 +264,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.v_scale = c.head_scale(a[15], "v_scale", cache.v);
         g.page_table = static_cast<const int32_t*>(table.data_ptr());
         g.table_stride = table.stride(0);
-        g.x_type = code(k); g.cache_type = code(cache.k);
+        g.x_type = code(k); g.cache_type = cache.type;
         g.pages = size32(cache.k.size(0), "k_cache");
         g.max_pages = size32(table.size(1), "page_table");
         g.page_size = size32(cache.k.size(2), "k_cache");
@@ -267,9 +275,45 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (q, k_cache, v_cache, page_table, lengths, scale, window, k_scale, v_scale, workspace, out, lse, stream)
+// (positions, k_cache, v_cache, page_table, seq_ids, k_scale, v_scale, k_out, v_out, stream)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> int {
+        const Checks c;
+        nvfp4_cache_read_args g{};
+        const Caches cache = caches(c, a[1], a[2]);
+        const at::Tensor& pos = c.whole(a[0], "positions", kI32, 1);
+        g.tokens = size32(pos.size(0), "positions");
+        g.kv_heads = size32(cache.k.size(1), "k_cache");
+        g.head_dim = size32(cache.head_dim, "k_cache");
+        const at::Tensor& table = c.any(a[3], "page_table", kI32, 2);
+        g.seqs = size32(table.size(0), "page_table");
+        if (a[4] != Py_None) g.seq_ids = static_cast<const int32_t*>(c.vector(a[4], "seq_ids", kI32, g.tokens).data_ptr());
+        else if (g.seqs == 0 ? g.tokens != 0 : g.tokens % g.seqs != 0)
+            refuse(PyExc_ValueError, "%s do not divide among the sequences: pass seq_ids", "the tokens");
+        const at::Tensor& ko = c.whole(a[7], "k_out", kBf16, 3);
+        const at::Tensor& vo = c.whole(a[8], "v_out", kBf16, 3);
+        for (const at::Tensor* t : {&ko, &vo})
+            if (t->size(0) != g.tokens || t->size(1) != g.kv_heads || t->size(2) != g.head_dim)
+                refuse(PyExc_ValueError, "%s must be [tokens, kv_heads, head_dim]", t == &ko ? "k_out" : "v_out");
+        g.positions = static_cast<const int32_t*>(pos.data_ptr());
+        g.k_cache = cache.k.data_ptr(); g.v_cache = cache.v.data_ptr();
+        g.k_page_stride = cache.k.stride(0); g.v_page_stride = cache.v.stride(0);
+        g.k_scale = c.head_scale(a[5], "k_scale", cache.k);
+        g.v_scale = c.head_scale(a[6], "v_scale", cache.v);
+        g.page_table = static_cast<const int32_t*>(table.data_ptr());
+        g.table_stride = table.stride(0);
+        g.k_out = ko.data_ptr(); g.v_out = vo.data_ptr();
+        g.cache_type = cache.type;
+        g.pages = size32(cache.k.size(0), "k_cache");
+        g.max_pages = size32(table.size(1), "page_table");
+        g.page_size = size32(cache.k.size(2), "k_cache");
+        return g_cache_read(&g, c.stream(a[9]));
+    });
+}
+
+// (q, k_cache, v_cache, page_table, lengths, scale, window, softcap, slopes, k_scale, v_scale, workspace, out, lse, stream)
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 13, [&]() -> int {
+    return guarded(n, 15, [&]() -> int {
         const Checks c;
         nvfp4_paged_attention_args g{};
         const at::Tensor& q = c.any(a[0], "q", kBf16, 3);
@@ -281,17 +325,17 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.q_heads = size32(q.size(1), "q");
         g.head_dim = size32(q.size(2), "q");
         g.kv_heads = size32(cache.k.size(1), "k_cache");
-        if (cache.k.size(3) != g.head_dim) refuse(PyExc_ValueError, "%s do not have the head size of q", "the caches");
+        if (cache.head_dim != g.head_dim) refuse(PyExc_ValueError, "%s do not have the head size of q", "the caches");
         if (g.seqs ? tokens % g.seqs != 0 : tokens != 0)
             refuse(PyExc_ValueError, "%s does not have the same number of rows for every sequence of page_table", "q");
         if (g.kv_heads ? g.q_heads % g.kv_heads != 0 : g.q_heads != 0)
             refuse(PyExc_ValueError, "%s do not divide among the kv heads", "the query heads");
         g.rows = g.seqs ? size32(tokens / g.seqs, "q") : 0;
-        const at::Tensor& ws = c.whole(a[9], "workspace", kU8, 1);
-        const at::Tensor& out = c.whole(a[10], "out", kBf16, 3);
+        const at::Tensor& ws = c.whole(a[11], "workspace", kU8, 1);
+        const at::Tensor& out = c.whole(a[12], "out", kBf16, 3);
         same_shape(out, q, "out", "q");
-        if (a[11] != Py_None) {
-            const at::Tensor& lse = c.whole(a[11], "lse", kF32, 2);
+        if (a[13] != Py_None) {
+            const at::Tensor& lse = c.whole(a[13], "lse", kF32, 2);
             if (lse.size(0) != tokens || lse.size(1) != g.q_heads)
                 refuse(PyExc_ValueError, "%s must be [rows, heads] like q", "lse");
             g.lse = static_cast<float*>(lse.data_ptr());
@@ -301,26 +345,29 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.q_token_stride = q.stride(0); g.q_head_stride = q.stride(1);
         g.k_cache = cache.k.data_ptr(); g.v_cache = cache.v.data_ptr();
         g.k_page_stride = cache.k.stride(0); g.v_page_stride = cache.v.stride(0);
-        g.k_scale = c.head_scale(a[7], "k_scale", cache.k);
-        g.v_scale = c.head_scale(a[8], "v_scale", cache.v);
+        g.k_scale = c.head_scale(a[9], "k_scale", cache.k);
+        g.v_scale = c.head_scale(a[10], "v_scale", cache.v);
         g.page_table = static_cast<const int32_t*>(table.data_ptr());
         g.table_stride = table.stride(0);
         g.lengths = static_cast<const int32_t*>(lengths.data_ptr());
-        g.cache_type = code(cache.k);
+        g.cache_type = cache.type;
         g.pages = size32(cache.k.size(0), "k_cache");
         g.max_pages = size32(table.size(1), "page_table");
         g.page_size = size32(cache.k.size(2), "k_cache");
         g.window = static_cast<int32_t>(integer(a[6], "window"));
         g.scale = real(a[5]);
-        return g_paged_attention(&g, c.stream(a[12]));
+        nvfp4_attention_scores scores{};
+        scores.softcap = real(a[7]);
+        if (a[8] != Py_None) scores.slopes = static_cast<const float*>(c.vector(a[8], "slopes", kF32, g.q_heads).data_ptr());
+        return g_paged_attention(&g, &scores, c.stream(a[14]));
     });
 }
 
-// (address of nvfp4_rms_norm, of nvfp4_rope_append, of nvfp4_paged_attention)
+// (address of nvfp4_rms_norm, of nvfp4_rope_append, of nvfp4_cache_read, of nvfp4_paged_attention_scored)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 3, [&]() -> int {
-        void* at[3];
-        for (int i = 0; i < 3; ++i) {
+    return guarded(n, 4, [&]() -> int {
+        void* at[4];
+        for (int i = 0; i < 4; ++i) {
             at[i] = PyLong_AsVoidPtr(a[i]);
             if (!at[i]) {
                 if (PyErr_Occurred()) throw Refused{};
@@ -329,14 +376,15 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         g_rms_norm = reinterpret_cast<RmsNorm>(at[0]);
         g_rope_append = reinterpret_cast<RopeAppend>(at[1]);
-        g_paged_attention = reinterpret_cast<PagedAttention>(at[2]);
+        g_cache_read = reinterpret_cast<CacheRead>(at[2]);
+        g_paged_attention = reinterpret_cast<PagedAttention>(at[3]);
         return 0;
     });
 }
 
 #define NVFP4_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {NVFP4_METHOD(bind), NVFP4_METHOD(rms_norm), NVFP4_METHOD(rope_append), NVFP4_METHOD(paged_attention),
-                           {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {NVFP4_METHOD(bind), NVFP4_METHOD(rms_norm), NVFP4_METHOD(rope_append), NVFP4_METHOD(cache_read),
+                           NVFP4_METHOD(paged_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_decode_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -58,6 +58,44 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
     return d;
 }
 
+// The 4-bit cache: 16 keys (or values) of a kv head are a record of 9 D bytes: E2M1 codes [16][D / 2], element
+// 2j in the low nibble of byte j, then the E4M3 scales of 16 elements each, [D / 16][16 keys]. So a key's
+// codes are whole bytes of its own, which tokens appended side by side can store, any number of records in a
+// page is one contiguous copy, and a lane of the attention kernel finds the scales of its four values' keys in
+// one word.
+constexpr int kRecordKeys = 16;
+__host__ __device__ constexpr int64_t record_bytes(int dim) { return 9ll * dim; }
+
+// Eight E2M1 codes (element 2i in the low nibble of byte i) to four f16x2, low half = even element (exact).
+__device__ __forceinline__ void e2m1x8_f16x2(uint32_t codes, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+        " mov.b32 {b0, b1, b2, b3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+}
+
+// Eight floats to E2M1 codes (element 0 in the lowest nibble), to nearest, ties to the even code, beyond 6 to 6.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float* v) {
+    uint32_t d;
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        " mov.b32 %0, {b0, b1, b2, b3};\n}"
+        : "=r"(d)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return d;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_f16x2(code & 0xffu) & 0xffffu)));
+}
+
 // A quotient x / s from q = x * inv, inv near 1 / s: q put right by its remainder (P. Markstein, IBM J. Res. Dev.
 // 34, 1990). What is stored as E4M3 gets the codes of an fp32 quotient this way (tested against it), at two
 // products a value: q alone took the other code for values beside the middle of two.

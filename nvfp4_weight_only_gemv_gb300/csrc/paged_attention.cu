@@ -3,6 +3,8 @@
 //   s_j = scale * q . k_j  over the keys j that the row sees,   m = max s_j,   l = sum exp(s_j - m)
 //   out = sum exp(s_j - m) v_j / l,   lse = m + log l
 //
+// or, for other scores, with z_j = cap tanh(s_j / cap) - slope[head] * (position - j) in place of s_j.
+//
 // Keys are taken in one pass: a part of them leaves (m, l, sum exp(s - m) v), and two parts join by
 // rescaling both to the larger maximum.
 
@@ -33,8 +35,10 @@ struct AttnParams {
     __nv_bfloat16* out;
     float* lse;
     int64_t q_ts, q_hs;
-    int seqs, rows, hq, hk, group, D, pages, max_pages, page, window, fp8;
+    int seqs, rows, hq, hk, group, D, pages, max_pages, page, window, cache_type;
     float scale;
+    const float* slopes;        // [hq]: how much a score falls with each key of distance, or NULL
+    float cap;                  // of the scores' tanh, or 0
     // tile kernel
     int* counters;              // workspace: arrivals, two per slot of a part: see kCtasPerSm; zero between calls
     float* part_o;              // workspace: unnormalised sums [2 * grid][rows * group][D]
@@ -66,16 +70,33 @@ __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
     return n;
 }
 
-// Values d, d + 32, ... of a key or value row, one lane each.
+// Values d, d + 32, ... of the key or value at `slot` of a page, one lane each.
 template <int V>
-__device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t at, int lane, float (&v)[V]) {
+__device__ __forceinline__ void load_row(const AttnParams& p, int which, int64_t page, int head, int slot, int lane, float (&v)[V]) {
+    if (p.cache_type == NVFP4_E2M1) {
+        const int64_t record = static_cast<int64_t>(head) * (p.page / kRecordKeys) + slot / kRecordKeys;
+        const uint8_t* const rec = static_cast<const uint8_t*>(p.cache[which]) + page * p.page_stride[which] + record * record_bytes(p.D);
+        const int key = slot % kRecordKeys;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int d = lane + 32 * i;
+            v[i] = 0.0f;
+            if (d < p.D) {
+                uint32_t h[4];
+                e2m1x8_f16x2(rec[key * (p.D / 2) + d / 2], h);
+                v[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(d & 1 ? h[0] >> 16 : h[0] & 0xffffu))) *
+                       e4m3_value(rec[8 * p.D + d / 16 * kRecordKeys + key]);
+            }
+        }
+        return;
+    }
+    const int64_t at = page * p.page_stride[which] + (static_cast<int64_t>(head) * p.page + slot) * p.D;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int d = lane + 32 * i;
         v[i] = 0.0f;
         if (d < p.D) {
-            if (p.fp8) v[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(
-                                   e4m3x2_f16x2(static_cast<const uint8_t*>(p.cache[which])[at + d]) & 0xffffu)));
+            if (p.cache_type == NVFP4_E4M3) v[i] = e4m3_value(static_cast<const uint8_t*>(p.cache[which])[at + d]);
             else v[i] = load_one(static_cast<const __nv_bfloat16*>(p.cache[which]) + at + d);
         }
     }
@@ -110,6 +131,7 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
     const int begin = p.window > 0 && end > p.window ? end - p.window : 0;
     float q[V], o[V], m = -INFINITY, l = 0.0f;
     const float ks = p.cache_scale[0] ? p.cache_scale[0][hk] : 1.0f;
+    const float slope = p.slopes ? p.slopes[h] : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int d = lane + 32 * i;
@@ -122,15 +144,17 @@ __global__ void __launch_bounds__(kScalarWarps * 32) paged_attention_scalar_kern
             if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
             continue;
         }
-        const int64_t row = (static_cast<int64_t>(hk) * p.page + (j - pi * p.page)) * p.D;
+        const int slot = j - pi * p.page;
         float x[V], s = 0.0f;
-        load_row(p, 0, page * p.page_stride[0] + row, lane, x);
+        load_row(p, 0, page, hk, slot, lane, x);
 #pragma unroll
         for (int i = 0; i < V; ++i) s = fmaf(q[i], x[i], s);
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
         s *= p.scale * ks;
-        load_row(p, 1, page * p.page_stride[1] + row, lane, x);
+        if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
+        if (p.slopes) s = fmaf(slope, static_cast<float>(j - (end - 1)), s);
+        load_row(p, 1, page, hk, slot, lane, x);
         if (s == -INFINITY) continue;  // weight zero, also while every score was -inf
         const float top = fmaxf(m, s);
         const float keep = m == -INFINITY ? 0.0f : expf(m - top), add = expf(s - top);
@@ -1422,15 +1446,22 @@ extern "C" int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_hea
 }
 
 extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* a, void* stream) {
+    return nvfp4_paged_attention_scored(a, nullptr, stream);
+}
+
+extern "C" nvfp4_status nvfp4_paged_attention_scored(const nvfp4_paged_attention_args* a, const nvfp4_attention_scores* sc,
+                                                     void* stream) {
     using namespace nvfp4;
     using namespace nvfp4::ops;
     if (!a) return NVFP4_ERR_NULL;
     if (!sizes_ok(a->seqs, a->rows, a->q_heads, a->kv_heads, a->head_dim) || a->pages < 0 || a->max_pages < 0 ||
         a->page_size < 1 || a->window < 0)
         return NVFP4_ERR_SHAPE;
-    if ((a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3) ||
+    if (sc && sc->softcap != 0.0f && !(sc->softcap >= 0x1p-40f && sc->softcap <= 0x1p40f)) return NVFP4_ERR_SHAPE;
+    if ((a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3 && a->cache_type != NVFP4_E2M1) ||
         (a->cache_type == NVFP4_BF16 && (a->k_scale || a->v_scale)))
         return NVFP4_ERR_DTYPE;
+    if (a->cache_type == NVFP4_E2M1 && (a->head_dim % 16 || a->page_size % kRecordKeys)) return NVFP4_ERR_SHAPE;
     if (a->seqs == 0 || a->rows == 0 || a->q_heads == 0 || a->head_dim == 0) return NVFP4_OK;
     if (a->head_dim > kMaxDim || a->q_heads > 65535 || static_cast<int64_t>(a->seqs) * a->rows > (1 << 30) ||
         static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))
@@ -1455,10 +1486,11 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
     // no row stands further than that from its sequence's first key, and the kernels may subtract it in 32 bits
     const int64_t reach = static_cast<int64_t>(a->max_pages) * a->page_size + kMaxRows;
     p.window = static_cast<int>(a->window < reach ? a->window : reach);
-    p.fp8 = a->cache_type == NVFP4_E4M3; p.scale = a->scale;
-    const int rows_all = p.rows * p.group, es = p.fp8 ? 1 : 2;
+    p.cache_type = a->cache_type; p.scale = a->scale;
+    if (sc) { p.slopes = sc->slopes; p.cap = sc->softcap; }
+    const int rows_all = p.rows * p.group, es = p.cache_type == NVFP4_BF16 ? 2 : 1;
     TilePlan t;
-    const bool tiles = host_variant() != 1 && p.group <= kMaxGroup && plan_tile(p.D, rows_all, &t);
+    const bool tiles = p.cache_type != NVFP4_E2M1 && !p.slopes && p.cap == 0.0f && host_variant() != 1 && p.group <= kMaxGroup && plan_tile(p.D, rows_all, &t);
     // units are counted in 31 bits: at least 16 keys each, one at least per sequence and column
     const int64_t most_units = (static_cast<int64_t>(a->max_pages) * a->page_size / 16 + 2) * a->seqs * a->kv_heads * t.chunks;
     // Whole 16-byte pieces of keys, and 16 keys of one page at a time; else a key per warp.
@@ -1480,7 +1512,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* 
         p.page_tiles = p.page / 16;
         p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        return p.fp8 ? dispatch_tile<true>(t, p, grid, st) : dispatch_tile<false>(t, p, grid, st);
+        return p.cache_type == NVFP4_E4M3 ? dispatch_tile<true>(t, p, grid, st) : dispatch_tile<false>(t, p, grid, st);
     }
     return launch(paged_attention_scalar_kernel, dim3(a->seqs * a->rows, a->q_heads), dim3(kScalarWarps * 32), 0,
                   static_cast<cudaStream_t>(stream), p);

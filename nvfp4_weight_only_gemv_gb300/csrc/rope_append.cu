@@ -6,7 +6,8 @@
 //   c_i, s_i = mscale * cos, sin(n * inv_freq[i])
 //   (a_i, b_i) = (i, i + half) or, interleaved, (2i, 2i + 1); the head's other values pass through
 // q goes to q_out in bf16, k and v to row n % page of page table[seq][n / page] of the cache
-// [pages, kv heads, page, D], in bf16 or as E4M3(value / scale[kv head]).
+// [pages, kv heads, page, D], in bf16, as E4M3(value / scale[kv head]), or in 4 bits: of 16 neighbours
+// t = value / scale[kv head] a block scale b = E4M3(max|t| / 6) and the codes E2M1(t / b).
 //
 // The kernel moves each value once and is bound by that traffic for prompts, by latency for
 // single tokens.
@@ -35,7 +36,7 @@ struct AppendParams {
     const int32_t* table;
     int64_t table_stride;
     int T, hq, hk, D, half, seqs, per_seq, pages, max_pages, page;
-    int norm_type, interleaved, fp8;
+    int norm_type, interleaved, cache_type;
     float mscale, eps, one_over_d;
     int shares, lanes_log2;  // vector kernel: warps per token, lanes per head
 };
@@ -77,6 +78,14 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, int t, int n, Pl
     return false;
 }
 
+// The E4M3 code of a block's scale from the bits of its largest magnitude `top`: the fp32 quotient by 6, rounded to
+// nearest, at most 448; NaN where top is one.
+__device__ __forceinline__ uint32_t block_scale(uint32_t top) {
+    if (top > 0x7f800000u) return 0x7fu;
+    const float t = fminf(__uint_as_float(top), 8192.0f), inv = 1.0f / 6.0f;  // 8192 / 6 is far beyond 448
+    return pack_e4m3(put_right(t * inv, t, 6.0f, inv), 0.0f) & 0xffu;
+}
+
 // One value a thread, one CTA per (head, token): any head size, alignment and rotary size.
 template <typename XT>
 __global__ void __launch_bounds__(128) rope_append_scalar_kernel(const __grid_constant__ AppendParams p) {
@@ -111,7 +120,7 @@ __global__ void __launch_bounds__(128) rope_append_scalar_kernel(const __grid_co
     Place at{0, 0};
     const bool ok = part == 0 ? n >= 0 : place_of(p, t, n, at);
     if (part != 0 && !ok) return;
-    for (int d = tid; d < p.D; d += 128) {
+    auto turned = [&](int d) {
         float y = u[d];
         if (part < 2 && d < 2 * p.half) {
             const int i = p.interleaved ? d >> 1 : d % p.half;
@@ -122,11 +131,36 @@ __global__ void __launch_bounds__(128) rope_append_scalar_kernel(const __grid_co
             cs.y *= p.mscale;
             y = first ? y * cs.x - other * cs.y : y * cs.x + other * cs.y;
         }
+        return y;
+    };
+    if (part > 0 && p.cache_type == NVFP4_E2M1) {
+        // 16 lanes hold a block: its largest magnitude (a NaN's is the largest of all), its scale, its codes
+        const float* const sc = p.cache_scale[part - 1];
+        const int64_t record = static_cast<int64_t>(h) * (p.page / kRecordKeys) + at.slot / kRecordKeys;
+        uint8_t* const rec = static_cast<uint8_t*>(p.cache[part - 1]) + at.page * p.page_stride[part - 1] + record * record_bytes(p.D);
+        const int key = at.slot % kRecordKeys;
+        for (int first = 0; first < p.D; first += 128) {  // every lane goes through the shuffles
+            const int d = first + tid;
+            const float v = d < p.D ? turned(d) / (sc ? sc[h] : 1.0f) : 0.0f;
+            uint32_t top = __float_as_uint(v) & 0x7fffffffu;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t b = block_scale(top);
+            const float bs = e4m3_value(b), mine = bs == 0.0f ? 0.0f : v / bs;
+            const float pair[8] = {mine, __shfl_xor_sync(0xffffffffu, mine, 1), 0, 0, 0, 0, 0, 0};
+            if (d >= p.D) continue;
+            if ((d & 1) == 0) rec[key * (p.D / 2) + d / 2] = static_cast<uint8_t>(pack_e2m1x8(pair));
+            if (d % 16 == 0) rec[8 * p.D + d + key] = static_cast<uint8_t>(b);
+        }
+        return;
+    }
+    for (int d = tid; d < p.D; d += 128) {
+        const float y = turned(d);
         if (part == 0) {
             p.q_out[(static_cast<int64_t>(t) * p.hq + h) * p.D + d] = __float2bfloat16_rn(ok ? y : 0.0f);
         } else {
             const int64_t to = at.page * p.page_stride[part - 1] + (static_cast<int64_t>(h) * p.page + at.slot) * p.D + d;
-            if (p.fp8) {
+            if (p.cache_type == NVFP4_E4M3) {
                 const float* sc = p.cache_scale[part - 1];
                 static_cast<uint8_t*>(p.cache[part - 1])[to] = static_cast<uint8_t>(pack_e4m3(y / (sc ? sc[h] : 1.0f), 0.0f));
             } else {
@@ -263,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
         const int64_t between = part == 0 ? p.D : static_cast<int64_t>(p.page) * p.D;
         const int64_t row = (part == 0 ? static_cast<int64_t>(tok) * p.hq * p.D
                                        : at.page * p.page_stride[part - 1] + static_cast<int64_t>(at.slot) * p.D) + h * between;
-        const int y_size = part > 0 && p.fp8 ? 1 : 2;
+        const int y_size = part > 0 && p.cache_type == NVFP4_E4M3 ? 1 : 2;
         char* y = (part == 0 ? reinterpret_cast<char*>(p.q_out) : static_cast<char*>(p.cache[part - 1])) + row * y_size;
         const int64_t y_step = hpi * between * y_size;
         auto head = [&](Piece<XT, V>& ra, Piece<XT, V>& rb) {
@@ -305,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
                 for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
             }
             if (live && h < heads) {
-                if (part > 0 && p.fp8) {
+                if (part > 0 && p.cache_type == NVFP4_E4M3) {
                     const float* const sc = p.cache_scale[part - 1];
                     if (sc) {
                         float scale = sc[h];
@@ -357,10 +391,11 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         a->pages < 0 || a->max_pages < 0 || a->page_size < 1 || 2 * static_cast<int64_t>(a->rotary_half) > a->head_dim ||
         !(a->eps >= 0.0f))
         return NVFP4_ERR_SHAPE;
-    if ((a->x_type != NVFP4_F32 && a->x_type != NVFP4_BF16) || (a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3) ||
+    if ((a->x_type != NVFP4_F32 && a->x_type != NVFP4_BF16) || (a->cache_type != NVFP4_BF16 && a->cache_type != NVFP4_E4M3 && a->cache_type != NVFP4_E2M1) ||
         (a->cache_type == NVFP4_BF16 && (a->k_scale || a->v_scale)) ||
         ((a->q_norm || a->k_norm) && a->norm_type != NVFP4_F32 && a->norm_type != NVFP4_BF16))
         return NVFP4_ERR_DTYPE;
+    if (a->cache_type == NVFP4_E2M1 && (a->head_dim % 16 || a->page_size % kRecordKeys)) return NVFP4_ERR_SHAPE;
     if (a->tokens == 0 || a->head_dim == 0 || hq + a->kv_heads == 0) return NVFP4_OK;
     if (a->head_dim > 1024 || static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(a->kv_heads) > 65535 ||
         static_cast<int64_t>(a->max_pages) * a->page_size > (1 << 24))
@@ -383,12 +418,12 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
     p.T = a->tokens; p.hq = hq; p.hk = a->kv_heads; p.D = a->head_dim; p.half = a->rotary_half;
     p.seqs = a->seqs; p.per_seq = a->seqs > 0 ? (a->tokens + a->seqs - 1) / a->seqs : 1;
     p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
-    p.norm_type = a->norm_type; p.interleaved = a->interleaved; p.fp8 = a->cache_type == NVFP4_E4M3;
+    p.norm_type = a->norm_type; p.interleaved = a->interleaved; p.cache_type = a->cache_type;
     p.mscale = a->mscale; p.eps = a->eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     p.one_over_d = 1.0f / static_cast<float>(p.D);
     // Whole vectors of V values on their boundaries, for V = 8, then 4; else a value per thread.
-    const int eb = type_bytes(a->x_type), nb = type_bytes(p.norm_type), cb = p.fp8 ? 1 : 2;
+    const int eb = type_bytes(a->x_type), nb = type_bytes(p.norm_type), cb = p.cache_type == NVFP4_BF16 ? 2 : 1;
     auto fits = [&](int v) {
         auto on = [&](const void* q, int bytes) { return aligned(q, bytes < 16 ? bytes : 16); };
         bool ok = p.D % (2 * v) == 0 && p.D <= 32 * 2 * v && p.half % v == 0 && on(p.q_out, 2 * v) && on(p.q_norm, nb * v) &&
@@ -397,7 +432,7 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;
         return ok;
     };
-    const int v = host_variant() == 1 ? 0 : fits(8) ? 8 : fits(4) ? 4 : 0;
+    const int v = host_variant() == 1 || p.cache_type == NVFP4_E2M1 ? 0 : fits(8) ? 8 : fits(4) ? 4 : 0;
     if (v) {
         while ((2 * v << p.lanes_log2) < p.D) ++p.lanes_log2;
         // A token's heads are shared among warps, down to one step each, until the SMs' warps are filled twice

@@ -1,4 +1,4 @@
-"""The decode step's operators between the products: norm, rotary append, paged attention.
+"""The decode step's operators between the products: norm, rotary append, paged attention, cache rows read back.
 
 Like the products, these functions pass pointers, sizes and the current CUDA stream to the C ABI in
 ``include/nvfp4_gemv.h``; there is no other path. They are called many times per token on rows of
@@ -7,6 +7,11 @@ a few kilobytes, so their checks and marshalling are native too (``csrc/decode_o
 The cache: ``k_cache`` and ``v_cache`` [pages, kv_heads, page_size, head_dim] (bfloat16, or
 float8_e4m3fn with float32 scales per kv head), contiguous inside a page (``kv_cache`` makes a
 pair). ``page_table`` int32 [seqs, max_pages] names each sequence's pages in order.
+
+Or in 4 bits: uint8 [pages, kv_heads, page_size, 9 * head_dim / 16], head_dim and page_size multiples of 16. The
+bytes of every 16 keys of a head are a record: their E2M1 codes [16][head_dim / 2] (element 2j in the low nibble of
+byte j), then E4M3 scales of 16 elements each, [head_dim / 16][16 keys]. An element stands for code * block scale,
+times the float32 scale of its kv head where one is given.
 """
 from __future__ import annotations
 
@@ -25,13 +30,16 @@ import nvfp4_weight_only_gemv_gb300 as _nv
 
 from . import build as _build
 
-_F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_F32, _BF16, _E4M3, _U8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.uint8
 
-# the C structs nvfp4_rms_norm_args, nvfp4_rope_append_args and nvfp4_paged_attention_args as bytes, for
-# the C entry points called through the ctypes library (the tests of their checks do)
+# the C structs nvfp4_rms_norm_args, nvfp4_rope_append_args, nvfp4_cache_read_args, nvfp4_paged_attention_args and
+# nvfp4_attention_scores as bytes, for the C entry points called through the ctypes library (the tests of
+# their checks do)
 _NORM = struct.Struct("@6P4q7if").pack
 _APPEND = struct.Struct("@14P9q13i2f4x").pack
+_READ = struct.Struct("@9P3q8i").pack
 _ATTEND = struct.Struct("@10P6q10if4x").pack
+_SCORES = struct.Struct("@Pf4x").pack
 
 
 class _Unbound:
@@ -62,7 +70,7 @@ def _bound():
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_decode_ops", path, loader=loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                  for f in (lib.nvfp4_rms_norm, lib.nvfp4_rope_append, lib.nvfp4_paged_attention)))
+                  for f in (lib.nvfp4_rms_norm, lib.nvfp4_rope_append, lib.nvfp4_cache_read, lib.nvfp4_paged_attention_scored)))
     return module
 
 
@@ -116,9 +124,14 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out
 
 def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16, device=None):
     """A zeroed pair of caches (k, v), each [pages, kv_heads, page_size, head_dim], halves of one
-    allocation in which a page's keys and values are neighbours."""
-    if dtype not in (_BF16, _E4M3):
-        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn (got {dtype})")
+    allocation in which a page's keys and values are neighbours. dtype uint8 makes 4-bit caches, with 9 / 16
+    of head_dim bytes in the last dimension."""
+    if dtype not in (_BF16, _E4M3, _U8):
+        raise TypeError(f"a cache is bfloat16, float8_e4m3fn or uint8 (4 bits) (got {dtype})")
+    if dtype is _U8:
+        if head_dim % 16 or page_size % 16:
+            raise ValueError(f"a 4-bit cache has heads and pages of multiples of 16 (got {head_dim} and {page_size})")
+        head_dim = 9 * head_dim // 16
     both = torch.zeros((pages, 2, kv_heads, page_size, head_dim), dtype=dtype, device=device or "cuda")
     return both[:, 0], both[:, 1]
 
@@ -164,7 +177,8 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_
     many) say where each token stands; a negative position is padding. inv_freq float32 [half]
     turns the first 2 * half values of a head, in halves or ``interleaved`` pairs; mscale multiplies
     cos and sin (rope_frequencies gives both). q_norm, k_norm [D]: root-mean-square norm of each
-    head first. k_scale, v_scale float32 [kv_heads]: what an 8-bit cache's values are divided by."""
+    head first. k_scale, v_scale float32 [kv_heads]: what the values of an 8-bit or 4-bit cache are divided
+    by. In a 4-bit cache each 16 neighbours get a block scale of their own, E4M3(largest magnitude / 6)."""
     if stream is not None and out is None:
         return _nv._on_stream(stream, rope_append, q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_ids,
                               interleaved=interleaved, mscale=mscale, q_norm=q_norm, k_norm=k_norm, eps=eps,
@@ -178,6 +192,36 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_
     if st:
         raise _nv.NVFP4Error(st, "nvfp4_rope_append")
     return out
+
+
+def cache_read(positions, k_cache, v_cache, page_table, seq_ids=None, *, k_scale=None, v_scale=None, k_out=None,
+               v_out=None, stream=None):
+    """What the cache holds for the given tokens, as a pair (k, v) of bfloat16 [tokens, kv_heads, D].
+
+    positions and seq_ids name tokens as in rope_append; k_scale and v_scale are the scales that it was given. A
+    prompt's own attention over these rows sees the keys that every later step will see. Padding (a negative
+    position) gives zeros."""
+    if stream is not None and (k_out is None or v_out is None):
+        return _nv._on_stream(stream, cache_read, positions, k_cache, v_cache, page_table, seq_ids, k_scale=k_scale,
+                              v_scale=v_scale, k_out=k_out, v_out=v_out)
+    if k_out is None:
+        k_out = _like(positions, "positions", _BF16, _rows_shape(positions, k_cache))
+    if v_out is None:
+        v_out = _like(positions, "positions", _BF16, _rows_shape(positions, k_cache))
+    if stream is not None:
+        stream = _handle(stream)
+    st = _native.cache_read(positions, k_cache, v_cache, page_table, seq_ids, k_scale, v_scale, k_out, v_out, stream)
+    if st:
+        raise _nv.NVFP4Error(st, "nvfp4_cache_read")
+    return k_out, v_out
+
+
+def _rows_shape(positions, k_cache):
+    """[tokens, kv_heads, D] as bfloat16 rows of a cache; empty where the call will be refused anyway."""
+    if getattr(positions, "dim", int)() != 1 or getattr(k_cache, "dim", int)() != 4:
+        return (0, 0, 0)
+    d = k_cache.shape[3]
+    return (positions.shape[0], k_cache.shape[1], d // 9 * 16 if k_cache.dtype is _U8 else d)
 
 
 def attention_workspace_bytes(seqs: int, rows: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -206,20 +250,22 @@ def _workspace_for(q, k_cache, page_table):
 
 
 def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: Optional[float] = None, *, window: int = 0,
-                    k_scale=None, v_scale=None, workspace=None, out=None, lse=None, stream=None):
+                    softcap: float = 0.0, slopes=None, k_scale=None, v_scale=None, workspace=None, out=None, lse=None, stream=None):
     """softmax(scale * q . k) v over the cached keys, for the newest tokens of each sequence.
 
     q bfloat16 [seqs * rows, q_heads, D] holds the newest ``rows`` (1 to 8) tokens of each sequence,
     the rows of a sequence together; lengths int32 [seqs] counts each sequence's cached tokens, these
     included. Row r sees the keys up to its own position, lengths - rows + r, and with ``window``
-    only the last ``window`` of them. q_heads is a multiple of the cache's kv heads. scale: 1 /
+    only the last ``window`` of them. With ``softcap`` (2^-40 to 2^40; 0 for none) a score s becomes
+    softcap * tanh(s / softcap); with ``slopes`` (float32 [q_heads]) it then falls by its head's slope for each
+    key of distance from the row's own position. q_heads is a multiple of the cache's kv heads. scale: 1 /
     sqrt(D) unless given. ``lse``: an optional float32 [seqs * rows, q_heads] tensor that receives
     the log of each row's sum of exponentials. ``workspace``: a uint8 tensor zeroed before its first
     use, of at least attention_workspace_bytes; None allocates one for this call. Returns bfloat16
     like q; rows that see no key are zero (lse -inf)."""
     if stream is not None and (out is None or workspace is None):
         return _nv._on_stream(stream, paged_attention, q, k_cache, v_cache, page_table, lengths, scale, window=window,
-                              k_scale=k_scale, v_scale=v_scale, workspace=workspace, out=out, lse=lse)
+                              softcap=softcap, slopes=slopes, k_scale=k_scale, v_scale=v_scale, workspace=workspace, out=out, lse=lse)
     if out is None:
         out = _like(q, "q", _BF16)
     if workspace is None:
@@ -227,7 +273,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: Optional[fl
     if stream is not None:
         stream = _handle(stream)
     st = _native.paged_attention(q, k_cache, v_cache, page_table, lengths, q.shape[-1] ** -0.5 if scale is None else scale,
-                                 window, k_scale, v_scale, workspace, out, lse, stream)
+                                 window, softcap, slopes, k_scale, v_scale, workspace, out, lse, stream)
     if st:
         raise _nv.NVFP4Error(st, "nvfp4_paged_attention")
     return out
