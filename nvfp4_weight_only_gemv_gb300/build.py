@@ -10,7 +10,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRC = os.path.join(PKG_DIR, "csrc", "nvfp4_gemv.cu")
 OPERATORS = tuple(os.path.join(PKG_DIR, "csrc", f) for f in ("rms_norm.cu", "rope_append.cu", "cache_read.cu", "paged_attention.cu",
-                                                           "paged_attention_4bit.cu", "paged_attention_scores.cu"))
+                                                           "paged_attention_4bit.cu", "paged_attention_scores.cu",
+                                                           "paged_attention_4bit_scores.cu"))
 HEADER = os.path.join(ROOT, "include", "nvfp4_gemv.h")
 BINDING = os.path.join(PKG_DIR, "csrc", "decode_ops_binding.cpp")
 SOURCES = (SRC, *OPERATORS, *(os.path.join(PKG_DIR, "csrc", f) for f in ("ops_common.cuh", "paged_attention.cuh")), HEADER)

@@ -224,8 +224,9 @@ extern "C" nvfp4_status nvfp4_paged_attention_scored(const nvfp4_paged_attention
         p.page_tiles = p.page / 16;
         p.q_vec = aligned(p.q, 8) && p.q_ts % 4 == 0 && p.q_hs % 4 == 0;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        if (p.cache_type == NVFP4_E2M1) return launch_tiles_4bit(t, p, grid, st);
-        if (p.slopes || p.cap > 0.0f) return launch_tiles_scored(t, p, grid, st);
+        const bool scored = p.slopes || p.cap > 0.0f;
+        if (p.cache_type == NVFP4_E2M1) return scored ? launch_tiles_4bit_scored(t, p, grid, st) : launch_tiles_4bit(t, p, grid, st);
+        if (scored) return launch_tiles_scored(t, p, grid, st);
         return p.cache_type == NVFP4_E4M3 ? dispatch_tile<NVFP4_E4M3, false>(t, p, grid, st)
                                           : dispatch_tile<NVFP4_BF16, false>(t, p, grid, st);
     }

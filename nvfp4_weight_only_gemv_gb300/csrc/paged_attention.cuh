@@ -7,10 +7,8 @@
 //
 // Keys are taken in one pass: a part of them leaves (m, l, sum exp(s - m) v), and two parts join by
 // rescaling both to the larger maximum.
-
 //
-// The tile kernel, its plan and its launch; paged_attention.cu, paged_attention_4bit.cu and paged_attention_scores.cu
-// each make some of its instances.
+// The tile kernel, its plan and its launch; the paged_attention*.cu files each make some of its instances.
 #pragma once
 
 #include "ops_common.cuh"
@@ -64,9 +62,10 @@ struct TilePlan {
     int chunks = 1, chunk_rows = 0;  // of a kv head's query rows
 };
 
-// Launches the tile kernel over a cache of 4 bits (paged_attention_4bit.cu), or with scores that are
-// capped or biased over a cache of bf16 or E4M3 (paged_attention_scores.cu).
+// Launches the tile kernel over a cache of 4 bits, with scores that are capped or biased over a cache of bf16 or
+// E4M3, or with such scores over 4 bits: each in a translation unit of its own.
 nvfp4_status launch_tiles_4bit(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream);
+nvfp4_status launch_tiles_4bit_scored(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream);
 nvfp4_status launch_tiles_scored(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream);
 
 }  // namespace attn
@@ -167,13 +166,13 @@ struct TileShape {
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
     static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? kCtasPerSm : 2;  // per SM
-    static constexpr bool kQRegs = NT * DP <= 256;
+    static constexpr bool kQRegs = !kF4 && NT * DP <= 256;
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
     static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
     static constexpr int kBox = 16 * kBoxBytes;
     static constexpr int kPart = kF4 ? kHalves * 9 * DP : kHalves * kBoxes * kBox;  // K (or V) bytes of a tile
-    static constexpr int kStages = kF4 ? (DP == 128 && NT == 1 ? 1 : NT == 4 ? 4 : 2)
+    static constexpr int kStages = kF4 ? (NT == 4 ? 4 : DP == 128 && NT == 1 ? 1 : 2)
                                  : DP * kES == 512 ? 1 : NT * DP == 256 ? 3 : NT * DP <= 128 ? 1 : 2;
     static constexpr int kRing = kWarps * kStages * 2 * kPart;
     static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
@@ -621,32 +620,33 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
     if (arrive_last(sh, done, of)) join(0, size < parts ? size : 1, of, -1);
 }
 
-// DP, NT: see TileShape; C: the cache's type; S: scores with a cap or a bias.
+// DP, NT: see TileShape; C: the cache's type; S: scores with a cap or a bias; W: D is DP (4 bits: a lane's offsets in
+// a record are then constants of its loads).
 template <int C>
 using KernelParams = std::conditional_t<C == NVFP4_E2M1, AttnParams, TileParams>;
 
-template <int DP, int NT, int C, bool S>
+template <int DP, int NT, int C, bool S, bool W>
 __global__ void __launch_bounds__(TileShape<DP, NT, C>::kWarps * 32, TileShape<DP, NT, C>::kCtas)
 paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
     using T = TileShape<DP, NT, C>;
     constexpr bool F16 = T::kF16, F4 = T::kF4;
-    constexpr int H = T::kHalves, W = T::kWarps, kThreads = W * 32;
+    constexpr int H = T::kHalves, kWarps = T::kWarps, kThreads = kWarps * 32;
     constexpr int kRowsW = 8 * NT;
     constexpr float lift = F16 ? kLift : 0.0f;
     extern __shared__ uint8_t smem_raw[];
     // rings [W][kStages][K, V], on a boundary of the swizzle's pattern; then s_q
     float* const smem = reinterpret_cast<float*>(smem_raw + (-static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u));
-    __shared__ __align__(8) uint64_t s_bar[W][T::kStages][2];
-    __shared__ int s_scan[W];
-    __shared__ float s_f[8 * NT * W];  // rows' factors (not kQRegs)
+    __shared__ __align__(8) uint64_t s_bar[kWarps][T::kStages][2];
+    __shared__ int s_scan[kWarps];
+    __shared__ float s_f[8 * NT * kWarps];  // rows' factors (not kQRegs)
     __shared__ Run s_run;
     __shared__ JoinShared s_join;
     float* s_o = smem;                                        // merge, in the rings' place: [W][kRowsW][kOStride]
-    float2* s_ml = reinterpret_cast<float2*>(s_o + W * kRowsW * T::kOStride);  // [W][kRowsW]
+    float2* s_ml = reinterpret_cast<float2*>(s_o + kWarps * kRowsW * T::kOStride);  // [W][kRowsW]
     uint2* s_q = reinterpret_cast<uint2*>(smem + T::kMain / 4);  // [row_blocks][NT][kQ][32] (not kQRegs)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = W / p.row_blocks;
+    const int rb = warp % p.row_blocks, stream = warp / p.row_blocks, streams = kWarps / p.row_blocks;
     const int rows_all = p.rows * p.group;
     const int unit_keys = streams * T::kKeys, align = p.tall_box ? T::kKeys : 16;
 
@@ -741,7 +741,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         if (lane == 31) s_scan[warp] = incl;
         __syncthreads();
         int total = 0, before = incl - mine;
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < kWarps; ++i) {
             if (i < warp) before += s_scan[i];
             total += s_scan[i];
         }
@@ -784,8 +784,9 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
     // k_row + 2 of a record; so lane t's four keys of the second product are 4t .. 4t + 3, whose scales are one
     // word, in an order in which two lanes' rows lie in different halves of the banks.
     const int swap = t & 1, k_row = 4 * (g >> 1) + ((g & 1) ^ (g >> 1 & 1));
-    const uint32_t rec = 9 * p.D;
-    const int last_block = (p.D >> 4) - 1;  // blocks beyond the head's end are read as its last: their queries are zero
+    const int dim = W ? DP : p.D;
+    const uint32_t rec = 9 * dim;
+    const int last_block = (dim >> 4) - 1;  // blocks beyond the head's end are read as its last: their queries are zero
 
     // --- the ring's state. Tiles of this warp: stream, stream + streams, ... of the run's part of an item. A
     // tile's first 16-key block stands at block `slot` of the sequence's page `page`; both walk along.
@@ -1041,15 +1042,15 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                 // lane t has blocks t, t + 4, ... of its two keys' elements: codes to f16, times the block's scale (exact)
 #pragma unroll
                 for (int c = 0; c < T::kKC; ++c) {
-                    const int block = min(t + 4 * c, last_block);
-                    const uint32_t from = ring + 2 * cur * T::kPart + k_row * (p.D >> 1) + 8 * block;
-                    const uint32_t from_scale = ring + 2 * cur * T::kPart + 8 * p.D + 16 * block + (k_row & ~3);
+                    const int block = (W ? t + 4 * c : min(t + 4 * c, last_block));
+                    const uint32_t from = ring + 2 * cur * T::kPart + k_row * (dim >> 1) + 8 * block;
+                    const uint32_t from_scale = ring + 2 * cur * T::kPart + 8 * dim + 16 * block + (k_row & ~3);
                     uint2 x[H], y[H];
                     uint32_t sx[H], sy[H];
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         x[i] = lds8(from + i * rec);
-                        y[i] = lds8(from + i * rec + p.D);
+                        y[i] = lds8(from + i * rec + dim);
                         const uint32_t s4 = __byte_perm(lds4(from_scale + i * rec), 0, k_row & 1 ? 0x3311 : 0x2200);
                         sx[i] = e4m3x2_f16x2(s4);
                         sy[i] = e4m3x2_f16x2(s4 >> 16);
@@ -1240,20 +1241,20 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     const uint32_t from = ring + (2 * cur + 1) * T::kPart + i * rec;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {  // keys 4t .. 4t + 3, neighbours swapped in every other lane
-                        const uint32_t row = from + (4 * t + (k ^ swap)) * (p.D >> 1);
+                        const uint32_t row = from + (4 * t + (k ^ swap)) * (dim >> 1);
                         if constexpr (DP == 64) {
-                            vr[k][0] = lds4(row + min(8 * (g >> 1), 8 * last_block) + 4 * (g & 1));
+                            vr[k][0] = lds4(row + (W ? 8 * (g >> 1) : min(8 * (g >> 1), 8 * last_block)) + 4 * (g & 1));
                         } else {
 #pragma unroll
                             for (int c = 0; c < T::kVW / 2; ++c) {
-                                const uint2 v = lds8(row + 8 * min(g + 8 * c, last_block));
+                                const uint2 v = lds8(row + 8 * (W ? g + 8 * c : min(g + 8 * c, last_block)));
                                 vr[k][2 * c] = v.x; vr[k][2 * c + 1] = v.y;
                             }
                         }
                     }
 #pragma unroll
                     for (int c = 0; c < (DP == 256 ? 2 : 1); ++c)
-                        vs[c] = __byte_perm(lds4(from + 8 * p.D + 16 * min((DP == 64 ? g >> 1 : g) + 8 * c, last_block) + 4 * t), 0,
+                        vs[c] = __byte_perm(lds4(from + 8 * dim + 16 * (W ? (DP == 64 ? g >> 1 : g) + 8 * c : min((DP == 64 ? g >> 1 : g) + 8 * c, last_block)) + 4 * t), 0,
                                             swap ? 0x2301 : 0x3210);
                     return;
                 }
@@ -1288,22 +1289,27 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     }
                 }
             };
-            uint32_t pair[4];   // 4 bits: eight codes of the lane's first two and last two keys, side by side: those of
-                                // even and of odd elements
+            uint32_t wide[4][4];  // 4 bits: operands of four products, from a word of each key
             auto operands = [&](int mt, uint32_t (&a)[4]) {
                 if constexpr (F4) {
                     const int w = mt >> 2, j = mt & 3;
                     if (j == 0) {
+                        const uint32_t s4 = vs[DP == 256 ? w >> 1 : 0];
 #pragma unroll
                         for (int k = 0; k < 4; k += 2) {
-                            const uint32_t x = vr[k][w], y = vr[k + 1][w];
-                            pair[k] = (x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u);
-                            pair[k + 1] = (x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+                            // the codes of two keys side by side, of even and of odd elements
+                            const uint32_t x = vr[k][w], y = vr[k + 1][w], scales = e4m3x2_f16x2(s4 >> 8 * k);
+                            e2m1x8_f16x2((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), wide[k]);
+                            e2m1x8_f16x2((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), wide[k + 1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                wide[k][e] = mul_f16x2(wide[k][e], scales);
+                                wide[k + 1][e] = mul_f16x2(wide[k + 1][e], scales);
+                            }
                         }
                     }
-                    const uint32_t s4 = vs[DP == 256 ? w >> 1 : 0], s01 = e4m3x2_f16x2(s4), s23 = e4m3x2_f16x2(s4 >> 16);
-                    a[0] = mul_f16x2(e2m1x2_f16x2(pair[0] >> 8 * j), s01); a[1] = mul_f16x2(e2m1x2_f16x2(pair[1] >> 8 * j), s01);
-                    a[2] = mul_f16x2(e2m1x2_f16x2(pair[2] >> 8 * j), s23); a[3] = mul_f16x2(e2m1x2_f16x2(pair[3] >> 8 * j), s23);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) a[k] = wide[k][j];
                 } else if constexpr (F16) {
                     const int w = mt >> 1;
                     const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
@@ -1487,7 +1493,7 @@ bool encode_maps(TileParams& p) {
     return true;
 }
 
-template <int DP, int NT, int C, bool S>
+template <int DP, int NT, int C, bool S, bool W>
 nvfp4_status launch_tile(const AttnParams& a, int grid, cudaStream_t stream) {
     using T = TileShape<DP, NT, C>;
     KernelParams<C> p;
@@ -1499,21 +1505,21 @@ nvfp4_status launch_tile(const AttnParams& a, int grid, cudaStream_t stream) {
     }
     const size_t smem = 1024 + T::kMain + (T::kQRegs ? 0 : static_cast<size_t>(p.row_blocks) * NT * T::kQ * 256);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attention_tile_kernel<DP, NT, C, S>,
+        const cudaError_t e = cudaFuncSetAttribute(paged_attention_tile_kernel<DP, NT, C, S, W>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return host_cuda_fail(e);
     }
-    return launch(paged_attention_tile_kernel<DP, NT, C, S>, dim3(grid), dim3(T::kWarps * 32), smem, stream, p);
+    return launch(paged_attention_tile_kernel<DP, NT, C, S, W>, dim3(grid), dim3(T::kWarps * 32), smem, stream, p);
 }
 
-template <int C, bool S>
+template <int C, bool S, bool W = false>
 nvfp4_status dispatch_tile(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream) {
-    if (t.dp == 256) return launch_tile<256, 1, C, S>(p, grid, stream);
+    if (t.dp == 256) return launch_tile<256, 1, C, S, W>(p, grid, stream);
     if (t.dp == 128)
-        return t.nt == 1 ? launch_tile<128, 1, C, S>(p, grid, stream) : t.nt == 2 ? launch_tile<128, 2, C, S>(p, grid, stream)
-                                                                                  : launch_tile<128, 4, C, S>(p, grid, stream);
-    return t.nt == 1 ? launch_tile<64, 1, C, S>(p, grid, stream) : t.nt == 2 ? launch_tile<64, 2, C, S>(p, grid, stream)
-                                                                             : launch_tile<64, 4, C, S>(p, grid, stream);
+        return t.nt == 1 ? launch_tile<128, 1, C, S, W>(p, grid, stream) : t.nt == 2 ? launch_tile<128, 2, C, S, W>(p, grid, stream)
+                                                                                  : launch_tile<128, 4, C, S, W>(p, grid, stream);
+    return t.nt == 1 ? launch_tile<64, 1, C, S, W>(p, grid, stream) : t.nt == 2 ? launch_tile<64, 2, C, S, W>(p, grid, stream)
+                                                                             : launch_tile<64, 4, C, S, W>(p, grid, stream);
 }
 
 }  // namespace

@@ -3,6 +3,6 @@
 #include "paged_attention.cuh"
 
 nvfp4_status nvfp4::attn::launch_tiles_4bit(const TilePlan& t, const AttnParams& p, int grid, cudaStream_t stream) {
-    if (p.slopes || p.cap > 0.0f) return dispatch_tile<NVFP4_E2M1, true>(t, p, grid, stream);
-    return dispatch_tile<NVFP4_E2M1, false>(t, p, grid, stream);
+    if (p.D == t.dp) return dispatch_tile<NVFP4_E2M1, false, true>(t, p, grid, stream);
+    return dispatch_tile<NVFP4_E2M1, false, false>(t, p, grid, stream);
 }
