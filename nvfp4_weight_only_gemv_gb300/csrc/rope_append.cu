@@ -227,7 +227,37 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
     return put_right(fminf(fmaxf(x * inv, -512.0f), 512.0f), x, s, inv);
 }
 
-template <typename XT, int V>
+// Scales of which 1 / scale might not be normal are taken times a power of two, with the values.
+template <int V>
+__device__ __forceinline__ void lift_scale(float& scale, float (&a)[V], float (&b)[V]) {
+    if (fabsf(scale) >= 0x1p-100f && fabsf(scale) <= 0x1p100f) return;
+    const float lift = fabsf(scale) < 1.0f ? 0x1p64f : 0x1p-64f;
+    scale *= lift;
+#pragma unroll
+    for (int e = 0; e < V; ++e) { a[e] *= lift; b[e] *= lift; }
+}
+
+// Beyond any block's largest value that a scale can still express.
+constexpr float kFar = 8192.0f;
+
+// x / s for |x / s| up to `most` and something beyond for what lies beyond; as put_right, and a zero keeps its sign.
+__device__ __forceinline__ float quotient_to(float most, float x, float s, float inv) {
+    const float q = fminf(fmaxf(x * inv, -most), most);
+    return fmaf(fmaf(q, s, -x), -inv, q);
+}
+
+// The E2M1 codes of eight values of a block whose scale stands for b.
+__device__ __forceinline__ uint32_t block_codes(float (&v)[8], float b) {
+    if (b == 0.0f) return 0u;
+    const float inv = 1.0f / b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = quotient_to(8.0f, v[e], b, inv);
+    return pack_e2m1x8(v);
+}
+
+// F4: a cache of 4 bits. A lane's vectors are halves of two blocks, whose other halves its neighbour has, or, where
+// pairs are neighbours or do not turn, one block.
+template <typename XT, int V, bool F4>
 __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int kDepth = sizeof(XT) == 2 ? 2 : 1;   // heads requested ahead
     extern __shared__ __align__(16) float2 cs_all[];  // [warps][half]
@@ -294,10 +324,12 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
             }
         }
         // the head's row in the output or the cache, bytes
-        const int64_t between = part == 0 ? p.D : static_cast<int64_t>(p.page) * p.D;
+        const bool records = F4 && part > 0;
+        const int64_t between = part == 0 ? p.D : records ? p.page / kRecordKeys * record_bytes(p.D) : static_cast<int64_t>(p.page) * p.D;
         const int64_t row = (part == 0 ? static_cast<int64_t>(tok) * p.hq * p.D
-                                       : at.page * p.page_stride[part - 1] + static_cast<int64_t>(at.slot) * p.D) + h * between;
-        const int y_size = part > 0 && p.cache_type == NVFP4_E4M3 ? 1 : 2;
+                                       : at.page * p.page_stride[part - 1] + (records ? at.slot / kRecordKeys * record_bytes(p.D)
+                                                                                      : static_cast<int64_t>(at.slot) * p.D)) + h * between;
+        const int y_size = part > 0 && p.cache_type != NVFP4_BF16 ? 1 : 2;
         char* y = (part == 0 ? reinterpret_cast<char*>(p.q_out) : static_cast<char*>(p.cache[part - 1])) + row * y_size;
         const int64_t y_step = hpi * between * y_size;
         auto head = [&](Piece<XT, V>& ra, Piece<XT, V>& rb) {
@@ -338,17 +370,48 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
 #pragma unroll
                 for (int e = 0; e < V; ++e) a[e] = b[e] = 0.0f;
             }
+            if constexpr (F4) {
+                if (part > 0) {
+                    const float* const sc = p.cache_scale[part - 1];
+                    if (sc && h < heads) {
+                        float scale = sc[h];
+                        lift_scale(scale, a, b);
+                        const float inv = 1.0f / scale;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            a[e] = quotient_to(kFar, a[e], scale, inv);
+                            b[e] = quotient_to(kFar, b[e], scale, inv);
+                        }
+                    }
+                    uint32_t ta = 0, tb = 0;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        ta = max(ta, __float_as_uint(a[e]) & 0x7fffffffu);
+                        tb = max(tb, __float_as_uint(b[e]) & 0x7fffffffu);
+                    }
+                    const uint32_t na = __shfl_xor_sync(0xffffffffu, ta, 1), nb = __shfl_xor_sync(0xffffffffu, tb, 1);
+                    const uint32_t ba = block_scale(max(ta, halves ? na : tb)), bb = halves ? block_scale(max(tb, nb)) : ba;
+                    if (live && h < heads) {
+                        const int key = at.slot % kRecordKeys;
+                        uint8_t* const rec = reinterpret_cast<uint8_t*>(y);
+                        uint8_t* const codes = rec + key * (p.D >> 1);
+                        *reinterpret_cast<uint32_t*>(codes + (oa >> 1)) = block_codes(a, e4m3_value(ba));
+                        *reinterpret_cast<uint32_t*>(codes + (ob >> 1)) = block_codes(b, e4m3_value(bb));
+                        // one lane stores a block's scale: of two neighbours the first that of a, the second that of b
+                        const bool second = halves && (i & 1);
+                        rec[8 * p.D + ((second ? ob : oa) & ~15) + key] = static_cast<uint8_t>(second ? bb : ba);
+                    }
+                    h += hpi;
+                    y += y_step;
+                    return;
+                }
+            }
             if (live && h < heads) {
                 if (part > 0 && p.cache_type == NVFP4_E4M3) {
                     const float* const sc = p.cache_scale[part - 1];
                     if (sc) {
                         float scale = sc[h];
-                        if (!(fabsf(scale) >= 0x1p-100f && fabsf(scale) <= 0x1p100f)) {  // 1 / scale might not be normal
-                            const float lift = fabsf(scale) < 1.0f ? 0x1p64f : 0x1p-64f;
-                            scale *= lift;
-#pragma unroll
-                            for (int e = 0; e < V; ++e) { a[e] *= lift; b[e] *= lift; }
-                        }
+                        lift_scale(scale, a, b);
                         const float inv = 1.0f / scale;
 #pragma unroll
                         for (int e = 0; e < V; ++e) { a[e] = quotient(a[e], scale, inv); b[e] = quotient(b[e], scale, inv); }
@@ -429,10 +492,12 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         bool ok = p.D % (2 * v) == 0 && p.D <= 32 * 2 * v && p.half % v == 0 && on(p.q_out, 2 * v) && on(p.q_norm, nb * v) &&
                   on(p.k_norm, nb * v);
         for (int i = 0; i < 3; ++i) ok = ok && on(p.x[i], eb * v) && p.ts[i] % v == 0 && p.hs[i] % v == 0;
-        for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;
+        for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;  // (E2M1: words of codes)
         return ok;
     };
-    const int v = host_variant() == 1 || p.cache_type == NVFP4_E2M1 ? 0 : fits(8) ? 8 : fits(4) ? 4 : 0;
+    // In 4 bits a block is two lanes' halves or one lane's: whole blocks turn, or pairs are neighbours.
+    const bool f4 = p.cache_type == NVFP4_E2M1;
+    const int v = host_variant() == 1 || (f4 && !p.interleaved && p.half % 16) ? 0 : fits(8) ? 8 : !f4 && fits(4) ? 4 : 0;
     if (v) {
         while ((2 * v << p.lanes_log2) < p.D) ++p.lanes_log2;
         // A token's heads are shared among warps, down to one step each, until the SMs' warps are filled twice
@@ -445,11 +510,14 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         const dim3 grid(static_cast<unsigned>(ctas));
         const size_t smem = static_cast<size_t>(warps) * p.half * sizeof(float2);
         const bool f32 = a->x_type == NVFP4_F32;
+        if (f4)
+            return f32 ? launch(rope_append_kernel<float, 8, true>, grid, dim3(kThreads), smem, st, p)
+                       : launch(rope_append_kernel<__nv_bfloat16, 8, true>, grid, dim3(kThreads), smem, st, p);
         if (v == 8)
-            return f32 ? launch(rope_append_kernel<float, 8>, grid, dim3(kThreads), smem, st, p)
-                       : launch(rope_append_kernel<__nv_bfloat16, 8>, grid, dim3(kThreads), smem, st, p);
-        return f32 ? launch(rope_append_kernel<float, 4>, grid, dim3(kThreads), smem, st, p)
-                   : launch(rope_append_kernel<__nv_bfloat16, 4>, grid, dim3(kThreads), smem, st, p);
+            return f32 ? launch(rope_append_kernel<float, 8, false>, grid, dim3(kThreads), smem, st, p)
+                       : launch(rope_append_kernel<__nv_bfloat16, 8, false>, grid, dim3(kThreads), smem, st, p);
+        return f32 ? launch(rope_append_kernel<float, 4, false>, grid, dim3(kThreads), smem, st, p)
+                   : launch(rope_append_kernel<__nv_bfloat16, 4, false>, grid, dim3(kThreads), smem, st, p);
     }
     const dim3 grid(p.T, p.hq + 2 * p.hk);
     return a->x_type == NVFP4_F32 ? launch(rope_append_scalar_kernel<float>, grid, dim3(128), p.D * 4, st, p)
