@@ -22,28 +22,101 @@ struct ReadParams {
     const int32_t* table;
     __nv_bfloat16* out[2];
     int64_t page_stride[2], table_stride;
-    int64_t pieces;          // of all tokens
+    int64_t pieces;          // of all tokens' keys
     int T, hk, D, seqs, per_seq, pages, max_pages, page, cache_type;
     int head_pieces;         // of a head
 };
 
-// One thread takes V neighbouring values of a row: 16 where rows are whole blocks on their boundaries, else one.
+// V neighbouring values of a row as they stand in the cache.
+template <int V>
+struct Piece {
+    uint4 w[V == 16 ? 2 : 1];  // bf16: 32 bytes; E4M3: 16; E2M1: 8 of codes
+    uint32_t block;            // E2M1: the scale's code
+    __device__ __forceinline__ void load(const ReadParams& p, int which, int64_t page, int head, int slot, int d) {
+        const char* const base = static_cast<const char*>(p.cache[which]);
+        if (p.cache_type == NVFP4_E2M1) {
+            const int64_t record = static_cast<int64_t>(head) * (p.page / kRecordKeys) + slot / kRecordKeys;
+            const char* const rec = base + page * p.page_stride[which] + record * record_bytes(p.D);
+            const int key = slot % kRecordKeys;
+            const char* const codes = rec + key * (p.D / 2) + d / 2;
+            if constexpr (V == 16) {
+                const uint2 c = *reinterpret_cast<const uint2*>(codes);
+                w[0].x = c.x; w[0].y = c.y;
+            } else {
+                w[0].x = static_cast<uint8_t>(*codes) >> 4 * (d & 1);
+            }
+            block = static_cast<uint8_t>(rec[8 * p.D + d / 16 * kRecordKeys + key]);
+            return;
+        }
+        const int64_t at = page * p.page_stride[which] + (static_cast<int64_t>(head) * p.page + slot) * p.D + d;
+        if (p.cache_type == NVFP4_E4M3) {
+            if constexpr (V == 16) w[0] = *reinterpret_cast<const uint4*>(base + at);
+            else w[0].x = static_cast<uint8_t>(base[at]);
+        } else {
+            if constexpr (V == 16) {
+                w[0] = *reinterpret_cast<const uint4*>(base + 2 * at);
+                w[1] = *reinterpret_cast<const uint4*>(base + 2 * at + 16);
+            } else {
+                w[0].x = *reinterpret_cast<const uint16_t*>(base + 2 * at);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const ReadParams& p, float scale, __nv_bfloat16* out) const {
+        if (p.cache_type == NVFP4_BF16) {  // as it stands
+            if constexpr (V == 16) {
+                *reinterpret_cast<uint4*>(out) = w[0];
+                *reinterpret_cast<uint4*>(out + 8) = w[1];
+            } else {
+                *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(w[0].x);
+            }
+            return;
+        }
+        const uint32_t words[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        const float b = p.cache_type == NVFP4_E2M1 ? e4m3_value(block) : 1.0f;
+        uint32_t halves[V == 16 ? 8 : 1];
+        if constexpr (V == 16) {
+            if (p.cache_type == NVFP4_E2M1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t h4[4];
+                    e2m1x8_f16x2(words[i], h4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) halves[4 * i + e] = h4[e];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) halves[i] = e4m3x2_f16x2(words[i / 2] >> 16 * (i & 1));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&halves[4 * i + e]));
+                    y[e] = pack_bf16(f.x * b * scale, f.y * b * scale);
+                }
+                *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        } else {
+            uint32_t h4[4];
+            e2m1x8_f16x2(words[0], h4);
+            const uint32_t code = p.cache_type == NVFP4_E2M1 ? h4[0] : e4m3x2_f16x2(words[0]);
+            *out = __float2bfloat16_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(code & 0xffffu))) * b * scale);
+        }
+    }
+};
+
+// One thread takes V neighbouring values of a key and the same of its value: 16 where rows are whole blocks on their
+// boundaries, else one.
 template <int V>
 __global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__ ReadParams p) {
     pdl_launch_dependents();
     pdl_wait();
     const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
     if (at >= p.pieces) return;
-    const int per_token = 2 * p.hk * p.head_pieces;
-    const int t = static_cast<int>(at / per_token);
-    int i = static_cast<int>(at - static_cast<int64_t>(t) * per_token);
-    const int which = i >= p.hk * p.head_pieces;
-    i -= which * p.hk * p.head_pieces;
-    const int h = i / p.head_pieces, d = (i - h * p.head_pieces) * V;
-    __nv_bfloat16* const out = p.out[which] + (static_cast<int64_t>(t) * p.hk + h) * p.D + d;
-    float v[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = 0.0f;
+    const int per_token = p.hk * p.head_pieces;
+    const int t = p.pieces <= INT32_MAX ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per_token)) : static_cast<int>(at / per_token);
+    const int i = static_cast<int>(at - static_cast<int64_t>(t) * per_token), h = i / p.head_pieces, d = (i - h * p.head_pieces) * V;
     const int n = p.positions[t];
     int64_t page = -1;
     if (n >= 0) {
@@ -54,66 +127,25 @@ __global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__
             atomicOr(&g_read_status, NVFP4_DEV_BAD_PAGE);
         }
     }
-    if (page >= 0) {
-        const int slot = n % p.page;
-        const float scale = p.cache_scale[which] ? p.cache_scale[which][h] : 1.0f;
-        if (p.cache_type == NVFP4_E2M1) {
-            const int64_t record = static_cast<int64_t>(h) * (p.page / kRecordKeys) + slot / kRecordKeys;
-            const uint8_t* const rec = static_cast<const uint8_t*>(p.cache[which]) + page * p.page_stride[which] + record * record_bytes(p.D);
-            const int key = slot % kRecordKeys;
-            const uint8_t* const codes = rec + key * (p.D / 2) + d / 2;
-            const float block = e4m3_value(rec[8 * p.D + d / 16 * kRecordKeys + key]);
-            uint32_t h2[4];
-            if constexpr (V == 16) {
-                const uint2 w = *reinterpret_cast<const uint2*>(codes);
+    const int64_t to = (static_cast<int64_t>(t) * p.hk + h) * p.D + d;
+    if (page < 0) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    e2m1x8_f16x2(half ? w.y : w.x, h2);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[e]));
-                        v[8 * half + 2 * e] = f.x * block * scale;
-                        v[8 * half + 2 * e + 1] = f.y * block * scale;
-                    }
-                }
-            } else {
-                e2m1x8_f16x2(*codes, h2);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[0]));
-                v[0] = (d & 1 ? f.y : f.x) * block * scale;
-            }
-        } else {
-            const int64_t from = page * p.page_stride[which] + (static_cast<int64_t>(h) * p.page + slot) * p.D + d;
-            if (p.cache_type == NVFP4_E4M3) {
-                const uint8_t* const codes = static_cast<const uint8_t*>(p.cache[which]) + from;
-                if constexpr (V == 16) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = e4m3_value((e < 4 ? w.x : e < 8 ? w.y : e < 12 ? w.z : w.w) >> 8 * (e & 3)) * scale;
-                } else {
-                    v[0] = e4m3_value(*codes) * scale;
-                }
-            } else {  // as it stands
-                const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(p.cache[which]) + from;
-                if constexpr (V == 16) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(x), b = *reinterpret_cast<const uint4*>(x + 8);
-                    *reinterpret_cast<uint4*>(out) = a;
-                    *reinterpret_cast<uint4*>(out + 8) = b;
-                } else {
-                    *out = *x;
-                }
-                return;
-            }
+        for (int which = 0; which < 2; ++which) {
+            __nv_bfloat16* const out = p.out[which] + to;
+            if constexpr (V == 16) reinterpret_cast<uint4*>(out)[0] = reinterpret_cast<uint4*>(out)[1] = make_uint4(0, 0, 0, 0);
+            else *out = __float2bfloat16_rn(0.0f);
         }
+        return;
     }
-    if constexpr (V == 16) {
-        float lo[8], hi[8];
+    Piece<V> piece[2];
+    float scale[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) { lo[e] = v[e]; hi[e] = v[8 + e]; }
-        store_vec(out, lo);
-        store_vec(out + 8, hi);
-    } else {
-        *out = __float2bfloat16_rn(v[0]);
+    for (int which = 0; which < 2; ++which) {
+        piece[which].load(p, which, page, h, n % p.page, d);
+        scale[which] = p.cache_scale[which] ? p.cache_scale[which][h] : 1.0f;
     }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) piece[which].store(p, scale[which], p.out[which] + to);
 }
 
 cudaError_t read_status(int* bits) {
@@ -158,7 +190,7 @@ extern "C" nvfp4_status nvfp4_cache_read(const nvfp4_cache_read_args* a, void* s
     for (int i = 0; i < 2; ++i)
         wide = wide && aligned(p.cache[i], piece) && p.page_stride[i] % elements == 0 && aligned(p.out[i], 16);
     p.head_pieces = wide ? p.D / 16 : p.D;
-    p.pieces = 2ll * p.T * p.hk * p.head_pieces;
+    p.pieces = static_cast<int64_t>(p.T) * p.hk * p.head_pieces;
     const int64_t ctas = (p.pieces + 127) / 128;
     if (ctas > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(ctas));
