@@ -172,7 +172,7 @@ struct TileShape {
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
     static constexpr int kBox = 16 * kBoxBytes;
     static constexpr int kPart = kF4 ? kHalves * 9 * DP : kHalves * kBoxes * kBox;  // K (or V) bytes of a tile
-    static constexpr int kStages = kF4 ? (NT == 4 ? 4 : DP == 128 && NT == 1 ? 1 : 2)
+    static constexpr int kStages = kF4 ? (NT == 4 ? 4 : DP == 128 ? 1 : 2)
                                  : DP * kES == 512 ? 1 : NT * DP == 256 ? 3 : NT * DP <= 128 ? 1 : 2;
     static constexpr int kRing = kWarps * kStages * 2 * kPart;
     static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
@@ -1045,39 +1045,29 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     const int block = (W ? t + 4 * c : min(t + 4 * c, last_block));
                     const uint32_t from = ring + 2 * cur * T::kPart + k_row * (dim >> 1) + 8 * block;
                     const uint32_t from_scale = ring + 2 * cur * T::kPart + 8 * dim + 16 * block + (k_row & ~3);
-                    uint2 x[H], y[H];
-                    uint32_t sx[H], sy[H];
+                    uint2 q[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) q[nt][e] = query(nt, 4 * c + e);
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        x[i] = lds8(from + i * rec);
-                        y[i] = lds8(from + i * rec + dim);
+                        const uint2 x = lds8(from + i * rec), y = lds8(from + i * rec + dim);
                         const uint32_t s4 = __byte_perm(lds4(from_scale + i * rec), 0, k_row & 1 ? 0x3311 : 0x2200);
-                        sx[i] = e4m3x2_f16x2(s4);
-                        sy[i] = e4m3x2_f16x2(s4 >> 16);
-                    }
+                        const uint32_t sx = e4m3x2_f16x2(s4), sy = e4m3x2_f16x2(s4 >> 16);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t a[H][2][4];
-#pragma unroll
-                        for (int i = 0; i < H; ++i) {
+                        for (int half = 0; half < 2; ++half) {
                             uint32_t xs[4], ys[4];
-                            e2m1x8_f16x2(half ? x[i].y : x[i].x, xs);
-                            e2m1x8_f16x2(half ? y[i].y : y[i].x, ys);
+                            e2m1x8_f16x2(half ? x.y : x.x, xs);
+                            e2m1x8_f16x2(half ? y.y : y.x, ys);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                a[i][e][0] = mul_f16x2(xs[2 * e], sx[i]); a[i][e][2] = mul_f16x2(xs[2 * e + 1], sx[i]);
-                                a[i][e][1] = mul_f16x2(ys[2 * e], sy[i]); a[i][e][3] = mul_f16x2(ys[2 * e + 1], sy[i]);
-                            }
+                            for (int e = 0; e < 4; ++e) { xs[e] = mul_f16x2(xs[e], sx); ys[e] = mul_f16x2(ys[e], sy); }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma<true>(s[i][nt], xs[2 * e], ys[2 * e], xs[2 * e + 1], ys[2 * e + 1], q[nt][2 * half + e].x, q[nt][2 * half + e].y);
                         }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 q = query(nt, 4 * c + 2 * half + e);
-#pragma unroll
-                                for (int i = 0; i < H; ++i)
-                                    mma<true>(s[i][nt], a[i][e][0], a[i][e][1], a[i][e][2], a[i][e][3], q.x, q.y);
-                            }
                     }
                 }
             } else
@@ -1321,17 +1311,40 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     a[2] = __byte_perm(vr[2][mt], vr[3][mt], 0x5410); a[3] = __byte_perm(vr[2][mt], vr[3][mt], 0x7632);
                 }
             };
+            // 4 bits: a block scale of NaN does the same to its 16 elements. It is taken as zero, and the rows that see its
+            // key become NaN there by themselves. (Their values taken row by row cost the loop 80 registers.)
+            auto silence = [&](int i) {
+#pragma unroll
+                for (int c = 0; c < (DP == 256 ? 2 : 1); ++c) {
+                    const uint32_t nan = (((vs[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in such bytes
+                    if (!__any_sync(0xffffffffu, nan != 0)) continue;
+                    vs[c] &= ~(nan * 0xffu);
+                    uint32_t keys = 0;  // of the block, a bit each; the lanes with the same elements have four each
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) keys |= (nan >> 8 * k & 1u) << (4 * t + (k ^ swap));
+                    keys |= __shfl_xor_sync(0xffffffffu, keys, 1);
+                    keys |= __shfl_xor_sync(0xffffffffu, keys, 2);
+                    const int first = base + tile * T::kKeys + 16 * i;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = row0 + 8 * nt + 2 * t + e;
+                            const int hi = sp.hi_all + row / p.group, lo = p.window > 0 ? hi - p.window : 0;
+                            const uint32_t seen = ((1u << min(max(hi - first, 0), 16)) - 1u) & ~((1u << min(max(lo - first, 0), 16)) - 1u);
+                            if (keys & seen) {
+#pragma unroll
+                                for (int mt = 8 * c; mt < T::kMT && mt < 8 * c + 8; ++mt) o[nt][mt][e] = o[nt][mt][2 + e] = NAN;
+                            }
+                        }
+                }
+            };
             bool special = false;
-            if (edge && (p.rows > 1 || p.window > 0)) {
+            if (!F4 && edge && (p.rows > 1 || p.window > 0)) {
 #pragma unroll 1
                 for (int i = 0; i < H; ++i) {
                     load_v(i);
                     keep_v(i, sp.lo, sp.n);
-                    if constexpr (F4) {
-#pragma unroll
-                        for (int c = 0; c < (DP == 256 ? 2 : 1); ++c)
-                            special |= (((vs[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-                    } else
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -1343,11 +1356,14 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                 }
                 special = __any_sync(0xffffffffu, special);
             }
-            if (!special) {
+            if (F4 || !special) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     load_v(i);
                     if (edge) keep_v(i, sp.lo, sp.n);  // what a page holds beyond the sequence may be anything
+                    if constexpr (F4) {
+                        if (edge && (p.rows > 1 || p.window > 0)) silence(i);
+                    }
 #pragma unroll
                     for (int mt = 0; mt < T::kMT; ++mt) {
                         uint32_t a[4];
