@@ -263,6 +263,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// The f16 product alone, without a sum to add to.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -300,6 +306,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // tanh without a branch: its power series up to x^9 below 0.3 (the next term is 2^-24 of it), 1 - 2 / (exp(2 |x|) + 1) beyond,
@@ -826,7 +838,11 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
     int id[H], next_id[H];          // page ids of the requested tile, and of the one after it
     int at[H], next_at[H];          // the block's first key in its page
     uint32_t bad = 0, bads = 0;     // blocks whose page id is out of range: requested tile; tiles in the ring
-    const bool mine = lane < (p.tall_box ? 1 : H);  // 4 bits: a lane looks up and copies one block, or the whole tile
+    // 4 bits: a lane looks up and copies one block, or the whole tile
+    const bool mine = lane < (p.tall_box ? 1 : H);
+    const char* head[2];            // the kv head's records in page 0, of keys and of values
+    const char* source[2];          // the requested tile's
+    const uint64_t pol4 = F4 ? evict_first() : 0;
 
     // looks up the tile after the requested one
     auto look_up = [&](int tl) {
@@ -854,16 +870,18 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
     };
     auto take = [&]() {
         if constexpr (F4) {
-            id[0] = next_id[0];
-            at[0] = next_at[0];
-            const bool out = mine && static_cast<unsigned>(id[0]) >= static_cast<unsigned>(p.pages);
+            const bool out = mine && static_cast<unsigned>(next_id[0]) >= static_cast<unsigned>(p.pages);
             bad = __ballot_sync(0xffffffffu, out);
-            if (bad == 0) return;
-            if (out) {
-                atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
-                id[0] = 0;
+            if (bad) {
+                if (out) {
+                    atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                    next_id[0] = 0;
+                }
+                if (p.tall_box) bad = (1u << H) - 1;
             }
-            if (p.tall_box) bad = (1u << H) - 1;
+            const uint32_t in_page = static_cast<uint32_t>(next_at[0]) * rec;  // below 2^20 records of 2304 bytes
+            source[0] = head[0] + next_id[0] * p.page_stride[0] + in_page;
+            source[1] = head[1] + next_id[0] * p.page_stride[1] + in_page;
             return;
         }
         bad = 0;
@@ -886,11 +904,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         if constexpr (F4) {
             if (lane == 0) barrier_expect(bar, H * rec);
             __syncwarp();
-            if (mine) {
-                const int64_t block = static_cast<int64_t>(h) * p.page_tiles + at[0];
-                copy_bytes(to + lane * rec, static_cast<const char*>(p.cache[which]) + id[0] * p.page_stride[which] + block * rec,
-                           p.tall_box ? H * rec : rec, bar, evict_first());
-            }
+            if (mine) copy_bytes(to + lane * rec, source[which], p.tall_box ? H * rec : rec, bar, pol4);
             return;
         }
         else if (lane == 0) {
@@ -916,6 +930,11 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         next_page = block / p.page_tiles;
         next_slot = block % p.page_tiles;
         bads = 0;
+        if constexpr (F4) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
+                head[which] = static_cast<const char*>(p.cache[which]) + static_cast<int64_t>(h) * p.page_tiles * rec;
+        }
         look_up(tile);
     };
     auto fill_ring = [&]() {
@@ -1064,7 +1083,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][nt][e] = s2[i][nt][e] = 0.0f;
+                    for (int e = 0; e < 4 && !F4; ++e) s[i][nt][e] = s2[i][nt][e] = 0.0f;
             if constexpr (F4) {
                 // lane t has blocks t, t + 4, ... of its two keys' elements: codes to f16, times the block's scale (exact)
 #pragma unroll
@@ -1093,7 +1112,8 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma<true>(s[i][nt], xs[2 * e], ys[2 * e], xs[2 * e + 1], ys[2 * e + 1], q[nt][2 * half + e].x, q[nt][2 * half + e].y);
+                                    if (c == 0 && half == 0 && e == 0) mma_first(s[i][nt], xs[0], ys[0], xs[1], ys[1], q[nt][0].x, q[nt][0].y);
+                                    else mma<true>(s[i][nt], xs[2 * e], ys[2 * e], xs[2 * e + 1], ys[2 * e + 1], q[nt][2 * half + e].x, q[nt][2 * half + e].y);
                         }
                     }
                 }
@@ -1207,7 +1227,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                 for (int c = 0; c < 2; ++c) {
                     float z = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < H; ++i) z = fmaxf(z, fmaxf(s[i][nt][c], s[i][nt][2 + c]));
+                    for (int i = 0; i < H; ++i) z = F4 ? max3(z, s[i][nt][c], s[i][nt][2 + c]) : fmaxf(z, fmaxf(s[i][nt][c], s[i][nt][2 + c]));
                     top[nt][c] = S ? z : z * zf[nt][c];
                     passed |= top[nt][c] > mx[nt][c] + kSlack;
                 }
