@@ -1252,6 +1252,63 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     }
                 }
             }
+            // 4 bits: what stays of the scales of the lane's four keys, of one or two blocks of elements; all settled here,
+            // so that from the weights to the last product no branch stands between instructions that can fill each
+            // other's waits. What a page holds beyond the sequence may be anything. A block scale of NaN must not reach a
+            // row that does not see its key, and a weight of zero would not keep it away: it is taken as zero, and the
+            // rows that see it become NaN there by themselves. (Such values taken row by row, as below, cost the loop 80
+            // registers.)
+            constexpr int kVS = DP == 256 ? 2 : 1;
+            uint32_t kept[F4 ? H : 1][kVS];
+            auto value_scales = [&](int i, int c) {
+                const int mine = (DP == 64 ? g >> 1 : g) + 8 * c;
+                return __byte_perm(lds4(ring + (2 * cur + 1) * T::kPart + i * rec + 8 * dim + 16 * (W ? mine : min(mine, last_block)) + 4 * t), 0,
+                                   swap ? 0x2301 : 0x3210);
+            };
+            if constexpr (F4) {
+                if (!arrived(1)) { dead = true; k_taken = 1; break; }
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int c = 0; c < kVS; ++c) kept[i][c] = 0xffffffffu;
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const int first = base + tile * T::kKeys + 16 * i;
+                        uint32_t in = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = first + 4 * t + (k ^ swap);
+                            if (key >= sp.lo && key < sp.n && !(bad_now >> i & 1u)) in |= 0xffu << 8 * k;
+                        }
+#pragma unroll
+                        for (int c = 0; c < kVS; ++c) {
+                            kept[i][c] = in;
+                            if (p.rows == 1 && p.window == 0) continue;
+                            const uint32_t nan = ((((value_scales(i, c) & in) & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in such bytes
+                            if (!__any_sync(0xffffffffu, nan != 0)) continue;
+                            kept[i][c] &= ~(nan * 0xffu);
+                            uint32_t keys = 0;  // of the block, a bit each; the lanes with the same elements have four each
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) keys |= (nan >> 8 * k & 1u) << (4 * t + (k ^ swap));
+                            keys |= __shfl_xor_sync(0xffffffffu, keys, 1);
+                            keys |= __shfl_xor_sync(0xffffffffu, keys, 2);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int row = row0 + 8 * nt + 2 * t + e;
+                                    const int hi = sp.hi_all + row / p.group, lo = p.window > 0 ? hi - p.window : 0;
+                                    const uint32_t seen = ((1u << min(max(hi - first, 0), 16)) - 1u) & ~((1u << min(max(lo - first, 0), 16)) - 1u);
+                                    if (keys & seen) {
+#pragma unroll
+                                        for (int mt = 8 * c; mt < T::kMT && mt < 8 * c + 8; ++mt) o[nt][mt][e] = o[nt][mt][2 + e] = NAN;
+                                    }
+                                }
+                        }
+                    }
+                }
+            }
             uint32_t pb[H][NT][2], pl[H][NT][2];  // weights; bf16: their first and last 8 bits
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -1279,9 +1336,9 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             }
             // --- O^T += V^T P^T. A weight of zero must also silence what is not finite: in tiles that
             // some row sees only in part, such values are taken row by row of the sequence below.
-            if (!arrived(1)) { dead = true; k_taken = 1; break; }
+            if (!F4 && !arrived(1)) { dead = true; k_taken = 1; break; }
             uint32_t vr[4][T::kVW];
-            uint32_t vs[DP == 256 ? 2 : 1];  // 4 bits: the scales of the lane's four keys, of one or two blocks
+            uint32_t vs[kVS];
             auto load_v = [&](int i) {
                 if constexpr (F4) {
                     const uint32_t from = ring + (2 * cur + 1) * T::kPart + i * rec;
@@ -1299,9 +1356,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < (DP == 256 ? 2 : 1); ++c)
-                        vs[c] = __byte_perm(lds4(from + 8 * dim + 16 * (W ? (DP == 64 ? g >> 1 : g) + 8 * c : min((DP == 64 ? g >> 1 : g) + 8 * c, last_block)) + 4 * t), 0,
-                                            swap ? 0x2301 : 0x3210);
+                    for (int c = 0; c < kVS; ++c) vs[c] = value_scales(i, c) & kept[i][c];
                     return;
                 }
 #pragma unroll
@@ -1323,15 +1378,10 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             auto keep_v = [&](int i, int lo, int hi) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int key = base + tile * T::kKeys + 16 * i + (F4 ? 4 * t + (k ^ swap) : 2 * t + (k & 1) + 8 * (k >> 1));
+                    const int key = base + tile * T::kKeys + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1);
                     if (key < lo || key >= hi || (bad_now >> i & 1u)) {
-                        if constexpr (F4) {  // codes are finite
 #pragma unroll
-                            for (int c = 0; c < (DP == 256 ? 2 : 1); ++c) vs[c] &= ~(0xffu << 8 * k);
-                        } else {
-#pragma unroll
-                            for (int w = 0; w < T::kVW; ++w) vr[k][w] = 0;
-                        }
+                        for (int w = 0; w < T::kVW; ++w) vr[k][w] = 0;
                     }
                 }
             };
@@ -1367,34 +1417,6 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                     a[2] = __byte_perm(vr[2][mt], vr[3][mt], 0x5410); a[3] = __byte_perm(vr[2][mt], vr[3][mt], 0x7632);
                 }
             };
-            // 4 bits: a block scale of NaN does the same to its 16 elements. It is taken as zero, and the rows that see its
-            // key become NaN there by themselves. (Their values taken row by row cost the loop 80 registers.)
-            auto silence = [&](int i) {
-#pragma unroll
-                for (int c = 0; c < (DP == 256 ? 2 : 1); ++c) {
-                    const uint32_t nan = (((vs[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in such bytes
-                    if (!__any_sync(0xffffffffu, nan != 0)) continue;
-                    vs[c] &= ~(nan * 0xffu);
-                    uint32_t keys = 0;  // of the block, a bit each; the lanes with the same elements have four each
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) keys |= (nan >> 8 * k & 1u) << (4 * t + (k ^ swap));
-                    keys |= __shfl_xor_sync(0xffffffffu, keys, 1);
-                    keys |= __shfl_xor_sync(0xffffffffu, keys, 2);
-                    const int first = base + tile * T::kKeys + 16 * i;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int row = row0 + 8 * nt + 2 * t + e;
-                            const int hi = sp.hi_all + row / p.group, lo = p.window > 0 ? hi - p.window : 0;
-                            const uint32_t seen = ((1u << min(max(hi - first, 0), 16)) - 1u) & ~((1u << min(max(lo - first, 0), 16)) - 1u);
-                            if (keys & seen) {
-#pragma unroll
-                                for (int mt = 8 * c; mt < T::kMT && mt < 8 * c + 8; ++mt) o[nt][mt][e] = o[nt][mt][2 + e] = NAN;
-                            }
-                        }
-                }
-            };
             bool special = false;
             if (!F4 && edge && (p.rows > 1 || p.window > 0)) {
 #pragma unroll 1
@@ -1416,10 +1438,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     load_v(i);
-                    if (edge) keep_v(i, sp.lo, sp.n);  // what a page holds beyond the sequence may be anything
-                    if constexpr (F4) {
-                        if (edge && (p.rows > 1 || p.window > 0)) silence(i);
-                    }
+                    if (!F4 && edge) keep_v(i, sp.lo, sp.n);  // what a page holds beyond the sequence may be anything
 #pragma unroll
                     for (int mt = 0; mt < T::kMT; ++mt) {
                         uint32_t a[4];
