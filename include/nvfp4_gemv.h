@@ -269,7 +269,8 @@ int nvfp4_sdict_encode(const uint8_t* scales, int N, int K, uint8_t* plane_out, 
  * entries past a sequence's length are not read. Values are bf16, or E4M3 codes that stand for
  * code * scale[kv_head] (k_scale, v_scale [kv_heads] f32; NULL = 1, as a bf16 cache wants it).
  *
- * Or they are held in 4 bits (NVFP4_E2M1): head_dim and page_size are multiples of 16, and every 16 keys of
+ * Or they are held in 4 bits (NVFP4_E2M1): head_dim and page_size are multiples of 16 (else
+ * NVFP4_ERR_SHAPE), and every 16 keys of
  * a kv head are a record of 9 * head_dim bytes, first their E2M1 codes [16][head_dim / 2] (element 2j in the
  * low nibble of byte j), then the E4M3 scales of 16 elements each, [head_dim / 16][16]: key i's scale of
  * elements 16c .. 16c + 15 is byte 8 * head_dim + 16 c + i. A page holds [kv_heads][page_size / 16] records;
@@ -322,7 +323,8 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  * types' largest to the largest; b = 0 gives zeros, a NaN makes b NaN. Long-context scalings of the
  * frequencies are the caller's, in inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
  * row is zero. Positions are below 2^24 (beyond it, a call without keys rounds them to fp32). A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
- * nothing. Two tokens of one call at the same sequence and position leave either's values.
+ * nothing. Two tokens of one call at the same sequence and position leave either's values, in 4 bits perhaps
+ * the codes of one under a scale of the other.
  * q, k, v: [tokens, heads, head_dim] with unit stride inside a head and the given strides between
  * tokens and heads. head_dim <= 1024, 2 * rotary_half <= head_dim, max_pages * page_size <= 2^24.
  */

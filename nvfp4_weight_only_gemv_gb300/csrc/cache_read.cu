@@ -3,7 +3,9 @@
 // For token t at position n = positions[t]: out[t, h] = bf16(code * block scale * scale[h]) (E2M1),
 // bf16(code * scale[h]) (E4M3) or the value (bf16) of row n % page of page table[seq][n / page].
 //
-// Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens.
+// Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens. (4 bits,
+// 8192 tokens of 8 + 8 heads of 128 values: 12.2 us for 7.7 us of bytes, position, page and row being three trips one
+// after the other; one token 2.4 us.)
 
 #include "ops_common.cuh"
 

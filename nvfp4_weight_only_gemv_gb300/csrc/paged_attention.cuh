@@ -15,6 +15,7 @@
 
 #include <cuda.h>
 
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -156,7 +157,7 @@ template <int DP, int NT, int C>
 struct TileShape {
     static constexpr bool kF16 = C != NVFP4_BF16;          // products in f16
     static constexpr bool kF4 = C == NVFP4_E2M1;
-    static constexpr int kHalves = kF4 ? (DP >= 256 || NT == 4 ? 2 : 4)  // 16-key blocks
+    static constexpr int kHalves = kF4 ? (NT == 4 ? 2 : 4)  // 16-key blocks
                                  : kF16 ? (DP >= 256 ? 1 : 256 / DP) : (DP >= 128 ? 1 : 128 / DP);
     static constexpr int kKeys = 16 * kHalves;
     static constexpr int kES = kF16 ? 1 : 2;               // bytes per value (kF4: half of that, and the scales)
@@ -172,7 +173,7 @@ struct TileShape {
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
     static constexpr int kBox = 16 * kBoxBytes;
     static constexpr int kPart = kF4 ? kHalves * 9 * DP : kHalves * kBoxes * kBox;  // K (or V) bytes of a tile
-    static constexpr int kStages = kF4 ? (NT == 4 ? 4 : DP == 128 ? 1 : 2)
+    static constexpr int kStages = kF4 ? (NT == 4 ? 3 : 1)
                                  : DP * kES == 512 ? 1 : NT * DP == 256 ? 3 : NT * DP <= 128 ? 1 : 2;
     static constexpr int kRing = kWarps * kStages * 2 * kPart;
     static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
@@ -1186,7 +1187,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                             for (int e = 0; e < 4; ++e) s[i][nt][e] = f(s[i][nt][e], zf[nt][e & 1]);
                 };
                 if (p.cap == 0.0f) each([&](float z, float f) { return z * f; });
-                else if (p.cap <= kCloseCap) each([&](float z, float f) { return capped(z * (f * cap_in), cap_out); });
+                else if (p.cap <= kCloseCap) each([&](float z, float f) { return capped(z * fminf(f * cap_in, FLT_MAX), cap_out); });
                 else each([&](float z, float f) { return cap_out * tanh_fast(z * f * cap_in); });
                 if (p.slopes) {
 #pragma unroll

@@ -115,6 +115,17 @@ def test_infinite_scores_reach_the_cap():
     assert not got.float().any() and bool((lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("scale,cap", [(1e30, 2.0 ** -40), (1e30, 50.0), (1e-30, 2.0 ** 40)])
+def test_extreme_scales_and_caps(cache, scale, cap):
+    # scores far beyond the cap are +-cap, those of zero stay zero: every other key is zero
+    q, kc, vc, table, ln, ks, vs = _inputs([32], 1, 2, 1, 64, cache, 16, 9)
+    kc.view(torch.uint8).zero_()
+    lse = torch.empty((1, 2), device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, ln, scale, softcap=cap, k_scale=ks, v_scale=vs, lse=lse)
+    assert torch.allclose(lse, torch.full_like(lse, math.log(32)), atol=1e-5) and torch.isfinite(got.float()).all()
+
+
 def test_refusals():
     q, kc, vc, table, ln, _, _ = _inputs([5, 6], 2, 4, 2, 64, BF16, 16, 8)
     one = torch.ones(4, device=DEV)

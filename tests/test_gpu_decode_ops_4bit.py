@@ -518,6 +518,35 @@ def test_offsets_past_32_bits():
     assert torch.equal(nv.cache_read(pos, kc, vc, table)[0][0].double(), _values(kc[4999:])[0, :, 3])
 
 
+@pytest.mark.parametrize("offset,stride", [(0, 0), (1, 0), (0, 1), (8, 8), (16, 16)])
+def test_caches_on_any_boundary_and_with_strides_of_their_own(offset, stride):
+    # keys and values in separate pools, whose pages begin on other boundaries and lie apart by other strides
+    g = _gen(offset + 40 * stride)
+    page, D, hk, pages = 32, 128, 2, 6
+    row = 9 * D // 16
+    size = hk * page * row
+
+    def pool(extra):
+        mem = torch.zeros(pages * (size + extra) + 64, dtype=FP4, device=DEV)
+        return mem.as_strided((pages, hk, page, row), (size + extra, page * row, row, 1), offset)
+
+    kc, vc = pool(stride), pool(2 * stride)
+    T, table = 70, torch.tensor([[4, 1, 5]], dtype=torch.int32, device=DEV)
+    k, v = (_randn((T, hk, D), g, BF16) for _ in "kv")
+    at = torch.arange(T, dtype=torch.int32, device=DEV)
+    nv.rope_append(None, k, v, at, torch.empty(0, device=DEV), kc, vc, table)
+    even = nv.kv_cache(pages, hk, page, D, FP4)
+    nv.rope_append(None, k, v, at, torch.empty(0, device=DEV), *even, table)
+    assert torch.equal(kc, even[0]) and torch.equal(vc, even[1])
+    for a, b in zip(nv.cache_read(at, kc, vc, table), nv.cache_read(at, *even, table)):
+        assert torch.equal(a, b)
+    q, ln = _randn((2, 8, D), g, BF16), torch.tensor([T], dtype=torch.int32, device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, ln)
+    ref, tol, _, _ = _ref(q, _values(even[0]), _values(even[1]), table, [T], 2, D ** -0.5, 0, None, None, P_ERR[FP4])
+    _within(got, ref, tol)
+    assert nv.device_status() == 0
+
+
 # ------------------------------------------------------------------------------- used together
 
 def test_append_read_and_attend_together_in_a_graph():
