@@ -4,7 +4,7 @@
 // bf16(code * scale[h]) (E4M3) or the value (bf16) of row n % page of page table[seq][n / page].
 //
 // Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens. (4 bits,
-// 8192 tokens of 8 + 8 heads of 128 values: 12.2 us for 7.7 us of bytes, position, page and row being three trips one
+// 8192 tokens of 8 + 8 heads of 128 values: 10.0 us for 6.3 us of bytes, position, page and row being three trips one
 // after the other; one token 2.4 us.)
 
 #include "ops_common.cuh"
@@ -27,127 +27,141 @@ struct ReadParams {
     int64_t pieces;          // of all tokens' keys
     int T, hk, D, seqs, per_seq, pages, max_pages, page, cache_type;
     int head_pieces;         // of a head
+    int sectors;             // the outputs begin on 32-byte boundaries
 };
 
-// V neighbouring values of a row as they stand in the cache.
-template <int V>
+// 32 bytes, a whole sector at once where they lie on its boundary: in two halves a warp's stores touch every sector twice.
+__device__ __forceinline__ void store32(__nv_bfloat16* out, bool sector, uint4 a, uint4 b) {
+    if (sector) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(out), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+    } else {
+        reinterpret_cast<uint4*>(out)[0] = a;
+        reinterpret_cast<uint4*>(out)[1] = b;
+    }
+}
+
+// Sixteen neighbouring values of a row as they stand in a cache of type C, or one in any.
+template <int C>
 struct Piece {
-    uint4 w[V == 16 ? 2 : 1];  // bf16: 32 bytes; E4M3: 16; E2M1: 8 of codes
-    uint32_t block;            // E2M1: the scale's code
+    uint4 w[C == NVFP4_BF16 ? 2 : 1];  // bf16: 32 bytes; E4M3: 16; E2M1: 8 of codes
+    uint32_t block;                    // E2M1: the scale's code
     __device__ __forceinline__ void load(const ReadParams& p, int which, int64_t page, int head, int slot, int d) {
-        const char* const base = static_cast<const char*>(p.cache[which]);
-        if (p.cache_type == NVFP4_E2M1) {
-            const int64_t record = static_cast<int64_t>(head) * (p.page / kRecordKeys) + slot / kRecordKeys;
-            const char* const rec = base + page * p.page_stride[which] + record * record_bytes(p.D);
+        const char* const base = static_cast<const char*>(p.cache[which]) + page * p.page_stride[which] * (C == NVFP4_BF16 ? 2 : 1);
+        if constexpr (C == NVFP4_E2M1) {
             const int key = slot % kRecordKeys;
-            const char* const codes = rec + key * (p.D / 2) + d / 2;
-            if constexpr (V == 16) {
-                const uint2 c = *reinterpret_cast<const uint2*>(codes);
-                w[0].x = c.x; w[0].y = c.y;
-            } else {
-                w[0].x = static_cast<uint8_t>(*codes) >> 4 * (d & 1);
-            }
-            block = static_cast<uint8_t>(rec[8 * p.D + d / 16 * kRecordKeys + key]);
-            return;
-        }
-        const int64_t at = page * p.page_stride[which] + (static_cast<int64_t>(head) * p.page + slot) * p.D + d;
-        if (p.cache_type == NVFP4_E4M3) {
-            if constexpr (V == 16) w[0] = *reinterpret_cast<const uint4*>(base + at);
-            else w[0].x = static_cast<uint8_t>(base[at]);
+            const char* const rec = base + (static_cast<int64_t>(head) * (p.page / kRecordKeys) + slot / kRecordKeys) * record_bytes(p.D);
+            const uint2 c = *reinterpret_cast<const uint2*>(rec + key * (p.D / 2) + d / 2);
+            w[0].x = c.x; w[0].y = c.y;
+            block = static_cast<uint8_t>(rec[8 * p.D + d + key]);
         } else {
-            if constexpr (V == 16) {
-                w[0] = *reinterpret_cast<const uint4*>(base + 2 * at);
-                w[1] = *reinterpret_cast<const uint4*>(base + 2 * at + 16);
-            } else {
-                w[0].x = *reinterpret_cast<const uint16_t*>(base + 2 * at);
-            }
+            const char* const at = base + ((static_cast<int64_t>(head) * p.page + slot) * p.D + d) * (C == NVFP4_BF16 ? 2 : 1);
+            w[0] = *reinterpret_cast<const uint4*>(at);
+            if constexpr (C == NVFP4_BF16) w[1] = *reinterpret_cast<const uint4*>(at + 16);
         }
     }
-    __device__ __forceinline__ void store(const ReadParams& p, float scale, __nv_bfloat16* out) const {
-        if (p.cache_type == NVFP4_BF16) {  // as it stands
-            if constexpr (V == 16) {
-                *reinterpret_cast<uint4*>(out) = w[0];
-                *reinterpret_cast<uint4*>(out + 8) = w[1];
-            } else {
-                *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(w[0].x);
-            }
-            return;
-        }
-        const uint32_t words[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-        const float b = p.cache_type == NVFP4_E2M1 ? e4m3_value(block) : 1.0f;
-        uint32_t halves[V == 16 ? 8 : 1];
-        if constexpr (V == 16) {
-            if (p.cache_type == NVFP4_E2M1) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t h4[4];
-                    e2m1x8_f16x2(words[i], h4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) halves[4 * i + e] = h4[e];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) halves[i] = e4m3x2_f16x2(words[i / 2] >> 16 * (i & 1));
-            }
+    __device__ __forceinline__ void store(float scale, __nv_bfloat16* out, bool sector) const {
+        if constexpr (C == NVFP4_BF16) {  // as it stands
+            store32(out, sector, w[0], w[1]);
+        } else {
+            uint4 out2[2];
+            const uint32_t words[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+            const float b = C == NVFP4_E2M1 ? e4m3_value(block) : 1.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                uint32_t y[4];
+                uint32_t halves[4], y[4];
+                if constexpr (C == NVFP4_E2M1) {
+                    e2m1x8_f16x2(words[i], halves);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) halves[e] = e4m3x2_f16x2(words[2 * i + e / 2] >> 16 * (e & 1));
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&halves[4 * i + e]));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&halves[e]));
                     y[e] = pack_bf16(f.x * b * scale, f.y * b * scale);
                 }
-                *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+                out2[i] = make_uint4(y[0], y[1], y[2], y[3]);
             }
-        } else {
-            uint32_t h4[4];
-            e2m1x8_f16x2(words[0], h4);
-            const uint32_t code = p.cache_type == NVFP4_E2M1 ? h4[0] : e4m3x2_f16x2(words[0]);
-            *out = __float2bfloat16_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(code & 0xffffu))) * b * scale);
+            store32(out, sector, out2[0], out2[1]);
         }
     }
 };
 
-// One thread takes V neighbouring values of a key and the same of its value: 16 where rows are whole blocks on their
-// boundaries, else one.
-template <int V>
+// The page of token t's row and its slot there; -1 for padding, and (with a status bit) where there is no such place.
+__device__ __forceinline__ int64_t page_of(const ReadParams& p, int t, int& slot) {
+    const int n = p.positions[t];
+    if (n < 0) return -1;
+    const int seq = p.seq_ids ? p.seq_ids[t] : t / p.per_seq, pi = n / p.page;
+    slot = n - pi * p.page;
+    if (seq >= 0 && seq < p.seqs && pi < p.max_pages) {
+        const int page = p.table[seq * p.table_stride + pi];
+        if (page >= 0 && page < p.pages) return page;
+    }
+    atomicOr(&g_read_status, NVFP4_DEV_BAD_PAGE);
+    return -1;
+}
+
+// One value a thread: any head size and alignment.
+__global__ void __launch_bounds__(128) cache_read_scalar_kernel(const __grid_constant__ ReadParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+    if (at >= 2 * p.pieces) return;
+    const int which = at >= p.pieces;
+    const int64_t to = at - which * p.pieces;
+    const int per_token = p.hk * p.D, t = static_cast<int>(to / per_token), i = static_cast<int>(to - static_cast<int64_t>(t) * per_token);
+    const int h = i / p.D, d = i - h * p.D;
+    int slot = 0;
+    const int64_t page = page_of(p, t, slot);
+    __nv_bfloat16* const out = p.out[which] + to;
+    if (page < 0) {
+        *out = __float2bfloat16_rn(0.0f);
+        return;
+    }
+    const float scale = p.cache_scale[which] ? p.cache_scale[which][h] : 1.0f;
+    if (p.cache_type == NVFP4_E2M1) {
+        const int64_t record = static_cast<int64_t>(h) * (p.page / kRecordKeys) + slot / kRecordKeys;
+        const uint8_t* const rec = static_cast<const uint8_t*>(p.cache[which]) + page * p.page_stride[which] + record * record_bytes(p.D);
+        const int key = slot % kRecordKeys;
+        uint32_t h2[4];
+        e2m1x8_f16x2(rec[key * (p.D / 2) + d / 2], h2);
+        const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(d & 1 ? h2[0] >> 16 : h2[0] & 0xffffu)));
+        *out = __float2bfloat16_rn(v * e4m3_value(rec[8 * p.D + d / 16 * kRecordKeys + key]) * scale);
+        return;
+    }
+    const int64_t from = page * p.page_stride[which] + (static_cast<int64_t>(h) * p.page + slot) * p.D + d;
+    if (p.cache_type == NVFP4_E4M3) *out = __float2bfloat16_rn(e4m3_value(static_cast<const uint8_t*>(p.cache[which])[from]) * scale);
+    else *out = static_cast<const __nv_bfloat16*>(p.cache[which])[from];
+}
+
+// One thread takes 16 neighbouring values of a key and the same of its value. (4 bits, 8192 tokens of 8 + 8 heads of
+// 128 values, us: 10.0; with stores of 16 bytes 12.2; two or four such pairs a thread 12.3 and 13.5, 8 values 14.2.)
+template <int C>
 __global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__ ReadParams p) {
     pdl_launch_dependents();
     pdl_wait();
     const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
     if (at >= p.pieces) return;
     const int per_token = p.hk * p.head_pieces;
-    const int t = p.pieces <= INT32_MAX ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per_token)) : static_cast<int>(at / per_token);
-    const int i = static_cast<int>(at - static_cast<int64_t>(t) * per_token), h = i / p.head_pieces, d = (i - h * p.head_pieces) * V;
-    const int n = p.positions[t];
-    int64_t page = -1;
-    if (n >= 0) {
-        const int seq = p.seq_ids ? p.seq_ids[t] : t / p.per_seq, pi = n / p.page;
-        if (seq >= 0 && seq < p.seqs && pi < p.max_pages) page = p.table[seq * p.table_stride + pi];
-        if (page < 0 || page >= p.pages) {
-            page = -1;
-            atomicOr(&g_read_status, NVFP4_DEV_BAD_PAGE);
-        }
-    }
-    const int64_t to = (static_cast<int64_t>(t) * p.hk + h) * p.D + d;
+    const int t = at >> 32 ? static_cast<int>(at / per_token) : static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per_token));
+    const int i = static_cast<int>(at - static_cast<int64_t>(t) * per_token), h = i / p.head_pieces, d = (i - h * p.head_pieces) * 16;
+    int slot = 0;
+    const int64_t page = page_of(p, t, slot);
+    __nv_bfloat16* const out[2] = {p.out[0] + at * 16, p.out[1] + at * 16};  // pieces lie as the output does
     if (page < 0) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __nv_bfloat16* const out = p.out[which] + to;
-            if constexpr (V == 16) reinterpret_cast<uint4*>(out)[0] = reinterpret_cast<uint4*>(out)[1] = make_uint4(0, 0, 0, 0);
-            else *out = __float2bfloat16_rn(0.0f);
-        }
+        for (int which = 0; which < 2; ++which) store32(out[which], p.sectors, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
         return;
     }
-    Piece<V> piece[2];
+    Piece<C> piece[2];
     float scale[2];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        piece[which].load(p, which, page, h, n % p.page, d);
+        piece[which].load(p, which, page, h, slot, d);
         scale[which] = p.cache_scale[which] ? p.cache_scale[which][h] : 1.0f;
     }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) piece[which].store(p, scale[which], p.out[which] + to);
+    for (int which = 0; which < 2; ++which) piece[which].store(scale[which], out[which], p.sectors);
 }
 
 cudaError_t read_status(int* bits) {
@@ -193,9 +207,11 @@ extern "C" nvfp4_status nvfp4_cache_read(const nvfp4_cache_read_args* a, void* s
         wide = wide && aligned(p.cache[i], piece) && p.page_stride[i] % elements == 0 && aligned(p.out[i], 16);
     p.head_pieces = wide ? p.D / 16 : p.D;
     p.pieces = static_cast<int64_t>(p.T) * p.hk * p.head_pieces;
-    const int64_t ctas = (p.pieces + 127) / 128;
-    if (ctas > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(ctas));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return wide ? launch(cache_read_kernel<16>, grid, dim3(128), 0, st, p) : launch(cache_read_kernel<1>, grid, dim3(128), 0, st, p);
+    const int64_t ctas = ((wide ? 1 : 2) * p.pieces + 127) / 128;
+    if (ctas > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+    p.sectors = aligned(p.out[0], 32) && aligned(p.out[1], 32);
+    const auto kernel = !wide ? cache_read_scalar_kernel : p.cache_type == NVFP4_E2M1 ? cache_read_kernel<NVFP4_E2M1>
+                      : p.cache_type == NVFP4_E4M3 ? cache_read_kernel<NVFP4_E4M3> : cache_read_kernel<NVFP4_BF16>;
+    return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, st, p);
 }

@@ -255,6 +255,24 @@ def test_cache_read(cache, D, page, T):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("offset", [1, 8, 16])
+def test_cache_read_into_outputs_on_any_boundary(cache, offset):
+    g = _gen(offset)
+    T, hk, D, page = 5, 2, 64, 16
+    kc, vc = nv.kv_cache(3, hk, page, D, cache)
+    for c in (kc, vc):
+        _fill(c, g) if cache is FP4 else c.copy_(_randn(c.shape, g).to(cache))
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    pos = torch.tensor([40, 3, -1, 17, 0], dtype=torch.int32, device=DEV)
+    want = nv.cache_read(pos, kc, vc, table)
+    mem = [torch.full((T * hk * D + 64,), math.nan, dtype=BF16, device=DEV) for _ in "kv"]
+    outs = [m[offset:offset + T * hk * D].view(T, hk, D) for m in mem]
+    nv.cache_read(pos, kc, vc, table, k_out=outs[0], v_out=outs[1])
+    for m, o, w in zip(mem, outs, want):
+        assert torch.equal(o, w) and bool(torch.isnan(m[:offset]).all()) and bool(torch.isnan(m[offset + T * hk * D:]).all())
+
+
 @pytest.mark.parametrize("cache", [BF16, FP8])
 def test_cache_read_of_odd_heads_and_pages(cache):
     g = _gen(3)
