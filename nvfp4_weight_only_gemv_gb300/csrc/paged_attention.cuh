@@ -145,6 +145,17 @@ constexpr int kCtasPerSm = 3;
 //
 // The kernel is bound by the cache's bytes.
 //
+// A cache of 4 bits has whole tiles of 64 keys in one run of memory, so a plain bulk copy brings them, issued by one lane a
+// 16-key record where pages cut the tile. Codes are widened to f16 two at a time and multiplied by their
+// block's scale (6 significant bits: exact), for keys as the codes stand in memory (a lane has whole blocks of its two
+// keys), for values with two keys' codes brought side by side first, four logic operations on two words. With 9
+// bits a value the arithmetic no longer hides behind the copies: 64 values of each lane's warp take 4.4 instructions
+// with up to 8 rows (widening and scales 1.1, their products 1, integers 0.7, tensor products 0.25), 5.1 with 16, on
+// pipes of which the widening's takes one every other cycle. 64 x 8191 keys: one row 104.6 us, 5.8 TB/s, 0.86 of
+// the copy rate; four rows of a group of 4 143 us. What such a tile costs beside its values counts: tiles of 32
+// keys took 139 us for one row, steps of 32 keys inside tiles of 64 129, and keys of the next step formed
+// between this one's products 142, all at their own best number of stages.
+//
 // Work is split over the length without the host knowing the lengths: all (sequence, kv head)
 // items lie end to end in units of S tiles (S warps side by side), and every CTA takes an equal
 // run of units, or, up to 32 sequences and where that costs little, an equal part of one item
@@ -167,7 +178,7 @@ struct TileShape {
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
     static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? kCtasPerSm : 2;  // per SM
-    static constexpr bool kQRegs = !kF4 && NT * DP <= 256;
+    static constexpr bool kQRegs = !kF4 && NT * DP <= 256;  // (kF4: read once for 64 keys: 114 us from shared memory, 119)
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
     static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
@@ -328,7 +339,7 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // cap tanh(x / cap) in base-2 units, x times 2 log2(e) / cap given: 1 - 2 / (exp(2 |x|) + 1) throughout, which is off by
 // 2^-22 of the cap where the score is small too. Up to a cap of 256 that is 2^-14 of a nat at most, and 2^-16 at the usual 50,
 // less than the weights' own 11 bits. (7 sequences up to 12001 keys of 4 bits, 15 rows, slopes too: 33.2 us with it, 35.1 with
-// tanh_fast, 35.4 with tanhf, 28.8 with plain scores.)
+// tanh_fast, 35.4 with tanhf, 28.8 with plain scores; all 3 less since.)
 constexpr float kCloseCap = 256.0f;
 __device__ __forceinline__ float capped(float x, float cap) {
     return copysignf(fmaf(-2.0f * cap, rcp_fast(exp2_fast(fabsf(x)) + 1.0f), cap), x);
@@ -660,8 +671,9 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
     if (arrive_last(sh, done, of)) join(0, size < parts ? size : 1, of, -1);
 }
 
-// DP, NT: see TileShape; C: the cache's type; S: scores with a cap or a bias; W: D is DP (4 bits: a lane's offsets in
-// a record are then constants of its loads).
+// DP, NT: see TileShape; C: the cache's type; S: scores with a cap or a bias (7 sequences up to 12001 keys of 4 bits, 15
+// rows: 29.7 us with both, 26.4 without); W: D is DP (4 bits: a lane's offsets in a record are then constants of its loads,
+// 119 us for 125).
 template <int C>
 using KernelParams = std::conditional_t<C == NVFP4_E2M1, AttnParams, TileParams>;
 
