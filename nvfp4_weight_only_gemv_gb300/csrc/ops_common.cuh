@@ -66,7 +66,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
 constexpr int kRecordKeys = 16;
 __host__ __device__ constexpr int64_t record_bytes(int dim) { return 9ll * dim; }
 
-
 // Eight E2M1 codes (element 2i in the low nibble of byte i) to four f16x2, low half = even element (exact).
 __device__ __forceinline__ void e2m1x8_f16x2(uint32_t codes, uint32_t (&h)[4]) {
     asm("{\n .reg .b8 b0, b1, b2, b3;\n"

@@ -339,7 +339,7 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // cap tanh(x / cap) in base-2 units, x times 2 log2(e) / cap given: 1 - 2 / (exp(2 |x|) + 1) throughout, which is off by
 // 2^-22 of the cap where the score is small too. Up to a cap of 256 that is 2^-14 of a nat at most, and 2^-16 at the usual 50,
 // less than the weights' own 11 bits. (7 sequences up to 12001 keys of 4 bits, 15 rows, slopes too: 33.2 us with it, 35.1 with
-// tanh_fast, 35.4 with tanhf, 28.8 with plain scores; all 3 less since.)
+// tanh_fast, 35.4 with tanhf, 28.8 with plain scores, before the join that takes 29.7 now.)
 constexpr float kCloseCap = 256.0f;
 __device__ __forceinline__ float capped(float x, float cap) {
     return copysignf(fmaf(-2.0f * cap, rcp_fast(exp2_fast(fabsf(x)) + 1.0f), cap), x);
@@ -918,9 +918,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             if (lane == 0) barrier_expect(bar, H * rec);
             __syncwarp();
             if (mine) copy_bytes(to + lane * rec, source[which], p.tall_box ? H * rec : rec, bar, pol4);
-            return;
-        }
-        else if (lane == 0) {
+        } else if (lane == 0) {
             const uint64_t pol = evict_first();
             barrier_expect(bar, T::kPart);
 #pragma unroll
@@ -1082,7 +1080,8 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             for (int mt = 0; mt < T::kMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
-        const float cap_out = S ? p.cap * 1.4426950408889634f : 0.0f, cap_in = S && p.cap > 0.0f ? (p.cap <= kCloseCap ? 2.8853900817779268f : 1.0f) / cap_out : 0.0f;
+        const float cap_out = S ? p.cap * 1.4426950408889634f : 0.0f;
+        const float cap_in = S && p.cap > 0.0f ? (p.cap <= kCloseCap ? 2.8853900817779268f : 1.0f) / cap_out : 0.0f;
         const bool was_dead = dead;
         for (; tile < tile_end && !dead; tile += streams) {
             // --- scores

@@ -661,3 +661,109 @@ def test_refusals():
     b16 = nv.kv_cache(1, 2, 16, 64)
     with pytest.raises(ValueError):
         nv.cache_read(pos, *b16, table, k_scale=torch.ones(2, device=DEV))
+
+
+# ------------------------------------------------------------------------------ beside the usual
+
+def test_a_long_prompt_on_both_kernels():
+    # a warp takes a whole token where tokens are many: the same values, and the same keys but for their last bits
+    g = _gen(31)
+    T, hq, hk, D, page = 3001, 4, 3, 128, 64
+    q, k, v = (_randn((T, n, D), g, BF16) for n in (hq, hk, hk))
+    at = torch.randperm(T, generator=g, device=DEV).int()
+    freq, _ = nv.rope_frequencies(D)
+    table = torch.randperm(48, generator=g, device=DEV).int()[None, :47]
+    norm, scale = (1 + 0.2 * _randn((D,), g)).to(BF16), 0.5 + torch.rand(hk, generator=g, device=DEV)
+    got = []
+    for variant in (0, 1):
+        kc, vc = nv.kv_cache(48, hk, page, D, FP4)
+        nv.set_variant(variant)
+        try:
+            out = nv.rope_append(q, k, v, at, freq, kc, vc, table, k_norm=norm, k_scale=scale, v_scale=scale)
+        finally:
+            nv.set_variant(0)
+        got.append((out, *nv.cache_read(at, kc, vc, table, k_scale=scale, v_scale=scale)))
+    assert nv.device_status() == 0
+    (qa, ka, va), (qb, kb, vb) = got
+    assert torch.equal(va, vb)
+    # queries: each kernel's fp32 value, up to 24 roundings of magnitudes below 8 off, rounded to bf16
+    _within(qa, qb.double(), qb.double().abs() * 2 * U16 + 2 * 24 * U32 * 8, "q")
+    # a key beside a border takes the other code of two, or its block the other scale: one in 10^5, not more
+    assert float((ka != kb).float().mean()) < 1e-4
+    back = vb.double() / scale.double()[:, None]
+    top = (v.double() / scale.double()[:, None]).view(T, hk, 8, 16).abs().amax(dim=3, keepdim=True)
+    off = (back - v.double() / scale.double()[:, None]).view(T, hk, 8, 16).abs()
+    # half a step of the largest binade, 1 / 6 of the largest value, of a scale 2^-4 off, and the row's bf16
+    assert bool((off <= top * ((1 / 6) * (1 + U8) + U8 + U16)).all())
+
+
+def test_the_same_token_twice_leaves_one_of_its_places_whole():
+    # all bytes of the place are one of the tokens': codes of either, the scale of either
+    g = _gen(5)
+    k = _randn((2, 1, 16), g, BF16)
+    kc, vc = nv.kv_cache(1, 1, 16, 16, FP4)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    nv.rope_append(None, k, k, zero, torch.empty(0, device=DEV), kc, vc, zero[:1][None], zero)
+    codes, blocks = _records_of(k, torch.ones(1, device=DEV))
+    for c in (kc, vc):
+        gc, gb = _bytes_at(c, 0, 0)
+        assert bool(((gc == codes[0]) | (gc == codes[1])).all()) and bool(((gb == blocks[0]) | (gb == blocks[1])).all())
+        assert not c.reshape(-1)[8:128].any() and nv.device_status() == 0
+
+
+def test_two_graphs_share_a_workspace():
+    calls = []
+    for i, (lengths, rows, cap) in enumerate([([3000, 30], 1, 0.0), ([700, 1, 0, 90], 4, 20.0)]):
+        q, kc, vc, table, ln, ks, vs = _inputs(lengths, rows, 8, 2, 128, FP4, 16, i)
+        calls.append((q, kc, vc, table, ln, dict(k_scale=ks, v_scale=vs, softcap=cap)))
+    ws = max((nv.attention_workspace(len(c[4]), len(c[0]) // len(c[4]), 8, 2, 128) for c in calls), key=len)
+    want = [nv.paged_attention(*c[:5], **c[5]) for c in calls]
+    graphs, kept = [], []
+    for c in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kept.append(nv.paged_attention(*c[:5], workspace=ws, **c[5]))
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 0, 1):
+        kept[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept[i], want[i]), i
+    assert nv.device_status() == 0
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    q, kc, vc, table, ln, ks, vs = _inputs([9000, 2000], 2, 8, 2, 128, FP4, 16, 3)
+    want = nv.paged_attention(q, kc, vc, table, ln, k_scale=ks, v_scale=vs)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [nv.paged_attention(q, kc, vc, table, ln, k_scale=ks, v_scale=vs, stream=s) for s in streams for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got) and nv.device_status() == 0
+
+
+def test_rows_read_on_another_stream_are_its_own():
+    from test_gpu_decode_ops_edges import _owner
+    _, kc, vc, table, _, ks, vs = _inputs([40], 1, 2, 2, 64, FP4, 16, 3)
+    at = torch.arange(40, dtype=torch.int32, device=DEV)
+    want = nv.cache_read(at, kc, vc, table, k_scale=ks, v_scale=vs)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = nv.cache_read(at, kc, vc, table, k_scale=ks, v_scale=vs, stream=side)
+    mixed = nv.cache_read(at, kc, vc, table, k_scale=ks, v_scale=vs, stream=side.cuda_stream, k_out=torch.empty_like(want[0]))
+    side.synchronize()
+    for g, w in zip((*got, *mixed), (*want, *want)):
+        assert torch.equal(g, w)
+    assert _owner(got[0]) == _owner(got[1]) == _owner(mixed[1]) == side.cuda_stream
+
+
+def test_nothing_to_do():
+    kc, vc = nv.kv_cache(2, 2, 16, 64, FP4)
+    none = torch.zeros((0, 3), dtype=torch.int32, device=DEV)
+    q, i = torch.empty((0, 4, 64), dtype=BF16, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV)
+    assert nv.paged_attention(q, kc, vc, none, i, softcap=3.0).shape == (0, 4, 64)
+    assert nv.rope_append(None, q[:, :2], q[:, :2], i, torch.empty(0, device=DEV), kc, vc, none) is None
+    k, v = nv.cache_read(i, kc, vc, none)
+    assert k.shape == v.shape == (0, 2, 64) and nv.device_status() == 0
+    with pytest.raises(ValueError):
+        nv.cache_read(torch.zeros(1, dtype=torch.int32, device=DEV), kc, vc, none)
