@@ -732,10 +732,14 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         // An item of few units is not split where a join takes longer than they do. us split and not: 2
         // units of one row 8.8 and 7.0, 5 units of one row 8.7 and 9.8, of two 11.1 and 12.0, of four
         // 13.3 and 12.5, of eight 21.8 and 20.2 (rows that a thread joins).
-        const int least = (total + grid - 1) / grid, alone = min(2 + join_turns(p), 6);
+        // 4 bits: a unit of 256 keys, and its start, cost more (1 x 1000 keys, 4 rows: 13.9 us cut above 2 units, 16.2 above 6;
+        // 1 x 500, one row: 8.1 and, cut above one, 9.4), and a unit beyond the share is a larger part of it (30 x 3000 keys:
+        // 31.7 us with one, 32.2 with three; 16 ragged up to 8191 26.0, 26.3 and, with none, 30.0).
+        constexpr bool kLarge = F4 && NT < 4;
+        const int least = (total + grid - 1) / grid, alone = kLarge ? 2 : min(2 + join_turns(p), 6), slack = kLarge ? 1 : kAlignSlack;
         int n = 0, before = 0;  // CTAs of an item of this lane's sequence; CTAs or units before the sequence
         bool whole_items = false;
-        for (int load = least; load <= least + kAlignSlack && !whole_items; ++load) {
+        for (int load = least; load <= least + slack && !whole_items; ++load) {
             n = sp.units <= alone ? sp.units > 0 : (sp.units + load - 1) / load;
             whole_items = __reduce_add_sync(0xffffffffu, n) * p.columns <= grid;
         }
