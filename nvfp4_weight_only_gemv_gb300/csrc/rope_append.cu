@@ -258,7 +258,7 @@ __device__ __forceinline__ uint32_t block_codes(float (&v)[8], float b) {
     return pack_e2m1x8(v);
 }
 
-// F4: a cache of 4 bits. A lane's vectors are halves of two blocks, whose other halves its neighbour has, or, where
+// F4: a cache of 4 bits. A lane's vectors are halves of two blocks, whose other halves its neighbours have, or, where
 // pairs are neighbours or do not turn, one block. (8192 tokens of 32 + 8 + 8 heads: 47 us, 4.0 TB/s, as latency-bound as
 // the others: without the codes' arithmetic 44; a block's scale stored or not, quotients without clamps, 128 registers,
 // 80, cosines read from shared memory each time, rows prefetched into L2: 47, 47, 52, 58, 53, 51.)
@@ -395,7 +395,13 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
                         ta = max(ta, __float_as_uint(a[e]) & 0x7fffffffu);
                         tb = max(tb, __float_as_uint(b[e]) & 0x7fffffffu);
                     }
-                    const uint32_t na = __shfl_xor_sync(0xffffffffu, ta, 1), nb = __shfl_xor_sync(0xffffffffu, tb, 1);
+                    uint32_t na = __shfl_xor_sync(0xffffffffu, ta, 1), nb = __shfl_xor_sync(0xffffffffu, tb, 1);
+                    if (p.half & 8) {  // where the halves meet, a block has the last lane's first and the first lane's second vector
+                        const uint32_t first = __shfl_sync(0xffffffffu, tb, lane - i), last = __shfl_sync(0xffffffffu, ta, lane - i + (p.half >> 3) - 1);
+                        const uint32_t mid = __shfl_sync(0xffffffffu, tb, i == 0 ? lane : i & 1 ? lane + 1 : lane - 1);
+                        if (i == (p.half >> 3) - 1) na = first;
+                        nb = i == 0 ? last : mid;
+                    }
                     const uint32_t ba = block_scale(max(ta, halves ? na : tb)), bb = halves ? block_scale(max(tb, nb)) : ba;
                     if (live && h < heads) {
                         const int key = at.slot % kRecordKeys;
@@ -501,9 +507,8 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;  // (E2M1: words of codes)
         return ok;
     };
-    // In 4 bits a block is two lanes' halves or one lane's: whole blocks turn, or pairs are neighbours.
-    const bool f4 = p.cache_type == NVFP4_E2M1;
-    const int v = host_variant() == 1 || (f4 && !p.interleaved && p.half % 16) ? 0 : fits(8) ? 8 : !f4 && fits(4) ? 4 : 0;
+    const bool f4 = p.cache_type == NVFP4_E2M1;  // in vectors of 8 alone: a block is two lanes' halves or one lane's
+    const int v = host_variant() == 1 ? 0 : fits(8) ? 8 : !f4 && fits(4) ? 4 : 0;
     if (v) {
         while ((2 * v << p.lanes_log2) < p.D) ++p.lanes_log2;
         // A token's heads are shared among warps, down to one step each, until the SMs' warps are filled twice
