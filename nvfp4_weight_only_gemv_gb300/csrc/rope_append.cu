@@ -246,20 +246,22 @@ __device__ __forceinline__ float quotient_to(float most, float x, float s, float
     return fmaf(fmaf(q, s, -x), -inv, q);
 }
 
-// The E2M1 codes of eight values of a block whose scale stands for b.
-__device__ __forceinline__ uint32_t block_codes(float (&v)[8], float b) {
+// The E2M1 codes of eight (or, in the low half, four) values of a block whose scale stands for b.
+template <int V>
+__device__ __forceinline__ uint32_t block_codes(const float (&x)[V], float b) {
     if (b == 0.0f) return 0u;
     // b has 4 bits, so a quotient lies 2^-28 of itself and more from the middle of two floats, and what the correction
     // leaves of a reciprocal that is a unit off, 2^-46, does not reach it
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(b));
+    float v[8] = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = quotient_to(8.0f, v[e], b, inv);
+    for (int e = 0; e < V; ++e) v[e] = quotient_to(8.0f, x[e], b, inv);
     return pack_e2m1x8(v);
 }
 
-// F4: a cache of 4 bits. A lane's vectors are halves of two blocks, whose other halves its neighbours have, or, where
-// pairs are neighbours or do not turn, one block. (8192 tokens of 32 + 8 + 8 heads: 47 us, 4.0 TB/s, as latency-bound as
+// F4: a cache of 4 bits. With V = 8 a lane's vectors are halves of two blocks, whose other halves its neighbours have, or, where
+// pairs are neighbours or do not turn, one block; with V = 4, quarters of any, whose largest values meet in shared memory. (8192 tokens of 32 + 8 + 8 heads: 47 us, 4.0 TB/s, as latency-bound as
 // the others: without the codes' arithmetic 44; a block's scale stored or not, quotients without clamps, 128 registers,
 // 80, cosines read from shared memory each time, rows prefetched into L2: 47, 47, 52, 58, 53, 51.)
 template <typename XT, int V, bool F4>
@@ -395,6 +397,31 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
                         ta = max(ta, __float_as_uint(a[e]) & 0x7fffffffu);
                         tb = max(tb, __float_as_uint(b[e]) & 0x7fffffffu);
                     }
+                    if constexpr (V == 4) {
+                        // the head's vectors in order: this lane's are the va-th and the vb-th
+                        const int va = oa / V, vb = ob / V, row0 = sub * 2 * lanes;
+                        uint32_t* const tops = reinterpret_cast<uint32_t*>(cs_all + kThreads / 32 * p.half) + warp * 64;
+                        if (live) { tops[row0 + va] = ta; tops[row0 + vb] = tb; }
+                        __syncwarp();
+                        if (live && h < heads) {
+                            auto top_of = [&](int vec) {
+                                const uint4 t4 = *reinterpret_cast<const uint4*>(tops + row0 + (vec & ~3));
+                                return max(max(t4.x, t4.y), max(t4.z, t4.w));
+                            };
+                            const uint32_t ba = block_scale(top_of(va)), bb = block_scale(top_of(vb));
+                            const int key = at.slot % kRecordKeys;
+                            uint8_t* const rec = reinterpret_cast<uint8_t*>(y);
+                            uint8_t* const codes = rec + key * (p.D >> 1);
+                            *reinterpret_cast<uint16_t*>(codes + (oa >> 1)) = static_cast<uint16_t>(block_codes(a, e4m3_value(ba)));
+                            *reinterpret_cast<uint16_t*>(codes + (ob >> 1)) = static_cast<uint16_t>(block_codes(b, e4m3_value(bb)));
+                            if (va % 4 == 0) rec[8 * p.D + oa + key] = static_cast<uint8_t>(ba);
+                            if (vb % 4 == 0) rec[8 * p.D + ob + key] = static_cast<uint8_t>(bb);
+                        }
+                        __syncwarp();
+                        h += hpi;
+                        y += y_step;
+                        return;
+                    }
                     uint32_t na = __shfl_xor_sync(0xffffffffu, ta, 1), nb = __shfl_xor_sync(0xffffffffu, tb, 1);
                     if (p.half & 8) {  // where the halves meet, a block has the last lane's first and the first lane's second vector
                         const uint32_t first = __shfl_sync(0xffffffffu, tb, lane - i), last = __shfl_sync(0xffffffffu, ta, lane - i + (p.half >> 3) - 1);
@@ -507,8 +534,8 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         for (int i = 0; i < 2; ++i) ok = ok && on(p.cache[i], cb * v) && p.page_stride[i] % v == 0;  // (E2M1: words of codes)
         return ok;
     };
-    const bool f4 = p.cache_type == NVFP4_E2M1;  // in vectors of 8 alone: a block is two lanes' halves or one lane's
-    const int v = host_variant() == 1 ? 0 : fits(8) ? 8 : !f4 && fits(4) ? 4 : 0;
+    const bool f4 = p.cache_type == NVFP4_E2M1;
+    const int v = host_variant() == 1 ? 0 : fits(8) ? 8 : fits(4) ? 4 : 0;
     if (v) {
         while ((2 * v << p.lanes_log2) < p.D) ++p.lanes_log2;
         // A token's heads are shared among warps, down to one step each, until the SMs' warps are filled twice
@@ -519,8 +546,11 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
         const int warps = kThreads / 32;
         const int64_t ctas = (static_cast<int64_t>(p.T) * p.shares + warps - 1) / warps;
         const dim3 grid(static_cast<unsigned>(ctas));
-        const size_t smem = static_cast<size_t>(warps) * p.half * sizeof(float2);
+        const size_t smem = static_cast<size_t>(warps) * (p.half * sizeof(float2) + (f4 && v == 4 ? 64 * sizeof(uint32_t) : 0));
         const bool f32 = a->x_type == NVFP4_F32;
+        if (f4 && v == 4)
+            return f32 ? launch(rope_append_kernel<float, 4, true>, grid, dim3(kThreads), smem, st, p)
+                       : launch(rope_append_kernel<__nv_bfloat16, 4, true>, grid, dim3(kThreads), smem, st, p);
         if (f4)
             return f32 ? launch(rope_append_kernel<float, 8, true>, grid, dim3(kThreads), smem, st, p)
                        : launch(rope_append_kernel<__nv_bfloat16, 8, true>, grid, dim3(kThreads), smem, st, p);

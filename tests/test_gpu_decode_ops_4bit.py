@@ -135,7 +135,8 @@ def _check_append(T, hq, hk, D, half, interleaved, xt, fused, page, norm, positi
                                                 (64, 32, False), (96, 48, True), (96, 48, False), (80, 40, False),
                                                 (256, 64, False), (128, 0, False), (48, 20, False), (48, 3, True),
                                                 (16, 8, False), (512, 256, False), (112, 56, True), (144, 16, False),
-                                                (112, 56, False), (80, 24, False), (144, 72, False), (48, 8, False), (80, 40, True)])
+                                                (112, 56, False), (80, 24, False), (144, 72, False), (48, 8, False), (80, 40, True),
+                                                (80, 20, False), (80, 20, True), (256, 60, False), (16, 4, False), (64, 28, True)])
 @pytest.mark.parametrize("xt,fused,norm", [(F32, False, True), (BF16, True, False), (BF16, True, True)])
 def test_append(D, half, interleaved, xt, fused, norm):
     _check_append(6, 5, 2, D, half, interleaved, xt, fused, 16, norm, [0, 1, 2, 15, 16, 40], 2, scaled=not norm)
