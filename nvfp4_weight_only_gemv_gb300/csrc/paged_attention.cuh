@@ -1202,7 +1202,10 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                             for (int e = 0; e < 4; ++e) s[i][nt][e] = f(s[i][nt][e], zf[nt][e & 1]);
                 };
                 if (p.cap == 0.0f) each([&](float z, float f) { return z * f; });
-                else if (p.cap <= kCloseCap) each([&](float z, float f) { return capped(z * fminf(f * cap_in, FLT_MAX), cap_out); });
+                else if (p.cap <= kCloseCap) each([&](float z, float f) {
+                    const float by = f * cap_in;  // finite, or a score of zero would be NaN; a NaN stays one
+                    return capped(z * (by > FLT_MAX ? FLT_MAX : by), cap_out);
+                });
                 else each([&](float z, float f) { return cap_out * tanh_fast(z * f * cap_in); });
                 if (p.slopes) {
 #pragma unroll
