@@ -358,6 +358,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g.scale = real(a[5]);
         nvfp4_attention_scores scores{};
         scores.softcap = real(a[7]);
+        // a cap that only becomes zero here is too small, and no leave to go without one
+        if (scores.softcap == 0.0f && PyFloat_AsDouble(a[7]) != 0.0) return NVFP4_ERR_SHAPE;
         if (a[8] != Py_None) scores.slopes = static_cast<const float*>(c.vector(a[8], "slopes", kF32, g.q_heads).data_ptr());
         return g_paged_attention(&g, &scores, c.stream(a[14]));
     });

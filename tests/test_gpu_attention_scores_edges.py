@@ -32,3 +32,15 @@ def test_a_head_scale_of_nan_makes_its_head_nan(variant, cache, cap):
     assert bool(torch.isnan(got[:, 2:].float()).all()) and bool(torch.isnan(lse[1][:, 2:]).all())
     assert torch.equal(got[:, :2], clean[:, :2]) and torch.equal(lse[1][:, :2], lse[0][:, :2])
     assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("cap", [1e-46, -1e-46, 5e-324, 1e300, -1e300, 2.0 ** -40 * (1 - 2.0 ** -24), 2.0 ** 40 * (1 + 2.0 ** -23)])
+def test_caps_that_no_float_in_the_range_holds_are_refused(cap):
+    q, kc, vc, table, ln, _, _ = _inputs([5, 6], 2, 4, 2, 64, BF16, 16, 8)
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.paged_attention(q, kc, vc, table, ln, softcap=cap)
+    assert e.value.status == 2
+    # (integers and zeros of either sign are numbers like others)
+    want = nv.paged_attention(q, kc, vc, table, ln, softcap=0.0)
+    assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, softcap=-0.0), want)
+    assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, softcap=0), want)
