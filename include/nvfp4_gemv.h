@@ -422,7 +422,8 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_paged_attention_args* args, void*
 /*
  * The same attention with other scores. With s_j = scale * q . k_j, position i of the query row and its head h:
  *     z_j = softcap * tanh(s_j / softcap)  (softcap = 0: s_j)  - slopes[h] * (i - j)  (slopes NULL: no bias)
- * take the place of s_j in out and lse. softcap is 0 or between 2^-40 and 2^40 (else NVFP4_ERR_SHAPE); slopes
+ * take the place of s_j in out and lse, in fp32; over a cache of 4 bits a softcap of up to 64 leaves an error of
+ * 2^-22 softcap in z_j. softcap is 0 or between 2^-40 and 2^40 (else NVFP4_ERR_SHAPE); slopes
  * [q_heads] f32, finite, of either sign. scores = NULL, or neither form asked for: nvfp4_paged_attention.
  */
 typedef struct {

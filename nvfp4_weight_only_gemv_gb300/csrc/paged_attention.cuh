@@ -326,8 +326,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// tanh without a branch: its power series up to x^9 below 0.3 (the next term is 2^-24 of it), 1 - 2 / (exp(2 |x|) + 1) beyond,
-// within 2^-22 of 1.
+// tanh without a branch: its power series up to x^9 below 0.3 (the next term is 2^-24 of it), which keeps small scores' bits,
+// 1 - 2 / (exp(2 |x|) + 1) beyond, within 2^-22 of 1.
 __device__ __forceinline__ float tanh_fast(float x) {
     const float x2 = x * x, a = fabsf(x);
     float p = fmaf(x2, 62.0f / 2835.0f, -17.0f / 315.0f);
@@ -336,11 +336,11 @@ __device__ __forceinline__ float tanh_fast(float x) {
     const float low = fmaf(x * x2, p, x);
     return a < 0.3f ? low : copysignf(fmaf(-2.0f, rcp_fast(exp2_fast(a * 2.8853900817779268f) + 1.0f), 1.0f), x);
 }
-// cap tanh(x / cap) in base-2 units, x times 2 log2(e) / cap given: 1 - 2 / (exp(2 |x|) + 1) throughout, which is off by
-// 2^-22 of the cap where the score is small too. Up to a cap of 256 that is 2^-14 of a nat at most, and 2^-16 at the usual 50,
-// less than the weights' own 11 bits. (7 sequences up to 12001 keys of 4 bits, 15 rows, slopes too: 33.2 us with it, 35.1 with
-// tanh_fast, 35.4 with tanhf, 28.8 with plain scores, before the join that takes 29.7 now.)
-constexpr float kCloseCap = 256.0f;
+// cap tanh(x / cap) in base-2 units, x times 2 log2(e) / cap given, for caps up to kCloseCap over 4 bits: 1 - 2 / (exp(2 |x|) + 1)
+// throughout, which is off by 2^-22 of the cap where the score is small too. That is 2^-16 of a nat at most, next to weights
+// of 11 bits. Those tiles are bound by their instructions: 64 x 8191 keys, one row 112.8 us with it and 120 with tanh_fast, four rows
+// 168 and 191. Over bf16 tanh_fast costs nothing (32 x 8191 keys, two rows: 163 us both), over E4M3 0.5 % (64 x 8191: 162.6, 163.5).
+constexpr float kCloseCap = 64.0f;
 __device__ __forceinline__ float capped(float x, float cap) {
     return copysignf(fmaf(-2.0f * cap, rcp_fast(exp2_fast(fabsf(x)) + 1.0f), cap), x);
 }
@@ -1085,7 +1085,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         }
 
         const float cap_out = S ? p.cap * 1.4426950408889634f : 0.0f;
-        const float cap_in = S && p.cap > 0.0f ? (p.cap <= kCloseCap ? 2.8853900817779268f : 1.0f) / cap_out : 0.0f;
+        const float cap_in = S && p.cap > 0.0f ? (F4 && p.cap <= kCloseCap ? 2.8853900817779268f : 1.0f) / cap_out : 0.0f;
         const bool was_dead = dead;
         for (; tile < tile_end && !dead; tile += streams) {
             // --- scores
@@ -1202,7 +1202,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                             for (int e = 0; e < 4; ++e) s[i][nt][e] = f(s[i][nt][e], zf[nt][e & 1]);
                 };
                 if (p.cap == 0.0f) each([&](float z, float f) { return z * f; });
-                else if (p.cap <= kCloseCap) each([&](float z, float f) {
+                else if (F4 && p.cap <= kCloseCap) each([&](float z, float f) {
                     const float by = f * cap_in;  // finite, or a score of zero would be NaN; a NaN stays one
                     return capped(z * (by > FLT_MAX ? FLT_MAX : by), cap_out);
                 });

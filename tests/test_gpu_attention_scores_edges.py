@@ -44,3 +44,35 @@ def test_caps_that_no_float_in_the_range_holds_are_refused(cap):
     want = nv.paged_attention(q, kc, vc, table, ln, softcap=0.0)
     assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, softcap=-0.0), want)
     assert torch.equal(nv.paged_attention(q, kc, vc, table, ln, softcap=0), want)
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("cap", [8.0, 50.0, 100.0, 256.0, 1000.0])
+def test_a_capped_score_has_the_bits_that_are_stated(variant, cache, cap):
+    # one key a sequence, of one value: lse is the score itself. x = s / cap takes 6 roundings of 2^-24 (the factor, its
+    # quotient by the cap, the product), tanh's series below 0.3 four, cap and lse's unit 5: 16 of the score, 24 with
+    # room for their meeting. Beyond 0.3 tanh is within 2^-22 of 1; with up to 64 over 4 bits that is so of any score.
+    x = torch.exp2(torch.linspace(-14, 3, 70, device=DEV))
+    q = torch.zeros((140, 1, 64), device=DEV, dtype=BF16)
+    q[:, 0, 0] = (torch.cat([x, -x]) * cap / 1.5).to(BF16)
+    n = len(q)
+    kc, vc = nv.kv_cache(n, 1, 16, 64, cache)
+    k = torch.zeros((n, 1, 64), device=DEV)
+    k[:, :, 0] = 1.5  # exact in every type
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[:, None]
+    none = torch.empty(0, device=DEV)
+    nv.rope_append(None, k, k, torch.zeros(n, dtype=torch.int32, device=DEV), none, kc, vc, table)
+    lse = torch.empty((n, 1), device=DEV)
+    nv.paged_attention(q, kc, vc, table, torch.ones(n, dtype=torch.int32, device=DEV), 1.0, softcap=cap, lse=lse)
+    assert nv.device_status() == 0
+    s = q[:, 0, :1].double() * 1.5
+    z = cap * torch.tanh(s / cap)
+    near = s.abs() >= 0.29 * cap
+    if cache is FP4 and cap <= 64 and variant == 0:
+        near[:] = True
+    err = (lse.double() - z).abs() - near * cap * 2.0 ** -22
+    if cache is not BF16 and variant == 0:
+        # f16 weights, and what l and the reference m refer to, carry 2^7: m - 7 in base 2, where |m| is below 1, has steps
+        # of 2^-21 and is off by 2^-22 of a power of two, 0.7 of it in lse; with larger |m| by 2^-24 of |m| + 7
+        err -= 0.7 * torch.clamp((z.abs() * 1.4427 + 7) * 2.0 ** -24, min=2.0 ** -22)
+    assert bool((err <= 24 * 2.0 ** -24 * z.abs()).all()), float((err / z.abs()).max() * 2 ** 24)
