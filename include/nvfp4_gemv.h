@@ -320,7 +320,8 @@ nvfp4_status nvfp4_rms_norm(const nvfp4_rms_norm_args* args, void* stream);
  * n % page_size of page page_table[seq][n / page_size], as bf16 or as E4M3(value / scale) (an fp32
  * quotient, to nearest even, clamped to +-448; scales are positive). A cache of 4 bits: of 16 elements t = value / scale
  * the block scale is b = E4M3(max|t| / 6), the codes E2M1(t / b), all fp32 quotients, to nearest even, beyond the
- * types' largest to the largest; b = 0 gives zeros, a NaN makes b NaN. Long-context scalings of the
+ * types' largest to the largest; b = 0 gives zeros, a NaN makes b NaN. So max|t| should lie between 0.094 (b is subnormal
+ * below it, and 0 up to 6 * 2^-10) and 2688 (beyond which blocks saturate). Long-context scalings of the
  * frequencies are the caller's, in inv_freq and mscale. A token with a negative position is padding: nothing is appended and its q
  * row is zero. Positions are below 2^24 (beyond it, a call without keys rounds them to fp32). A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and appends
  * nothing. Two tokens of one call at the same sequence and position leave either's values, in 4 bits perhaps

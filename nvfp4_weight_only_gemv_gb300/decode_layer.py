@@ -48,13 +48,17 @@ class DecodeLayer:
         self.norms = [(1 + 0.1 * torch.randn(n, generator=gen)).to(torch.bfloat16).to(device)
                       for n in (hidden, hidden, head_dim, head_dim)]  # input, post-attention, q, k
 
-    def make_cache(self, seqs, tokens, page_size=64, dtype=torch.bfloat16, device="cuda"):
-        """A cache of `tokens` places per sequence: (k, v, page table, k scales, v scales)."""
+    def make_cache(self, seqs, tokens, page_size=64, dtype=torch.bfloat16, device="cuda", scale=None):
+        """A cache of `tokens` places per sequence: (k, v, page table, k scales, v scales). ``scale`` is that of every head;
+        None takes 0.05 for 8 bits, and none for 4 bits, whose block scales cover rows like these: largest values of 16
+        neighbours between 0.1 and 2688 (see kv_cache)."""
         per_seq = -(-tokens // page_size)
         k, v = nv.kv_cache(seqs * per_seq, self.kv_heads, page_size, self.head_dim, dtype, device)
         table = torch.arange(seqs * per_seq, dtype=torch.int32, device=device).view(seqs, per_seq)
-        # (block scales take a 4-bit cache to any magnitude)
-        scale = torch.full((self.kv_heads,), 0.05, device=device) if dtype == torch.float8_e4m3fn else None
+        if scale is None and dtype == torch.float8_e4m3fn:
+            scale = 0.05
+        if scale is not None:
+            scale = torch.full((self.kv_heads,), float(scale), device=device)
         return k, v, table, scale, scale
 
     def fill_cache(self, cache, keys, values, positions, seq_ids):

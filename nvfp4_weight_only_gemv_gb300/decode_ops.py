@@ -125,7 +125,9 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out
 def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16, device=None):
     """A zeroed pair of caches (k, v), each [pages, kv_heads, page_size, head_dim], halves of one
     allocation in which a page's keys and values are neighbours. dtype uint8 makes 4-bit caches, with 9 / 16
-    of head_dim bytes in the last dimension."""
+    of head_dim bytes in the last dimension. Their block scales are E4M3: in units of the head's scale (1 without
+    one), 16 neighbours whose largest magnitude is at most 6 * 2^-10 = 0.0059 become zeros, below 0.094 their scale has
+    3 bits and fewer, and beyond 2688 they saturate. Rows of other magnitudes need a k_scale and v_scale."""
     if dtype not in (_BF16, _E4M3, _U8):
         raise TypeError(f"a cache is bfloat16, float8_e4m3fn or uint8 (4 bits) (got {dtype})")
     if dtype is _U8:
@@ -178,7 +180,8 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_
     turns the first 2 * half values of a head, in halves or ``interleaved`` pairs; mscale multiplies
     cos and sin (rope_frequencies gives both). q_norm, k_norm [D]: root-mean-square norm of each
     head first. k_scale, v_scale float32 [kv_heads]: what the values of an 8-bit or 4-bit cache are divided
-    by. In a 4-bit cache each 16 neighbours get a block scale of their own, E4M3(largest magnitude / 6)."""
+    by. In a 4-bit cache each 16 neighbours get a block scale of their own, E4M3(largest magnitude / 6), which covers
+    quotients of 0.0059 to 2688 (see kv_cache)."""
     if stream is not None and out is None:
         return _nv._on_stream(stream, rope_append, q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_ids,
                               interleaved=interleaved, mscale=mscale, q_norm=q_norm, k_norm=k_norm, eps=eps,
