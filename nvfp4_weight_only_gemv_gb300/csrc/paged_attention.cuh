@@ -732,11 +732,14 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         // An item of few units is not split where a join takes longer than they do. us split and not: 2
         // units of one row 8.8 and 7.0, 5 units of one row 8.7 and 9.8, of two 11.1 and 12.0, of four
         // 13.3 and 12.5, of eight 21.8 and 20.2 (rows that a thread joins).
-        // 4 bits: a unit of 256 keys, and its start, cost more (1 x 1000 keys, 4 rows: 13.9 us cut above 2 units, 16.2 above 6;
-        // 1 x 500, one row: 8.1 and, cut above one, 9.4), and a unit beyond the share is a larger part of it (30 x 3000 keys:
-        // 31.7 us with one, 32.2 with three; 16 ragged up to 8191 26.0, 26.3 and, with none, 30.0).
+        // 4 bits in tiles of 64 keys: a unit is 256 keys (heads of 256: 512 with up to 8 rows, 256 with 16, 128 with 32, 64
+        // with 64), and it and its start cost more (1 x 1000 keys, 16 rows: 13.9 us cut above 2 units, 16.2 above 6; 1 x 500,
+        // 4 rows: 8.1 and, cut above one, 9.4; heads of 256, 8 x 1000, 4 rows: 13.5 above 2, 14.4 above one; 1 x 400, 32
+        // rows: 17.7 above 2, 22.1 above 4), except that units of 64 keys stay whole up to 6: their 64 rows join slowly (1 x 150
+        // 21.4 us, 25.2 above 2; 1 x 300 27.9, 31.7; 1 x 600 36.4, and 43.8 uncut). A unit beyond the share is a larger part of
+        // it (30 x 3000 keys: 31.7 us with one, 32.2 with three; 16 ragged up to 8191 26.0, 26.3 and, with none, 30.0).
         constexpr bool kLarge = F4 && NT < 4;
-        const int least = (total + grid - 1) / grid, alone = kLarge ? 2 : min(2 + join_turns(p), 6), slack = kLarge ? 1 : kAlignSlack;
+        const int least = (total + grid - 1) / grid, alone = kLarge ? (unit_keys < 128 ? 6 : 2) : min(2 + join_turns(p), 6), slack = kLarge ? 1 : kAlignSlack;
         int n = 0, before = 0;  // CTAs of an item of this lane's sequence; CTAs or units before the sequence
         bool whole_items = false;
         for (int load = least; load <= least + slack && !whole_items; ++load) {
