@@ -14,8 +14,6 @@ namespace {
 
 using namespace ops;
 
-__device__ int g_read_status;
-
 struct ReadParams {
     const void* cache[2];    // k, v
     const float* cache_scale[2];
@@ -26,6 +24,7 @@ struct ReadParams {
     int64_t page_stride[2], table_stride;
     int64_t pieces;          // of all tokens' keys
     int T, hk, D, seqs, per_seq, pages, max_pages, page, cache_type;
+    int* status;             // see host_status_word
     int head_pieces;         // of a head
     int sectors;             // the outputs begin on 32-byte boundaries
 };
@@ -98,7 +97,7 @@ __device__ __forceinline__ int64_t page_of(const ReadParams& p, int t, int& slot
         const int page = p.table[seq * p.table_stride + pi];
         if (page >= 0 && page < p.pages) return page;
     }
-    atomicOr(&g_read_status, NVFP4_DEV_BAD_PAGE);
+    atomicOr(p.status, NVFP4_DEV_BAD_PAGE);
     return -1;
 }
 
@@ -164,13 +163,6 @@ __global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__
     for (int which = 0; which < 2; ++which) piece[which].store(scale[which], out[which], p.sectors);
 }
 
-cudaError_t read_status(int* bits) {
-    const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_read_status, sizeof(int));
-    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_read_status, &zero, sizeof(int));
-}
-const bool g_registered = register_status(read_status);
-
 }  // namespace
 }  // namespace nvfp4
 
@@ -210,6 +202,8 @@ extern "C" nvfp4_status nvfp4_cache_read(const nvfp4_cache_read_args* a, void* s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t ctas = ((wide ? 1 : 2) * p.pieces + 127) / 128;
     if (ctas > INT32_MAX) return NVFP4_ERR_UNSUPPORTED;
+    p.status = host_status_word();
+    if (!p.status) return NVFP4_ERR_CUDA;
     p.sectors = aligned(p.out[0], 32) && aligned(p.out[1], 32);
     const auto kernel = !wide ? cache_read_scalar_kernel : p.cache_type == NVFP4_E2M1 ? cache_read_kernel<NVFP4_E2M1>
                       : p.cache_type == NVFP4_E4M3 ? cache_read_kernel<NVFP4_E4M3> : cache_read_kernel<NVFP4_BF16>;

@@ -39,6 +39,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include <mutex>
 
@@ -4834,13 +4835,21 @@ void* ffn_static_scratch(int dev, cudaStream_t st) {
 
 // ------------------------------------------------------------------ host state shared with the other operators
 
-StatusReader g_status_reader[8];
-int g_status_readers = 0;
-
-bool register_status(StatusReader reader) {
-    if (g_status_readers == 8) std::abort();  // at load time: more translation units than slots
-    g_status_reader[g_status_readers++] = reader;
-    return true;
+int* host_status_word() {
+    static std::atomic<int*> at[64];  // by device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64) {
+        if (int* const word = at[dev].load(std::memory_order_relaxed)) return word;
+    }
+    void* a = nullptr;
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&a, g_device_status);
+    if (e != cudaSuccess) {
+        cuda_fail(e);
+        return nullptr;
+    }
+    if (dev < 64) at[dev].store(static_cast<int*>(a), std::memory_order_relaxed);
+    return static_cast<int*>(a);
 }
 
 bool host_pdl_enabled() { return g_pdl; }
@@ -5091,15 +5100,15 @@ nvfp4_status nvfp4_device_status(int32_t* flags_out, void* stream) {
     if (e != cudaSuccess) return cuda_fail(e);
     e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e);
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e);
-    for (int i = 0; i < g_status_readers; ++i) {
-        int bits = 0;
-        e = g_status_reader[i](&bits);
+    if (v) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e);
-        v |= bits;
     }
+    int bits = 0;
+    e = attention_status(&bits);
+    if (e != cudaSuccess) return cuda_fail(e);
+    v |= bits;
     *flags_out = v;
     return (v & NVFP4_DEV_TIMEOUT) ? NVFP4_ERR_TIMEOUT : NVFP4_OK;
 }

@@ -23,11 +23,12 @@ uint64_t host_wait_ns();                       // nvfp4_set_wait_budget_ns
 bool host_encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
-// Device status words of the operators' own translation units (device symbols are not shared
-// between units): each unit registers, when the library is loaded, a function that reads its word
-// and leaves zero. nvfp4_device_status calls them after synchronising its stream.
-using StatusReader = cudaError_t (*)(int* bits);
-bool register_status(StatusReader reader);
+// Where the current device's status word stands, which nvfp4_device_status reads; NULL on an error, which is recorded.
+// Device symbols are not shared between translation units, so the operators' kernels get it with their arguments: with a
+// word of each unit's own nvfp4_device_status waited for a copy of each, 77 us for six.
+int* host_status_word();
+// Reads and clears the word that paged_attention.cu has of its own (see status_word there).
+cudaError_t attention_status(int* bits);
 
 namespace ops {
 

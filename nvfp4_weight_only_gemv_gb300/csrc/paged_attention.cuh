@@ -54,6 +54,7 @@ struct AttnParams {
     int quad_log2;              // lanes (a power of two) that take a row's 4-value pieces
     uint64_t wait_ns;           // budget of a wait for a copy
     int q_vec;                  // q may be read 8 bytes at a time
+    int* status;                // see status_word
 };
 
 // The tile kernel's instance for a head size and number of query rows per kv head: the head is
@@ -71,13 +72,11 @@ nvfp4_status launch_tiles_scored(const TilePlan& t, const AttnParams& p, int gri
 
 }  // namespace attn
 
-// The kernels and their status word are each translation unit's own.
+// The kernels are each translation unit's own.
 namespace {
 
 using namespace ops;
 using namespace attn;
-
-__device__ int g_attention_status;
 
 struct TileParams : AttnParams {
     // k, v: [pages][kv heads][D / 64 pieces of 128 bytes][page][piece] (wide boxes) or
@@ -85,10 +84,13 @@ struct TileParams : AttnParams {
     CUtensorMap map[2];
 };
 
+// Where a unit's kernels report: its own word, or p.status.
+__device__ __forceinline__ int* status_word(const AttnParams& p);
+
 __device__ __forceinline__ int length_of(const AttnParams& p, int b) {
     const int n = p.lengths[b], most = p.max_pages * p.page;
     if (n < 0 || n > most) {
-        atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+        atomicOr(status_word(p), NVFP4_DEV_BAD_PAGE);
         return n < 0 ? 0 : most;
     }
     return n;
@@ -894,7 +896,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             bad = __ballot_sync(0xffffffffu, out);
             if (bad) {
                 if (out) {
-                    atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                    atomicOr(status_word(p), NVFP4_DEV_BAD_PAGE);
                     next_id[0] = 0;
                 }
                 if (p.tall_box) bad = (1u << H) - 1;
@@ -911,7 +913,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             id[i] = next_id[i];
             at[i] = next_at[i];
             if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(p.pages)) {
-                if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_BAD_PAGE);
+                if (lane == 0) atomicOr(status_word(p), NVFP4_DEV_BAD_PAGE);
                 id[i] = 0;
                 bad |= p.tall_box ? (1u << H) - 1 : 1u << i;
             }
@@ -1506,7 +1508,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         if (dead && !was_dead) {
             // the result is unspecified, but no copy may outlive the CTA: what was requested and has not
             // been waited for is K of this tile or of the one after the ring's, and all the ring's V
-            if (lane == 0) atomicOr(&g_attention_status, NVFP4_DEV_TIMEOUT);
+            if (lane == 0) atomicOr(status_word(p), NVFP4_DEV_TIMEOUT);
 #pragma unroll 1
             for (int st = 0; st < 2 * T::kStages; ++st) {
                 const int ahead = (st >> 1) + (st & 1 ? 0 : k_taken);  // tiles after this one
@@ -1579,13 +1581,6 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
         run = s_run;
     }
 }
-
-cudaError_t read_status(int* bits) {
-    const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_attention_status, sizeof(int));
-    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(int));
-}
-const bool g_registered = register_status(read_status);
 
 // Makes the copies' tensor maps.
 template <typename T>

@@ -19,8 +19,6 @@ namespace {
 
 using namespace ops;
 
-__device__ int g_append_status;
-
 struct AppendParams {
     const void* x[3];        // q, k, v
     int64_t ts[3], hs[3];    // token and head strides, elements
@@ -38,6 +36,7 @@ struct AppendParams {
     int T, hq, hk, D, half, seqs, per_seq, pages, max_pages, page;
     int norm_type, interleaved, cache_type;
     float mscale, eps, one_over_d;
+    int* status;             // see host_status_word
     int shares, lanes_log2;  // vector kernel: warps per token, lanes per head
 };
 
@@ -74,7 +73,7 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, int t, int n, Pl
             return true;
         }
     }
-    atomicOr(&g_append_status, NVFP4_DEV_BAD_PAGE);
+    atomicOr(p.status, NVFP4_DEV_BAD_PAGE);
     return false;
 }
 
@@ -474,13 +473,6 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_c
     }
 }
 
-cudaError_t read_status(int* bits) {
-    const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_append_status, sizeof(int));
-    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_append_status, &zero, sizeof(int));
-}
-const bool g_registered = register_status(read_status);
-
 }  // namespace
 }  // namespace nvfp4
 
@@ -522,6 +514,8 @@ extern "C" nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* a, void*
     p.pages = a->pages; p.max_pages = a->max_pages; p.page = a->page_size;
     p.norm_type = a->norm_type; p.interleaved = a->interleaved; p.cache_type = a->cache_type;
     p.mscale = a->mscale; p.eps = a->eps;
+    p.status = host_status_word();
+    if (!p.status) return NVFP4_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     p.one_over_d = 1.0f / static_cast<float>(p.D);
     // Whole vectors of V values on their boundaries, for V = 8, then 4; else a value per thread.
