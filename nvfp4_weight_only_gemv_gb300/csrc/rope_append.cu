@@ -226,12 +226,14 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
     return put_right(fminf(fmaxf(x * inv, -512.0f), 512.0f), x, s, inv);
 }
 
-// Scales of which 1 / scale might not be normal are taken times a power of two, with the values.
+// Scales of which 1 / scale might not be normal are taken times a power of two, with the values; by an infinite one what is
+// finite becomes zero.
 template <int V>
 __device__ __forceinline__ void lift_scale(float& scale, float (&a)[V], float (&b)[V]) {
     if (fabsf(scale) >= 0x1p-100f && fabsf(scale) <= 0x1p100f) return;
-    const float lift = fabsf(scale) < 1.0f ? 0x1p64f : 0x1p-64f;
-    scale *= lift;
+    const bool infinite = fabsf(scale) == INFINITY;
+    const float lift = fabsf(scale) < 1.0f ? 0x1p64f : infinite ? 0.0f : 0x1p-64f;
+    scale = infinite ? copysignf(1.0f, scale) : scale * lift;
 #pragma unroll
     for (int e = 0; e < V; ++e) { a[e] *= lift; b[e] *= lift; }
 }
