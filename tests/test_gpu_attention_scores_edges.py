@@ -76,3 +76,38 @@ def test_a_capped_score_has_the_bits_that_are_stated(variant, cache, cap):
         # of 2^-21 and is off by 2^-22 of a power of two, 0.7 of it in lse; with larger |m| by 2^-24 of |m| + 7
         err -= 0.7 * torch.clamp((z.abs() * 1.4427 + 7) * 2.0 ** -24, min=2.0 ** -22)
     assert bool((err <= 24 * 2.0 ** -24 * z.abs()).all()), float((err / z.abs()).max() * 2 ** 24)
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("cap", [2.0 ** -40, 8.0, 50.0, 100.0, 1000.0, 2.0 ** 40])
+@pytest.mark.parametrize("scale", [1e30, -1e30, 1e-30, -1e-30])
+def test_scores_beyond_the_cap_and_of_nothing(variant, cache, cap, scale):
+    # every third key is zero, the others are +-1.5 along the signs of the first head's query; the second head's is its
+    # opposite. So raw scores are 0 or +-1.5 sum|q| scale: their magnitude is beyond 2^40 or below 2^-80.
+    n, D, g = 41, 64, torch.Generator(device=DEV)
+    g.manual_seed(17)
+    q = torch.randn((1, 1, D), generator=g, device=DEV).to(BF16)
+    kind = torch.arange(n, device=DEV) % 3 - 1
+    k = (1.5 * kind[:, None].float() * torch.sign(q[0].float()))[:, None]
+    v = torch.randn((n, 1, D), generator=g, device=DEV).to(BF16).float()
+    kc, vc = nv.kv_cache(3, 1, 16, D, cache)
+    table, at = torch.arange(3, dtype=torch.int32, device=DEV)[None], torch.arange(n, dtype=torch.int32, device=DEV)
+    nv.rope_append(None, k, v, at, torch.empty(0, device=DEV), kc, vc, table)
+    k_held, v_held = (t[:, 0].double() for t in nv.cache_read(at, kc, vc, table))
+    assert torch.equal(k_held, k[:, 0].double())
+    lse = torch.empty((1, 2), device=DEV)
+    got = nv.paged_attention(torch.cat([q, -q], dim=1), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale,
+                             softcap=cap, lse=lse)
+    assert nv.device_status() == 0
+    s = torch.cat([q, -q], dim=1)[0].double() @ k_held.T * scale
+    z = cap * torch.tanh(s / cap)
+    # beyond the cap z is +-cap, as tanh is 1 there to 2^-22 (a short form's error, too, is 2^-22 of the cap); below it z
+    # is nothing. lse has roundings of its size and of the 2^7 that weights are raised by, 8 steps of 2^-24 of them.
+    far = float(z.abs().max()) if abs(scale) > 1 else 0.0
+    want = torch.logsumexp(z, dim=1)
+    off = 2.0 ** -21 * min(far, cap) + (2.0 ** -21 * cap if cache is FP4 and cap <= 64 else 0.0)
+    assert bool(((lse[0].double() - want).abs() <= off + 8 * 2.0 ** -24 * (want.abs() * 1.4427 + 8)).all()), (lse, want)
+    # weights: scores off by `off`, 11 bits; then the output's rounding
+    p = torch.softmax(z, dim=1)
+    tol = (p @ v_held.abs()) * (2 * off + 2.0 ** -11 + 2.0 ** -18) + (p @ v_held).abs() * 2.0 ** -8 + 2.0 ** -30
+    assert bool(((got[0].double() - p @ v_held).abs() <= tol).all())
