@@ -111,3 +111,28 @@ def test_scores_beyond_the_cap_and_of_nothing(variant, cache, cap, scale):
     p = torch.softmax(z, dim=1)
     tol = (p @ v_held.abs()) * (2 * off + 2.0 ** -11 + 2.0 ** -18) + (p @ v_held).abs() * 2.0 ** -8 + 2.0 ** -30
     assert bool(((got[0].double() - p @ v_held).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("cap,biased", [(50.0, False), (100.0, True), (1000.0, False)])
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_a_score_of_zero_by_a_factor_beyond_fp32(variant, cache, cap, biased, scale):
+    # in base-2 units the largest scales are beyond fp32's range; scores of zero stay zero, others reach the cap
+    n, D = 20, 64
+    q = torch.ones((1, 1, D), device=DEV, dtype=BF16)
+    k = torch.zeros((n, 1, D), device=DEV)
+    k[7] = math.copysign(1.5, -scale)  # a score of -cap, of weight exp(-cap)
+    v = torch.arange(n, device=DEV)[:, None, None].expand(-1, 1, D) % 4 * 0.5 + 1.5  # exact in every type
+    kc, vc = nv.kv_cache(2, 1, 16, D, cache)
+    table, at = torch.arange(2, dtype=torch.int32, device=DEV)[None], torch.arange(n, dtype=torch.int32, device=DEV)
+    nv.rope_append(None, k, v.contiguous(), at, torch.empty(0, device=DEV), kc, vc, table)
+    lse = torch.empty((1, 1), device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale, softcap=cap,
+                             slopes=torch.full((1,), 0.25, device=DEV) if biased else None, lse=lse)
+    z = torch.zeros(n, dtype=torch.float64, device=DEV)
+    z[7] = -cap
+    if biased:
+        z -= 0.25 * torch.arange(n - 1, -1, -1, device=DEV)
+    assert abs(float(lse) - float(torch.logsumexp(z, 0))) <= 2.0 ** -18  # 8 steps of 2^-24 of a lse below 4 and of 7
+    want = (torch.softmax(z, 0)[:, None] * v[:, 0].double()).sum(0)
+    assert bool(((got[0, 0].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -17)).all())
