@@ -4835,6 +4835,11 @@ void* ffn_static_scratch(int dev, cudaStream_t st) {
 
 // ------------------------------------------------------------------ host state shared with the other operators
 
+StatusReader g_attention_status = nullptr;
+bool set_attention_status(StatusReader reader) {
+    g_attention_status = reader;
+    return true;
+}
 int* host_status_word() {
     static std::atomic<int*> at[64];  // by device
     int dev = 0;
@@ -5106,7 +5111,7 @@ nvfp4_status nvfp4_device_status(int32_t* flags_out, void* stream) {
         if (e != cudaSuccess) return cuda_fail(e);
     }
     int bits = 0;
-    e = attention_status(&bits);
+    e = g_attention_status ? g_attention_status(&bits) : cudaSuccess;
     if (e != cudaSuccess) return cuda_fail(e);
     v |= bits;
     *flags_out = v;

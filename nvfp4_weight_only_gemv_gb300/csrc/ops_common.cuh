@@ -27,8 +27,10 @@ bool host_encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const
 // Device symbols are not shared between translation units, so the operators' kernels get it with their arguments: with a
 // word of each unit's own nvfp4_device_status waited for a copy of each, 77 us for six.
 int* host_status_word();
-// Reads and clears the word that paged_attention.cu has of its own (see status_word there).
-cudaError_t attention_status(int* bits);
+// Reads and clears the word that paged_attention.cu has of its own (see status_word there), which gives its function when the
+// library is loaded; NULL where nvfp4_gemv.cu is built alone.
+using StatusReader = cudaError_t (*)(int* bits);
+bool set_attention_status(StatusReader reader);
 
 namespace ops {
 

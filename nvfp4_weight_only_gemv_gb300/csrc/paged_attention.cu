@@ -8,8 +8,8 @@ namespace {
 
 // A word of this unit's own: by a pointer among their arguments the instances for E4M3, which are short of registers, took 1 to
 // 3 % longer (64 x 8191 keys, 16 rows: 174.9 us and 178.9).
-__device__ int g_attention_status;
-__device__ __forceinline__ int* status_word(const AttnParams&) { return &g_attention_status; }
+__device__ int g_plain_status;
+__device__ __forceinline__ int* status_word(const AttnParams&) { return &g_plain_status; }
 
 constexpr int kScalarWarps = 4;
 
@@ -150,14 +150,14 @@ bool sizes_ok(int seqs, int rows, int hq, int hk, int dim) {
     return seqs >= 0 && rows >= 0 && rows <= kMaxRows && hq >= 0 && hk >= 0 && dim >= 0 && (hk == 0 ? hq == 0 : hq % hk == 0);
 }
 
-}  // namespace
-
-cudaError_t attention_status(int* bits) {
+cudaError_t read_status(int* bits) {
     const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_attention_status, sizeof(int));
-    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(int));
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_plain_status, sizeof(int));
+    return e != cudaSuccess || *bits == 0 ? e : cudaMemcpyToSymbol(g_plain_status, &zero, sizeof(int));
 }
+const bool g_status_set = set_attention_status(read_status);
 
+}  // namespace
 }  // namespace nvfp4
 
 extern "C" int64_t nvfp4_attention_workspace_bytes(int seqs, int rows, int q_heads, int kv_heads, int head_dim) {
