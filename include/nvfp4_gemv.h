@@ -357,7 +357,8 @@ nvfp4_status nvfp4_rope_append(const nvfp4_rope_append_args* args, void* stream)
 /*
  * Reads rows of the cache back as bf16: for token t at position positions[t] of sequence seq_ids[t] (as
  * nvfp4_rope_append places it), k_out and v_out [tokens, kv_heads, head_dim] receive what the cache holds there:
- * the value, or code * scale, or code * block scale * scale, rounded once. For a program's own attention over a
+ * the value, or code * scale, or code * block scale * scale as an fp32 product, rounded to bf16 (without a scale the value is
+ * exact before that). For a program's own attention over a
  * prompt, which then sees the keys that later steps will see, and to move a cache. A negative position is padding
  * and gives zeros. A sequence, position or page outside its range sets NVFP4_DEV_BAD_PAGE and gives zeros. Strides,
  * limits and layouts as nvfp4_rope_append.

@@ -1,11 +1,12 @@
 // Rows of a paged cache read back as bf16.
 //
 // For token t at position n = positions[t]: out[t, h] = bf16(code * block scale * scale[h]) (E2M1),
-// bf16(code * scale[h]) (E4M3) or the value (bf16) of row n % page of page table[seq][n / page].
+// bf16(code * scale[h]) (E4M3) or the value (bf16) of row n % page of page table[seq][n / page]; code * block scale is exact,
+// its product with a head's scale fp32's.
 //
-// Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens. (4 bits,
-// 8192 tokens of 8 + 8 heads of 128 values: 10.0 us for 6.3 us of bytes, position, page and row being three trips one
-// after the other; one token 2.4 us.)
+// Each value is moved once; the kernel is bound by that traffic for prompts, by latency for single tokens. (8192 tokens of
+// 8 + 8 heads of 128 values, back to back in a graph: 9.6 us in 4 bits for 6.3 us of bytes, E4M3 10.2 for 7.4, bf16 12.6 for
+// 9.9, position, page and row being three trips one after the other; one token 2.0 us of any.)
 
 #include "ops_common.cuh"
 
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(128) cache_read_scalar_kernel(const __grid_con
 }
 
 // One thread takes 16 neighbouring values of a key and the same of its value. (4 bits, 8192 tokens of 8 + 8 heads of
-// 128 values, us: 10.0; with stores of 16 bytes 12.2; two or four such pairs a thread 12.3 and 13.5, 8 values 14.2.)
+// 128 values, us by single launches: 10.0; with stores of 16 bytes 12.2; two or four such pairs a thread 12.3 and 13.5, 8 values 14.2.)
 template <int C>
 __global__ void __launch_bounds__(128) cache_read_kernel(const __grid_constant__ ReadParams p) {
     pdl_launch_dependents();

@@ -180,7 +180,7 @@ struct TileShape {
     static constexpr int kQ = DP / 16;                     // operand pairs of a query row block per lane
     static constexpr int kWarps = DP >= 256 ? 8 : 4;
     static constexpr int kCtas = DP >= 256 ? 1 : NT * DP <= 128 ? kCtasPerSm : 2;  // per SM
-    static constexpr bool kQRegs = !kF4 && NT * DP <= 256;  // (kF4: read once for 64 keys: 114 us from shared memory, 119)
+    static constexpr bool kQRegs = !kF4 && NT * DP <= 256;  // (kF4: read once for 64 keys, 4 % faster from shared memory)
     static constexpr int kOStride = DP + 4;                // floats between rows of the merge buffer
     static constexpr int kBoxBytes = DP * kES >= 128 ? 128 : 64;       // of a key in a box
     static constexpr int kBoxes = DP * kES / kBoxBytes;    // boxes of a 16-key block
@@ -192,7 +192,9 @@ struct TileShape {
     static constexpr int kMerge = kWarps * 8 * NT * (kOStride * 4 + 8);
     static constexpr int kOwn = kRing > kMerge ? kRing : kMerge;   // the merge takes the ring's place
     // What 4 bits leave free lets a dozen parts of 15 rows join in one step (7 sequences up to 12001 keys: 27.1 us, 28.9 with
-    // two steps in the ring's place; one row a thread is read from L2 faster: 1 x 131071 keys 37.2 us, 37.7).
+    // two steps in the ring's place; one row a thread is read from L2 faster: 1 x 131071 keys 37.2 us, 37.7). Heads of 64 with
+    // 16 rows gain nothing from the 66 KB that three CTAs leave each (8 ragged, 3 rows: 17.8 us both), and 32 rows a warp, whose
+    // queries take 8 to 32 KB, would lose the second CTA (64 rows, 30 x 3000 keys: 113 us and 171).
     static constexpr int kMain = kF4 && NT == 2 && DP == 128 ? 100 * 1024 : kOwn;
 };
 
@@ -674,8 +676,8 @@ __device__ __noinline__ void finish_item(const AttnParams& p, JoinShared& sh, co
 }
 
 // DP, NT: see TileShape; C: the cache's type; S: scores with a cap or a bias (7 sequences up to 12001 keys of 4 bits, 15
-// rows: 29.7 us with both, 26.4 without); W: D is DP (4 bits: a lane's offsets in a record are then constants of its loads,
-// 119 us for 125).
+// rows: 29.9 us with both, 26.4 without); W: D is DP (4 bits: a lane's offsets in a record are then constants of its loads, 5 %
+// of a full batch's time).
 template <int C>
 using KernelParams = std::conditional_t<C == NVFP4_E2M1, AttnParams, TileParams>;
 
@@ -1348,6 +1350,9 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
                         l[nt][0] += e[2 * r];
                         l[nt][1] += e[2 * r + 1];
                         if constexpr (F16) {
+                            // 11 bits. A second f16 number for what they leave is not kept: the output's distance from 64 bits
+                            // is its own rounding either way (0.0017), and the product and its operands took 64 x 8191 keys of
+                            // 4 bits from 143 to 177 us with 16 rows, from 104.6 to 115 with four.
                             pb[i][nt][r] = transpose8x8(pack_f16(e[2 * r], e[2 * r + 1]));
                         } else {
                             const uint32_t word = pack_bf16_down(e[2 * r], e[2 * r + 1]);

@@ -262,9 +262,10 @@ __device__ __forceinline__ uint32_t block_codes(const float (&x)[V], float b) {
 }
 
 // F4: a cache of 4 bits. With V = 8 a lane's vectors are halves of two blocks, whose other halves its neighbours have, or, where
-// pairs are neighbours or do not turn, one block; with V = 4, quarters of any, whose largest values meet in shared memory. (8192 tokens of 32 + 8 + 8 heads: 47 us, 4.0 TB/s, as latency-bound as
-// the others: without the codes' arithmetic 44; a block's scale stored or not, quotients without clamps, 128 registers,
-// 80, cosines read from shared memory each time, rows prefetched into L2: 47, 47, 52, 58, 53, 51.)
+// pairs are neighbours or do not turn, one block; with V = 4, quarters of any, whose largest values meet in shared memory. (8192 tokens of 32 + 8 + 8 heads: 46.3 us, 3.8 TB/s, where bf16
+// takes 39.1 for more bytes: the codes' arithmetic is 2 to 3 us of that, the rest latency at the same 27 % of the warps, with more
+// state: 28 bytes of spills at 96 registers. A block's scale stored or not and quotients without clamps made no difference; 128 registers,
+// 80, cosines read from shared memory each time, rows prefetched into L2 took 52, 58, 53, 51.)
 template <typename XT, int V, bool F4>
 __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int kDepth = sizeof(XT) == 2 ? 2 : 1;   // heads requested ahead

@@ -199,7 +199,8 @@ def rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, seq_
 
 def cache_read(positions, k_cache, v_cache, page_table, seq_ids=None, *, k_scale=None, v_scale=None, k_out=None,
                v_out=None, stream=None):
-    """What the cache holds for the given tokens, as a pair (k, v) of bfloat16 [tokens, kv_heads, D].
+    """What the cache holds for the given tokens, as a pair (k, v) of bfloat16 [tokens, kv_heads, D]: fp32 products of code,
+    block scale and head scale, rounded.
 
     positions and seq_ids name tokens as in rope_append; k_scale and v_scale are the scales that it was given. A
     prompt's own attention over these rows sees the keys that every later step will see. Padding (a negative
