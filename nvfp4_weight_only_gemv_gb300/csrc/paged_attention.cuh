@@ -1031,7 +1031,7 @@ paged_attention_tile_kernel(const __grid_constant__ KernelParams<C> p) {
             }
 #pragma unroll
             for (int i = 0; i < T::kQ; ++i) raw[i] = make_uint2(raw[i].x ^ flip, raw[i].y ^ flip);
-            if constexpr (S) f = f > FLT_MAX ? FLT_MAX : f;  // a score of zero stays zero
+            f = f > FLT_MAX ? FLT_MAX : f;  // a score of zero stays zero
             return f < 1.1754943508e-38f ? 1.1754943508e-38f : f;
         };
         uint2 qf[T::kQRegs ? NT : 1][T::kQ];

@@ -136,3 +136,28 @@ def test_a_score_of_zero_by_a_factor_beyond_fp32(variant, cache, cap, biased, sc
     assert abs(float(lse) - float(torch.logsumexp(z, 0))) <= 2.0 ** -18  # 8 steps of 2^-24 of a lse below 4 and of 7
     want = (torch.softmax(z, 0)[:, None] * v[:, 0].double()).sum(0)
     assert bool(((got[0, 0].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -17)).all())
+
+
+@pytest.mark.parametrize("cache", [BF16, FP8, FP4])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_plain_scores_of_zero_by_a_factor_beyond_fp32(variant, cache, biased, scale):
+    # as above without a cap: the other key's score is beyond fp32 and its weight nothing
+    n, D = 20, 64
+    q = torch.ones((1, 1, D), device=DEV, dtype=BF16)
+    k = torch.zeros((n, 1, D), device=DEV)
+    k[7] = math.copysign(1.5, -scale)
+    v = (torch.arange(n, device=DEV)[:, None, None].expand(-1, 1, D) % 4 * 0.5 + 1.5).contiguous()
+    kc, vc = nv.kv_cache(2, 1, 16, D, cache)
+    table, at = torch.arange(2, dtype=torch.int32, device=DEV)[None], torch.arange(n, dtype=torch.int32, device=DEV)
+    nv.rope_append(None, k, v, at, torch.empty(0, device=DEV), kc, vc, table)
+    lse = torch.empty((1, 1), device=DEV)
+    got = nv.paged_attention(q, kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale,
+                             slopes=torch.full((1,), 0.25, device=DEV) if biased else None, lse=lse)
+    z = torch.zeros(n, dtype=torch.float64, device=DEV)
+    z[7] = -math.inf
+    if biased:
+        z -= 0.25 * torch.arange(n - 1, -1, -1, device=DEV)
+    assert abs(float(lse) - float(torch.logsumexp(z, 0))) <= 2.0 ** -18
+    want = (torch.softmax(z, 0)[:, None] * v[:, 0].double()).sum(0)
+    assert bool(((got[0, 0].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -17)).all())
